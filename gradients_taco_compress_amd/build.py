@@ -1,4 +1,4 @@
-"""Build libtaco.so in-tree with hipcc for gfx950.
+"""Build libtaco.so, libtaco_probe.so and libtaco_norm.so in-tree with hipcc for gfx950.
 
     python gradients_taco_compress_amd/build.py
     TACO_HIPCC_FLAGS="-DTACO_WAVES_PER_GROUP=8" python gradients_taco_compress_amd/build.py
@@ -34,6 +34,12 @@ LIB = os.path.join(PKG, "libtaco.so")
 #: The measurement kernels (not part of the operator), a library of their own.
 PROBE_SOURCE = os.path.join(CSRC, "taco_probe.hip")
 PROBE_LIB = os.path.join(PKG, "libtaco_probe.so")
+#: Layer norm and its 8-bit activation checkpoint, a library of their own: the
+#: C ABI, the row kernels (one unit per activation type) and the weight gradient.
+NORM_SOURCES = [os.path.join(CSRC, f) for f in
+                ("taco_norm_abi.hip", "taco_norm_bf16.hip", "taco_norm_f16.hip",
+                 "taco_norm_f32.hip", "taco_norm_weight_grad.hip")]
+NORM_LIB = os.path.join(PKG, "libtaco_norm.so")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -105,11 +111,36 @@ def build(verbose: bool = False, out: str | None = None) -> str:
     return lib
 
 
+def build_norm(verbose: bool = False) -> str:
+    """Compile NORM_SOURCES (in parallel) and link NORM_LIB; always
+    recompiles.  Returns NORM_LIB."""
+    from concurrent.futures import ThreadPoolExecutor
+    tag = f".tmp{os.getpid()}"
+    objs = [src + tag + ".o" for src in NORM_SOURCES]
+    try:
+        with ThreadPoolExecutor(max_workers=len(objs)) as pool:
+            jobs = [pool.submit(_run, [HIPCC, *FLAGS, "-I", os.path.join(ROOT, "include"),
+                                       "-c", src, "-o", obj], verbose)
+                    for src, obj in zip(NORM_SOURCES, objs)]
+            for j in jobs:
+                j.result()
+        _run([HIPCC, "--offload-arch=gfx950", "-shared", *objs, "-o", NORM_LIB + tag], verbose)
+        os.replace(NORM_LIB + tag, NORM_LIB)
+    finally:
+        for path in objs + [NORM_LIB + tag]:
+            if os.path.exists(path):
+                os.remove(path)
+    return NORM_LIB
+
+
 if __name__ == "__main__":
     import argparse
-    ap = argparse.ArgumentParser(description="Build libtaco (and libtaco_probe) for gfx950.")
+    ap = argparse.ArgumentParser(
+        description="Build libtaco (and libtaco_probe, libtaco_norm) for gfx950.")
     ap.add_argument("-q", action="store_true", help="quiet")
     ap.add_argument("--out", default=None,
                     help="build only the operator library, to this path")
     a = ap.parse_args()
     print(build(verbose=not a.q, out=a.out))
+    if not a.out:
+        print(build_norm(verbose=not a.q))
