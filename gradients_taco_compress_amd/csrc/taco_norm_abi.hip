@@ -258,11 +258,11 @@ taco_status taco_norm_weight_grad(const void *dy, int64_t lddy, const uint8_t *c
         st = accumulate ? TACO_OK : fill_zero(dw, out_features * hidden, dw_dtype, stream);
         return st != TACO_OK || !dbias ? st : fill_zero(dbias, out_features, TACO_NORM_F32, stream);
     }
-    if (!dy || !codes || !workspace) return TACO_ERR_NULL;
-    if (!aligned(dy, 2) || !aligned(weight, p) || !aligned(bias, p) || !aligned(dw, d) ||
-        !aligned(dbias, 4) || !aligned(workspace, 16))
-        return TACO_ERR_ALIGN;
     const int64_t need = weight_grad_workspace(rows, out_features, hidden);
+    if (!dy || !codes || (need && !workspace)) return TACO_ERR_NULL;
+    if (!aligned(dy, 2) || !aligned(weight, p) || !aligned(bias, p) || !aligned(dw, d) ||
+        !aligned(dbias, 4) || (need && !aligned(workspace, 16)))
+        return TACO_ERR_ALIGN;
     const Span outs[] = {dw_span, db_span, {workspace, need}};
     const Span ins[] = {rows_span(dy, rows, out_features, lddy, 2), {codes, rows * hidden}, w_span,
                         b_span};

@@ -15,9 +15,17 @@
 //    all start on one bank: the 32-byte (dY) or 16-byte (codes) units of row
 //    t are stored at unit index XOR f(t), with f such that the rows a half
 //    wave reads together fall on different banks.
-//  * Global loads go straight to LDS (16 bytes per lane, no registers) where
-//    rows start on 16-byte boundaries; other rows, and the last rows of a
+//  * Global loads go straight to LDS (16 bytes per lane, no registers) into
+//    three tiles in turn, so a tile's loads have two tiles' time to arrive.
+//    The next half tile's fragments are read while the current one is
+//    multiplied, and the one barrier per tile sits where both the finished
+//    tile's last fragments and the next tile's data are already there.
+//    Rows that do not start on 16-byte boundaries, and the last rows of a
 //    tensor, pass through registers with every element checked.
+//  * db, the column sums of dY, comes from the same fragments (dot products
+//    with ones), so dY is read by one kernel only.
+//  * Tiles beyond a whole number per CU are split along t and their partial
+//    sums joined, in order, by a second kernel.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -50,6 +58,10 @@ struct Mfma<__bf16> {
     static __device__ __forceinline__ v2 codes(uint32_t w) {
         return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI);
     }
+    // c + a[0] + a[1]
+    static __device__ __forceinline__ float add2(v2 a, float c) {
+        return __builtin_amdgcn_fdot2_f32_bf16(a, (v2){1.0f, 1.0f}, c, false);
+    }
 };
 template <>
 struct Mfma<_Float16> {
@@ -61,6 +73,9 @@ struct Mfma<_Float16> {
     template <bool HI>
     static __device__ __forceinline__ v2 codes(uint32_t w) {
         return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI);
+    }
+    static __device__ __forceinline__ float add2(v2 a, float c) {
+        return __builtin_amdgcn_fdot2(a, (v2){1.0f, 1.0f}, c, false);
     }
 };
 
@@ -76,50 +91,173 @@ __device__ __forceinline__ int turn_codes(int t) {
     return BK == 256 ? (t & 15) : ((t >> 1) & 7);
 }
 
-template <typename E>
-__device__ __forceinline__ float param(const void *p, int f32, int col, float missing) {
-    if (!p) return missing;
-    return f32 ? static_cast<const float *>(p)[col] : (float)static_cast<const E *>(p)[col];
+// 16 bytes at p, of which the first n (1..16) belong to a row that starts at
+// `row`: the others are zero, and nothing outside the row is read.
+__device__ __forceinline__ u4v load_tail(const char *p, const char *row, int n) {
+    if (n >= 16) return *reinterpret_cast<const u4v_any *>(p);
+    if (p + n - row >= 16) {
+        // The row's last 16 bytes, moved down.
+        const u4v v = *reinterpret_cast<const u4v_any *>(p + n - 16);
+        const uint64_t lo = ((uint64_t)v.y << 32) | v.x, hi = ((uint64_t)v.w << 32) | v.z;
+        const int sh = 8 * (16 - n);
+        const uint64_t a = sh >= 64 ? hi >> (sh - 64) : (lo >> sh) | (hi << (64 - sh));
+        const uint64_t b = sh >= 64 ? 0 : hi >> sh;
+        return (u4v){(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)};
+    }
+    u4v v = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const uint32_t c = (uint8_t)p[j < n ? j : n - 1];
+        v[j >> 2] |= (j < n ? c : 0u) << (8 * (j & 3));
+    }
+    return v;
 }
 
-// One output element from its raw sum: (w_k / S) sum + b_k db_n.
+// Which output tile and which rows a work-group takes.  The first `whole`
+// work-groups take a tile each; the others share the remaining tiles, `split`
+// to a tile.
+struct Schedule {
+    int32_t tiles_n, tiles_k;
+    int32_t whole, split;
+    int64_t slice;             // rows of a split, a multiple of kDepth
+};
+
+struct Tile { int n, k; };
+
+// Tile number t of an order in which neighbours share operands: strips of
+// four tile rows, each walked column by column.
+__device__ __forceinline__ Tile tile_at(const Schedule &s, int t) {
+    constexpr int kStrip = 4;
+    const int strip = t / (kStrip * s.tiles_k), in = t - strip * kStrip * s.tiles_k;
+    const int left = s.tiles_n - strip * kStrip, rows = left < kStrip ? left : kStrip;
+    return {strip * kStrip + in % rows, in / rows};
+}
+
+// The finished gradient of four neighbours of a row: (w_k / S) sum + b_k db_n.
 template <typename E>
-__device__ __forceinline__ void finish(const WeightGrad &a, const float *db, int n, int k,
-                                       float sum) {
-    float v = sum * (param<E>(a.weight, a.params_f32, k, 1.0f) * a.inv_scale);
-    if (a.bias) v = __builtin_fmaf(param<E>(a.bias, a.params_f32, k, 0.0f), db[n], v);
-    const int64_t at = (int64_t)n * a.hidden + k;
-    if (a.dw_f32) {
-        float *p = static_cast<float *>(a.dw) + at;
-        *p = a.accumulate ? *p + v : v;
-    } else {
-        static_cast<E *>(a.dw)[at] = (E)v;
+struct Finish {
+    const WeightGrad &a;
+    bool whole;                // rows of dW keep four neighbours aligned
+    __device__ __forceinline__ Finish(const WeightGrad &args)
+        : a(args),
+          whole(args.hidden % 4 == 0 &&
+                (reinterpret_cast<uintptr_t>(args.dw) & (args.dw_f32 ? 15u : 7u)) == 0) {}
+    __device__ __forceinline__ f4v param4(const void *p, int k, float missing) const {
+        f4v v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int at = k + e < a.hidden ? k + e : a.hidden - 1;
+            v[e] = !p ? missing
+                      : a.params_f32 ? static_cast<const float *>(p)[at]
+                                     : (float)static_cast<const E *>(p)[at];
+        }
+        return v;
+    }
+    __device__ __forceinline__ f4v scale(int k) const {
+        return param4(a.weight, k, 1.0f) * a.inv_scale;
+    }
+    __device__ __forceinline__ f4v bias(int k) const { return param4(a.bias, k, 0.0f); }
+    __device__ __forceinline__ void store(int n, int k, f4v sum, f4v sc, f4v b, float db) const {
+        f4v v = sum * sc;
+        if (a.bias) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(b[e], db, v[e]);
+        }
+        const int64_t at = (int64_t)n * a.hidden + k;
+        typedef E e4v __attribute__((ext_vector_type(4)));
+        if (whole && k + 4 <= a.hidden) {
+            if (a.dw_f32) {
+                f4v *p = reinterpret_cast<f4v *>(static_cast<float *>(a.dw) + at);
+                *p = a.accumulate ? *p + v : v;
+            } else {
+                *reinterpret_cast<e4v *>(static_cast<E *>(a.dw) + at) =
+                    __builtin_convertvector(v, e4v);
+            }
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (k + e >= a.hidden) break;
+            if (a.dw_f32) {
+                float *p = static_cast<float *>(a.dw) + at + e;
+                *p = a.accumulate ? *p + v[e] : v[e];
+            } else {
+                static_cast<E *>(a.dw)[at + e] = (E)v[e];
+            }
+        }
+    }
+};
+
+// Shape of a work-group's tile: BN x BK outputs by WN x WK waves.
+template <int BN_, int BK_, int WN_, int WK_>
+struct Shape {
+    static constexpr int BN = BN_, BK = BK_, WN = WN_, WK = WK_;
+    static constexpr int THREADS = WN * WK * kWave;
+    static constexpr int NI = BN / WN / 16, KI = BK / WK / 16;    // fragments of a wave
+    // A split's partial sums: every thread's, then the columns' sums.
+    static constexpr int SLAB = BN * BK + BN;
+};
+
+// Lane (g, r) = (lane / 16, lane % 16) of wave (wn, wk) holds, in fragment
+// (j, i), output row n = r and columns k = 4 g + (0..3) of that fragment.
+template <typename S>
+struct Place {
+    int g, r, wn, wk;
+    __device__ __forceinline__ explicit Place(int tid)
+        : g((tid >> 4) & 3), r(tid & 15),
+          wn(__builtin_amdgcn_readfirstlane(tid / kWave) % S::WN),
+          wk(__builtin_amdgcn_readfirstlane(tid / kWave) / S::WN) {}
+    __device__ __forceinline__ int n(int i) const { return (wn * S::NI + i) * 16 + r; }
+    __device__ __forceinline__ int k(int j) const { return (wk * S::KI + j) * 16 + 4 * g; }
+};
+
+// Order of the instructions of one half tile: for each code fragment its
+// conversion, its products, and two LDS reads of the next half.
+template <int KI, int NI>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+    for (int j = 0; j < KI; ++j) {
+        __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);        // VALU
+        __builtin_amdgcn_sched_group_barrier(0x008, NI, 0);       // MFMA
+        __builtin_amdgcn_sched_group_barrier(0x100, (2 * NI + KI + KI - 1) / KI, 0);   // LDS reads
     }
 }
 
-// Output tile (n0.., k0..) of BN x BK over rows [t0, t1): WN x WK waves, each
-// BN / WN by BK / WK.  parts != null: raw sums go there (one [N][K] slab per
-// blockIdx.y) instead of the finished gradient.
-template <typename E, int BN, int BK, int WN, int WK, bool DIRECT>
-__global__ __launch_bounds__(WN *WK *kWave) void grad_kernel(WeightGrad a, const float *db,
-                                                             float *parts, int64_t slice) {
-    constexpr int THREADS = WN * WK * kWave;
-    constexpr int NI = BN / WN / 16, KI = BK / WK / 16;      // fragments of a wave
+template <typename E, typename S, bool DIRECT>
+__global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule plan,
+                                                          float *slabs) {
+    constexpr int BN = S::BN, BK = S::BK, NI = S::NI, KI = S::KI, THREADS = S::THREADS;
     constexpr int DY_BYTES = kDepth * BN * 2, CODE_BYTES = kDepth * BK;
     constexpr int DY_LOADS = DY_BYTES / 16 / THREADS, CODE_LOADS = CODE_BYTES / 16 / THREADS;
-    constexpr int DY_CHUNKS = BN / 8, CODE_CHUNKS = BK / 16;  // 16-byte chunks of a row
+    constexpr int LOADS = DY_LOADS + CODE_LOADS;
+    constexpr int DY_CHUNKS = BN / 8, CODE_CHUNKS = BK / 16;      // 16-byte chunks of a row
     using M = Mfma<E>;
-    __shared__ __align__(1024) uint8_t lds[2][DY_BYTES + CODE_BYTES];
+    // Three variables, not one: the compiler then knows that a load into one
+    // tile does not touch the fragments being read from another.
+    __shared__ __align__(1024) uint8_t lds0[DY_BYTES + CODE_BYTES];
+    __shared__ __align__(1024) uint8_t lds1[DY_BYTES + CODE_BYTES];
+    __shared__ __align__(1024) uint8_t lds2[DY_BYTES + CODE_BYTES];
 
     const int tid = threadIdx.x;
-    const int lane = tid & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int tiles_n = (a.out_features + BN - 1) / BN;
-    const int tile_n = blockIdx.x % tiles_n, tile_k = blockIdx.x / tiles_n;
-    const int n0 = tile_n * BN, k0 = tile_k * BK;
-    const int64_t t0 = (int64_t)blockIdx.y * slice;
-    const int64_t t1 = t0 + slice < a.rows ? t0 + slice : a.rows;
-    const int steps = (int)((t1 - t0 + kDepth - 1) / kDepth);
+    [[maybe_unused]] const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const Place<S> place(tid);
+
+    // Consecutive work-groups go to the 8 XCDs in turn; each XCD gets a
+    // contiguous range of the whole tiles, whose operands meet in its L2.
+    int t_index, part = -1;
+    int64_t t0 = 0, t1 = a.rows;
+    if ((int)blockIdx.x < plan.whole) {
+        const int xcd = blockIdx.x % 8, q = plan.whole / 8, rem = plan.whole % 8;
+        t_index = xcd * q + (xcd < rem ? xcd : rem) + blockIdx.x / 8;
+    } else {
+        part = blockIdx.x - plan.whole;
+        t_index = plan.whole + part / plan.split;
+        t0 = (int64_t)(part % plan.split) * plan.slice;
+        t1 = t0 + plan.slice < a.rows ? t0 + plan.slice : a.rows;
+        if (t0 > t1) t0 = t1;
+    }
+    const Tile tile = tile_at(plan, t_index);
+    const int n0 = tile.n * BN, k0 = tile.k * BK;
     const char *const dy = static_cast<const char *>(a.dy);
     const char *const codes = reinterpret_cast<const char *>(a.codes);
 
@@ -136,327 +274,345 @@ __global__ __launch_bounds__(WN *WK *kWave) void grad_kernel(WeightGrad a, const
     };
 
     // Straight to LDS: every row exists; a chunk past the last column reads
-    // the tile's first one instead (its sums are never stored).
-    auto load_direct = [&](int step, int buf) {
-        const int64_t t = t0 + (int64_t)step * kDepth;
+    // the tile's first one instead (its sums are never stored).  Offsets from
+    // the tile's first element fit 32 bits (the launcher sees to it).
+    uint32_t dy_off[DY_LOADS], code_off[CODE_LOADS];
+    if constexpr (DIRECT) {
 #pragma unroll
         for (int i = 0; i < DY_LOADS; ++i) {
-            int col = n0 + dy_col(i);
-            col = col < a.out_features ? col : n0;
-            const char *p = dy + ((t + dy_row(i)) * a.lddy + col) * 2;
-            __builtin_amdgcn_global_load_lds(
-                (const __attribute__((address_space(1))) void *)p,
-                (__attribute__((address_space(3))) void *)(lds[buf] +
-                                                           (i * THREADS + wave * kWave) * 16),
-                16, 0, 0);
+            const int col = dy_col(i);
+            dy_off[i] = (uint32_t)(dy_row(i) * (int)a.lddy + (n0 + col < a.out_features ? col : 0)) * 2u;
         }
 #pragma unroll
         for (int i = 0; i < CODE_LOADS; ++i) {
-            int col = k0 + code_col(i);
-            col = col < a.hidden ? col : k0;
-            const char *p = codes + (t + code_row(i)) * a.hidden + col;
-            __builtin_amdgcn_global_load_lds(
-                (const __attribute__((address_space(1))) void *)p,
-                (__attribute__((address_space(3))) void *)(lds[buf] + DY_BYTES +
-                                                           (i * THREADS + wave * kWave) * 16),
-                16, 0, 0);
+            const int col = code_col(i);
+            code_off[i] = (uint32_t)(code_row(i) * a.hidden + (k0 + col < a.hidden ? col : 0));
         }
+    }
+    auto load_direct = [&](int64_t t, uint8_t *buf) {
+#if defined(__HIP_DEVICE_COMPILE__)      // the host pass does not know the resource type
+        // 0x00020000: raw 32-bit data; every offset is inside the operand.
+        const auto rd = __builtin_amdgcn_make_buffer_rsrc(
+            (void *)(dy + (t * a.lddy + n0) * 2), 0, 0x7FFFFFFF, 0x00020000);
+        const auto rc = __builtin_amdgcn_make_buffer_rsrc(
+            (void *)(codes + t * a.hidden + k0), 0, 0x7FFFFFFF, 0x00020000);
+#pragma unroll
+        for (int i = 0; i < DY_LOADS; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rd,
+                (__attribute__((address_space(3))) void *)(buf + (i * THREADS + wave * kWave) * 16),
+                16, dy_off[i], 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < CODE_LOADS; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rc,
+                (__attribute__((address_space(3))) void *)(buf + DY_BYTES +
+                                                           (i * THREADS + wave * kWave) * 16),
+                16, code_off[i], 0, 0, 0);
+#endif
     };
     // Through registers: rows past t1 and columns past the last are zero.
     u4v held_dy[DY_LOADS], held_codes[CODE_LOADS];
-    auto load_held = [&](int step) {
-        const int64_t t = t0 + (int64_t)step * kDepth;
+    auto load_held = [&](int64_t t) {
 #pragma unroll
         for (int i = 0; i < DY_LOADS; ++i) {
             const int col = n0 + dy_col(i);
-            const char *p = dy + ((t + dy_row(i)) * a.lddy + col) * 2;
             const int n = t + dy_row(i) < t1 ? a.out_features - col : 0;
             held_dy[i] = (u4v){0u, 0u, 0u, 0u};
-            if (n >= 8) {
-                held_dy[i] = *reinterpret_cast<const u4v_any *>(p);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (j < n)
-                        held_dy[i][j >> 1] |= (uint32_t) reinterpret_cast<const uint16_t *>(p)[j]
-                                              << (16 * (j & 1));
+            if (n > 0) {
+                const char *row = dy + (t + dy_row(i)) * a.lddy * 2;
+                held_dy[i] = load_tail(row + col * 2, row, n < 8 ? 2 * n : 16);
             }
         }
 #pragma unroll
         for (int i = 0; i < CODE_LOADS; ++i) {
             const int col = k0 + code_col(i);
-            const char *p = codes + (t + code_row(i)) * a.hidden + col;
             const int n = t + code_row(i) < t1 ? a.hidden - col : 0;
             held_codes[i] = (u4v){0u, 0u, 0u, 0u};
-            if (n >= 16) {
-                held_codes[i] = *reinterpret_cast<const u4v_any *>(p);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (j < n)
-                        held_codes[i][j >> 2] |= (uint32_t)(uint8_t)p[j] << (8 * (j & 3));
+            if (n > 0) {
+                const char *row = codes + (t + code_row(i)) * a.hidden;
+                held_codes[i] = load_tail(row + col, row, n < 16 ? n : 16);
             }
         }
     };
-    auto store_held = [&](int buf) {
+    auto store_held = [&](uint8_t *buf) {
 #pragma unroll
         for (int i = 0; i < DY_LOADS; ++i)
-            *reinterpret_cast<u4v *>(lds[buf] + (i * THREADS + tid) * 16) = held_dy[i];
+            *reinterpret_cast<u4v *>(buf + (i * THREADS + tid) * 16) = held_dy[i];
 #pragma unroll
         for (int i = 0; i < CODE_LOADS; ++i)
-            *reinterpret_cast<u4v *>(lds[buf] + DY_BYTES + (i * THREADS + tid) * 16) =
-                held_codes[i];
-    };
-    auto is_direct = [&](int step) {
-        return DIRECT && t0 + (int64_t)(step + 1) * kDepth <= t1;
+            *reinterpret_cast<u4v *>(buf + DY_BYTES + (i * THREADS + tid) * 16) = held_codes[i];
     };
 
-    // Fragment addresses: lane (g, r) = (lane / 16, lane % 16) reads 8 bytes
-    // of row 8 g + r / 4 (dY; then + 4) or 8 g + r / 2 (codes); the read
-    // hands lane (g, r) column r of those rows.
-    const int g = lane >> 4, r = lane & 15;
-    const int wn = wave / WK, wk = wave % WK;
-    int dy_at[NI], code_at[KI];
+    // Fragment addresses: lane (g, r) reads 8 bytes of row 8 g + r / 4 (dY;
+    // then + 4) or 8 g + r / 2 (codes); the read hands it column r of them.
+    // A wave's units differ in their low bits only, so fragment i's unit is
+    // the first one's XOR i.
+    static_assert((NI & (NI - 1)) == 0 && (KI & (KI - 1)) == 0, "units of a wave");
+    int dy_at, code_at;
     {
-        const int t = 8 * g + (r >> 2);
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-            dy_at[i] = t * BN * 2 + (((wn * NI + i) ^ turn_dy<BN>(t)) * 32) + (r & 3) * 8;
+        const int t = 8 * place.g + (place.r >> 2);
+        dy_at = t * BN * 2 + (((place.wn * NI) ^ turn_dy<BN>(t)) * 32) + (place.r & 3) * 8;
     }
     {
-        const int t = 8 * g + (r >> 1);
+        const int t = 8 * place.g + (place.r >> 1);
+        code_at = DY_BYTES + t * BK + (((place.wk * KI) ^ turn_codes<BK>(t)) * 16) +
+                  (place.r & 1) * 8;
+    }
+
+    struct Fragments {
+        typename M::v8 dy[NI];
+        i2v codes[KI];
+    };
+    auto read = [&](uint8_t *buf, int half, Fragments &f) {
+        // Opaque here, so that the addresses are formed again for each tile:
+        // kept, those of three tiles would not fit the registers.
+        int d = dy_at, c = code_at;
+        asm volatile("" : "+v"(d), "+v"(c));
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            uint8_t *p = buf + (d ^ (i * 32)) + half * 32 * BN * 2;
+            union { s4v s[2]; typename M::v8 v; } u;
+            u.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s4v *)p);
+            u.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s4v *)(p + 4 * BN * 2));
+            f.dy[i] = u.v;
+        }
 #pragma unroll
         for (int j = 0; j < KI; ++j)
-            code_at[j] = DY_BYTES + t * BK + (((wk * KI + j) ^ turn_codes<BK>(t)) * 16) +
-                         (r & 1) * 8;
-    }
+            f.codes[j] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                (__attribute__((address_space(3))) i2v *)(buf + (c ^ (j * 16)) + half * 32 * BK));
+    };
 
     f4v sum[KI][NI];
+    float db[NI];
 #pragma unroll
-    for (int j = 0; j < KI; ++j)
+    for (int i = 0; i < NI; ++i) {
+        db[i] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) sum[j][i] = (f4v){0.0f, 0.0f, 0.0f, 0.0f};
-
-    auto multiply = [&](int buf) {
-        uint8_t *const tile = lds[buf];
+        for (int j = 0; j < KI; ++j) sum[j][i] = (f4v){0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    auto multiply = [&](const Fragments &f) {
 #pragma unroll
-        for (int half = 0; half < kDepth / 32; ++half) {
-            typename M::v8 fd[NI];
+        for (int j = 0; j < KI; ++j) {
+            union { typename M::v2 h[4]; typename M::v8 v; } u;
+            u.h[0] = M::template codes<false>((uint32_t)f.codes[j][0]);
+            u.h[1] = M::template codes<true>((uint32_t)f.codes[j][0]);
+            u.h[2] = M::template codes<false>((uint32_t)f.codes[j][1]);
+            u.h[3] = M::template codes<true>((uint32_t)f.codes[j][1]);
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                uint8_t *p = tile + dy_at[i] + half * 32 * BN * 2;
-                union { s4v s[2]; typename M::v8 v; } u;
-                u.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s4v *)p);
-                u.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s4v *)(p + 4 * BN * 2));
-                fd[i] = u.v;
-            }
+            for (int i = 0; i < NI; ++i) sum[j][i] = M::run(u.v, f.dy[i], sum[j][i]);
+        }
 #pragma unroll
-            for (int j = 0; j < KI; ++j) {
-                uint8_t *p = tile + code_at[j] + half * 32 * BK;
-                const i2v c = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                    (__attribute__((address_space(3))) i2v *)p);
-                union { typename M::v2 h[4]; typename M::v8 v; } u;
-                u.h[0] = M::template codes<false>((uint32_t)c[0]);
-                u.h[1] = M::template codes<true>((uint32_t)c[0]);
-                u.h[2] = M::template codes<false>((uint32_t)c[1]);
-                u.h[3] = M::template codes<true>((uint32_t)c[1]);
+        for (int i = 0; i < NI; ++i) {
+            union { typename M::v8 v; typename M::v2 h[4]; } u;
+            u.v = f.dy[i];
 #pragma unroll
-                for (int i = 0; i < NI; ++i) sum[j][i] = M::run(u.v, fd[i], sum[j][i]);
-            }
+            for (int e = 0; e < 4; ++e) db[i] = M::add2(u.h[e], db[i]);
         }
     };
 
-    if (is_direct(0)) {
-        load_direct(0, 0);
-    } else {
-        load_held(0);
-        store_held(0);
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    for (int step = 0; step < steps; ++step) {
-        const int buf = step & 1;
-        const bool more = step + 1 < steps;
-        if (more) {
-            if (is_direct(step + 1)) load_direct(step + 1, buf ^ 1);
-            else load_held(step + 1);
+    Fragments fa, fb;
+    const int full = DIRECT ? (int)((t1 - t0) / kDepth) : 0;
+    if (DIRECT && full > 0) {
+        // Past the last full tile the loads fetch that tile again, into LDS that
+        // is not read any more: every step issues the same number of loads.
+        auto load = [&](int s, uint8_t *buf) {
+            load_direct(t0 + (int64_t)(s < full ? s : full - 1) * kDepth, buf);
+        };
+        load(0, lds0);
+        load(1, lds1);
+        load(2, lds2);
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(2 * LOADS) : "memory");
+        read(lds0, 0, fa);
+        // Tile s in `cur`: its first half's fragments are in fa (or arriving).
+        auto step = [&](int s, uint8_t *cur, uint8_t *next) {
+            read(cur, 1, fb);
+            multiply(fa);
+            interleave<KI, NI>();
+            __builtin_amdgcn_sched_barrier(0);
+            // This wave has read all of cur, and its part of the next tile is
+            // there (the one after may be on its way); then so for all waves.
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LOADS) : "memory");
+            load(s + 3, cur);
+            read(next, 0, fa);
+            multiply(fb);
+            interleave<KI, NI>();
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        int s = 0;
+        for (; s + 3 <= full; s += 3) {
+            step(s, lds0, lds1);
+            step(s + 1, lds1, lds2);
+            step(s + 2, lds2, lds0);
         }
-        multiply(buf);
-        if (more && !is_direct(step + 1)) store_held(buf ^ 1);
-        // The next tile is in LDS, and this one has been read by all.
+        if (s < full) step(s, lds0, lds1);
+        if (s + 1 < full) step(s + 1, lds1, lds2);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    // What is not read directly: the last rows, or all of them.
+    int64_t t = t0 + (int64_t)full * kDepth;
+    if (t < t1) {
+        load_held(t);
+        __syncthreads();                    // every earlier fragment has been read
+        store_held(lds0);
         __syncthreads();
+        for (uint8_t *cur = lds0, *next = lds1; t < t1; t += kDepth) {
+            const bool more = t + kDepth < t1;
+            if (more) load_held(t + kDepth);
+            read(cur, 0, fa);
+            read(cur, 1, fb);
+            multiply(fa);
+            multiply(fb);
+            if (more) store_held(next);
+            __syncthreads();
+            uint8_t *const swap = cur;
+            cur = next;
+            next = swap;
+        }
     }
 
-    // Lane (g, r) of a fragment's sums: column n = r, rows k = 4 g + (0..3).
+    // Column sums: a lane holds those of its rows' group g.
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-        const int n = n0 + (wn * NI + i) * 16 + r;
-        if (n >= a.out_features) continue;
+        db[i] += __shfl_xor(db[i], 16);
+        db[i] += __shfl_xor(db[i], 32);
+    }
+    if (part >= 0) {
+        float *const slab = slabs + (int64_t)part * S::SLAB;
 #pragma unroll
-        for (int j = 0; j < KI; ++j) {
-            const int k = k0 + (wk * KI + j) * 16 + 4 * g;
+        for (int j = 0; j < KI; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (k + e >= a.hidden) break;
-                if (parts)
-                    parts[((int64_t)blockIdx.y * a.out_features + n) * a.hidden + k + e] =
-                        sum[j][i][e];
-                else
-                    finish<E>(a, db, n, k + e, sum[j][i][e]);
-            }
+            for (int i = 0; i < NI; ++i)
+                *reinterpret_cast<f4v *>(slab + ((j * NI + i) * THREADS + tid) * 4) = sum[j][i];
+        if (place.wk == 0 && place.g == 0) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) slab[BN * BK + place.n(i)] = db[i];
+        }
+        return;
+    }
+    const Finish<E> finish(a);
+    if (a.dbias && tile.k == 0 && place.wk == 0 && place.g == 0) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            if (n0 + place.n(i) < a.out_features) a.dbias[n0 + place.n(i)] = db[i];
+    }
+#pragma unroll
+    for (int j = 0; j < KI; ++j) {
+        const int k = k0 + place.k(j);
+        if (k >= a.hidden) continue;
+        const f4v sc = finish.scale(k), b = finish.bias(k);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int n = n0 + place.n(i);
+            if (n < a.out_features) finish.store(n, k, sum[j][i], sc, b, db[i]);
         }
     }
 }
 
-// Adds the slabs of a split sum in order and finishes.
-template <typename E>
-__global__ __launch_bounds__(256) void join_kernel(WeightGrad a, const float *db,
-                                                   const float *parts, int splits) {
-    const int64_t count = (int64_t)a.out_features * a.hidden;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count;
-         i += (int64_t)gridDim.x * 256) {
-        float s = 0.0f;
-        for (int p = 0; p < splits; ++p) s += parts[p * count + i];
-        finish<E>(a, db, (int)(i / a.hidden), (int)(i % a.hidden), s);
+// Adds the parts of a split tile in order and finishes it: blockIdx.x is the
+// tile after the whole ones, blockIdx.y its fragment.
+template <typename E, typename S>
+__global__ __launch_bounds__(S::THREADS) void join_kernel(WeightGrad a, Schedule plan,
+                                                          const float *slabs) {
+    const int j = blockIdx.y / S::NI, i = blockIdx.y % S::NI;
+    const Place<S> place(threadIdx.x);
+    const Tile tile = tile_at(plan, plan.whole + blockIdx.x);
+    const int n = tile.n * S::BN + place.n(i), k = tile.k * S::BK + place.k(j);
+    if (n >= a.out_features || k >= a.hidden) return;
+    const float *p = slabs + (int64_t)blockIdx.x * plan.split * S::SLAB;
+    f4v sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    float db = 0.0f;
+    for (int s = 0; s < plan.split; ++s, p += S::SLAB) {
+        sum += *reinterpret_cast<const f4v *>(p + (blockIdx.y * S::THREADS + threadIdx.x) * 4);
+        db += p[S::BN * S::BK + place.n(i)];
     }
-}
-
-// Column sums of dY, first over the rows of a work-group (8 row lanes, 32
-// lanes of 8 columns), then over the work-groups.
-template <typename E>
-__global__ __launch_bounds__(256) void column_parts_kernel(const E *dy, int64_t ld, int64_t rows,
-                                                           int n, float *parts) {
-    __shared__ float lds[8][256];
-    const int c = threadIdx.x & 31, lane = threadIdx.x / 32;
-    const int col = blockIdx.x * 256 + 8 * c;
-    float s[8] = {};
-    for (int64_t t = (int64_t)blockIdx.y * 8 + lane; t < rows; t += (int64_t)gridDim.y * 8) {
-        const E *p = dy + t * ld + col;
-        if (col + 8 <= n) {
-            const u4v v = *reinterpret_cast<const u4v_any *>(p);
-            typedef E e8 __attribute__((ext_vector_type(8)));
-            const e8 e = __builtin_bit_cast(e8, v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s[j] += (float)e[j];
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (col + j < n) s[j] += (float)p[j];
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) lds[lane][8 * c + j] = s[j];
-    __syncthreads();
-    const int at = blockIdx.x * 256 + threadIdx.x;
-    if (at < n) {
-        float v = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v += lds[i][threadIdx.x];
-        parts[(int64_t)blockIdx.y * n + at] = v;
-    }
-}
-
-__global__ __launch_bounds__(1024) void column_sums_kernel(const float *parts, int count, int n,
-                                                           float *db, float *dbias) {
-    __shared__ float lds[16][kWave];
-    const int c = threadIdx.x & (kWave - 1), lane = threadIdx.x / kWave;
-    const int at = blockIdx.x * kWave + c;
-    float s = 0.0f;
-    if (at < n)
-        for (int i = lane; i < count; i += 16) s += parts[(int64_t)i * n + at];
-    lds[lane][c] = s;
-    __syncthreads();
-    if (lane == 0 && at < n) {
-        s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s += lds[i][c];
-        db[at] = s;
-        if (dbias) dbias[at] = s;
-    }
+    const Finish<E> finish(a);
+    finish.store(n, k, sum, finish.scale(k), finish.bias(k), db);
+    if (a.dbias && tile.k == 0 && j == 0 && place.wk == 0 && place.g == 0) a.dbias[n] = db;
 }
 
 // ---------------------------------------------------------------- host ----
 
+using Large = Shape<256, 256, 4, 2>;
+using Small = Shape<128, 128, 2, 2>;
+
 struct Plan {
-    bool big;              // 256 x 256 tiles, else 128 x 128
-    int64_t tiles;
-    int splits;            // of the sum over rows
-    int64_t slice;         // rows of a split, a multiple of kDepth
-    int column_parts;
-    int64_t column_floats, slab_floats;   // workspace: column sums, then slabs
+    bool large;
+    Schedule schedule;
+    int64_t split_tiles;
 };
 
 int64_t up(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
-Plan plan(int64_t rows, int64_t n, int64_t k) {
-    Plan p;
-    const int64_t big = up(n, 256) * up(k, 256);
-    p.big = big >= 160;
-    p.tiles = p.big ? big : up(n, 128) * up(k, 128);
-    // Few tiles: the rows are split until every CU has work, but no split
-    // is shorter than four tiles deep.
-    int64_t s = p.big ? 1 : 512 / p.tiles;
-    const int64_t most = up(rows, 4 * kDepth);
-    s = s < 1 ? 1 : s < most ? s : most;
-    p.slice = up(up(rows, s), kDepth) * kDepth;
-    p.splits = (int)up(rows, p.slice);
-    const int64_t wide = up(n, 256), deep = up(rows, 32);
-    int64_t c = 1024 / wide;
-    c = c < 1 ? 1 : c > 256 ? 256 : c;
-    p.column_parts = (int)(c < deep ? c : deep);
-    p.column_floats = up((p.column_parts + 1) * n, 4) * 4;
-    p.slab_floats = p.splits > 1 ? p.splits * n * k : 0;
+// Splits of the tiles left over after a whole number for each of `slots`
+// places: the number that takes least time, counting a tile's depth in steps,
+// and what writing, reading and joining a part costs.
+template <typename S>
+Plan plan_for(int64_t rows, int64_t n, int64_t k, int slots, double step_us, double slab_us,
+              double *us) {
+    Plan p = {};
+    p.large = S::BN == 256;
+    const int64_t tn = up(n, S::BN), tk = up(k, S::BK), tiles = tn * tk;
+    const int64_t steps = up(rows, kDepth);
+    const int64_t left = tiles % slots;
+    double best = (double)up(tiles, slots) * steps * step_us;
+    int64_t split = 1;
+    for (int64_t s = 2; left > 0 && s <= 16 && s * 2 <= steps; ++s) {
+        const double t = (double)(tiles / slots) * steps * step_us +
+                         (double)up(left * s, slots) * up(steps, s) * step_us +
+                         (double)(left * s) * slab_us + 4.0;
+        if (t < best) best = t, split = s;
+    }
+    p.schedule.tiles_n = (int32_t)tn;
+    p.schedule.tiles_k = (int32_t)tk;
+    p.split_tiles = split > 1 ? left : 0;
+    p.schedule.whole = (int32_t)(tiles - p.split_tiles);
+    p.schedule.slice = up(steps, split) * kDepth;
+    p.schedule.split = (int32_t)up(steps, up(steps, split));
+    *us = best;
     return p;
 }
 
-template <typename E, int BN, int BK, int WN, int WK>
-taco_status launch_grad(const WeightGrad &a, const Plan &p, const float *db, float *parts,
-                        hipStream_t stream) {
+Plan plan(int64_t rows, int64_t n, int64_t k) {
+    double large_us, small_us;
+    // One large tile fills a CU's LDS; two small ones share it.
+    const Plan large = plan_for<Large>(rows, n, k, 256, 1.2, 0.12, &large_us);
+    const Plan small = plan_for<Small>(rows, n, k, 512, 0.9, 0.03, &small_us);
+    return large_us <= small_us ? large : small;
+}
+
+int64_t slab_floats(const Plan &p) {
+    return p.split_tiles * p.schedule.split * (p.large ? Large::SLAB : Small::SLAB);
+}
+
+template <typename E, typename S>
+taco_status launch_grad(const WeightGrad &a, const Plan &p, hipStream_t stream) {
     const bool direct = ((reinterpret_cast<uintptr_t>(a.dy) | (uintptr_t)(a.lddy * 2) |
                           reinterpret_cast<uintptr_t>(a.codes) | (uintptr_t)a.hidden) & 15u) == 0 &&
-                        a.out_features % 8 == 0;
-    const dim3 grid((unsigned)p.tiles, (unsigned)p.splits);
-    return launch(direct ? reinterpret_cast<const void *>(&grad_kernel<E, BN, BK, WN, WK, true>)
-                         : reinterpret_cast<const void *>(&grad_kernel<E, BN, BK, WN, WK, false>),
-                  grid, WN * WK * kWave, stream, a, db, parts, p.slice);
+                        a.out_features % 8 == 0 && a.lddy < (INT64_C(1) << 24);
+    const int64_t groups = p.schedule.whole + p.split_tiles * p.schedule.split;
+    const taco_status st =
+        launch(direct ? reinterpret_cast<const void *>(&grad_kernel<E, S, true>)
+                      : reinterpret_cast<const void *>(&grad_kernel<E, S, false>),
+               dim3((unsigned)groups), S::THREADS, stream, a, p.schedule, a.workspace);
+    if (st != TACO_OK || p.split_tiles == 0) return st;
+    return launch(reinterpret_cast<const void *>(&join_kernel<E, S>),
+                  dim3((unsigned)p.split_tiles, S::NI * S::KI), S::THREADS, stream, a, p.schedule,
+                  static_cast<const float *>(a.workspace));
 }
 
 template <typename E>
 taco_status run(const WeightGrad &a, hipStream_t stream) {
     const Plan p = plan(a.rows, a.out_features, a.hidden);
-    float *const db = a.workspace;
-    float *const columns = db + a.out_features;
-    float *const slabs = a.workspace + p.column_floats;
-    taco_status st;
-    if (a.bias || a.dbias) {
-        st = launch(reinterpret_cast<const void *>(&column_parts_kernel<E>),
-                    dim3((unsigned)up(a.out_features, 256), (unsigned)p.column_parts), 256, stream,
-                    static_cast<const E *>(a.dy), a.lddy, a.rows, a.out_features, columns);
-        if (st != TACO_OK) return st;
-        st = launch(reinterpret_cast<const void *>(&column_sums_kernel),
-                    dim3((unsigned)up(a.out_features, kWave)), 1024, stream,
-                    static_cast<const float *>(columns), p.column_parts, a.out_features, db,
-                    a.dbias);
-        if (st != TACO_OK) return st;
-    }
-    float *const parts = p.splits > 1 ? slabs : nullptr;
-    st = p.big ? launch_grad<E, 256, 256, 4, 2>(a, p, db, parts, stream)
-               : launch_grad<E, 128, 128, 2, 2>(a, p, db, parts, stream);
-    if (st != TACO_OK || !parts) return st;
-    const int64_t groups = up((int64_t)a.out_features * a.hidden, 256);
-    return launch(reinterpret_cast<const void *>(&join_kernel<E>),
-                  dim3((unsigned)(groups < 8192 ? groups : 8192)), 256, stream, a,
-                  static_cast<const float *>(db), static_cast<const float *>(parts), p.splits);
+    return p.large ? launch_grad<E, Large>(a, p, stream) : launch_grad<E, Small>(a, p, stream);
 }
 
 }  // namespace
 
 int64_t weight_grad_workspace(int64_t rows, int64_t out_features, int64_t hidden) {
-    const Plan p = plan(rows, out_features, hidden);
-    return (p.column_floats + p.slab_floats) * (int64_t)sizeof(float);
+    return slab_floats(plan(rows, out_features, hidden)) * (int64_t)sizeof(float);
 }
 
 taco_status weight_grad(const WeightGrad &a, taco_norm_dtype dtype, hipStream_t stream) {

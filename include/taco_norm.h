@@ -120,8 +120,8 @@ taco_status taco_norm_checkpoint_backward(const void *dy, int64_t lddy, const ui
                                           void *dweight, void *dbias, void *workspace,
                                           int64_t workspace_bytes, hipStream_t stream);
 
-/* Bytes of workspace of taco_norm_weight_grad (0 with rows == 0; -1 for a
- * bad shape). */
+/* Bytes of workspace of taco_norm_weight_grad (0 where it needs none, -1 for
+ * a bad shape). */
 int64_t taco_norm_weight_grad_workspace(int64_t rows, int64_t out_features, int64_t hidden);
 
 /*
@@ -136,7 +136,8 @@ int64_t taco_norm_weight_grad_workspace(int64_t rows, int64_t out_features, int6
  *             float32); with accumulate != 0 (float32 only) the gradient is
  *             added to it.
  *   dbias     [out_features] float32 output db, may be NULL.
- *   workspace as above, taco_norm_weight_grad_workspace bytes.
+ *   workspace as above, taco_norm_weight_grad_workspace bytes (NULL where
+ *             that is 0).
  * A product of a code and a bf16 or fp16 value is exact in float32, and the
  * sums are float32: the gradient of the checkpointed tensor has no rounding
  * before the last.

@@ -151,7 +151,7 @@ def test_backward_workspace():
     assert f(1 << 20, 2560) == 512 * 2 * 2560 * 4
 
 
-def weight_grad(dy=A, lddy=64, codes=2 * A, rows=4, features=64, hidden=64, dtype=BF16, w=3 * A,
+def weight_grad(dy=A, lddy=64, codes=2 * A, rows=4096, features=64, hidden=64, dtype=BF16, w=3 * A,
                 b=4 * A, pdtype=F32, dw=5 * A, dwtype=BF16, accumulate=0, db=6 * A, ws=7 * A,
                 nbytes=None):
     if nbytes is None:
@@ -173,8 +173,9 @@ def test_weight_grad_refusals():
     assert weight_grad(ws=7 * A + 4) == ALIGN and weight_grad(db=6 * A + 2) == ALIGN
     assert weight_grad(dw=A + 64) == ALIAS and weight_grad(db=5 * A) == ALIAS
     assert weight_grad(ws=2 * A) == ALIAS
-    need = norm.taco_norm_weight_grad_workspace(4, 64, 64)
-    assert weight_grad(nbytes=need - 1) == PARAM
+    need = norm.taco_norm_weight_grad_workspace(4096, 64, 64)      # one tile, split
+    assert need > 0 and weight_grad(nbytes=need - 1) == PARAM
+    assert weight_grad(rows=4, nbytes=-1) == PARAM                 # needs none
     f = norm.taco_norm_weight_grad_workspace
     assert f(0, 64, 64) == 0 and f(4, 0, 64) == f(4, 64, 0) == f(-1, 64, 64) == -1
 
