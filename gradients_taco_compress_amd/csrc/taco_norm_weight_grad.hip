@@ -194,6 +194,11 @@ struct Shape {
     static constexpr int BN = BN_, BK = BK_, WN = WN_, WK = WK_;
     static constexpr int THREADS = WN * WK * kWave;
     static constexpr int NI = BN / WN / 16, KI = BK / WK / 16;    // fragments of a wave
+    // The waves that share columns of dY share their column sums: each adds up
+    // its first NB fragments, which differ (Place::n).
+    static constexpr int NB = NI / WK;
+    static_assert((NI & (NI - 1)) == 0 && (KI & (KI - 1)) == 0 && (NB & (NB - 1)) == 0 && NB > 0,
+                  "units of a wave");
     // A split's partial sums: every thread's, then the columns' sums.
     static constexpr int SLAB = BN * BK + BN;
 };
@@ -207,19 +212,24 @@ struct Place {
         : g((tid >> 4) & 3), r(tid & 15),
           wn(__builtin_amdgcn_readfirstlane(tid / kWave) % S::WN),
           wk(__builtin_amdgcn_readfirstlane(tid / kWave) / S::WN) {}
-    __device__ __forceinline__ int n(int i) const { return (wn * S::NI + i) * 16 + r; }
+    __device__ __forceinline__ int n(int i) const {
+        return (wn * S::NI + (i ^ (wk * S::NB))) * 16 + r;
+    }
     __device__ __forceinline__ int k(int j) const { return (wk * S::KI + j) * 16 + 4 * g; }
 };
 
 // Order of the instructions of one half tile: for each code fragment its
-// conversion, its products, and two LDS reads of the next half.
-template <int KI, int NI>
+// conversion, its products, the LDS reads of a fragment of the next half, and
+// (the first `LOADS` times) a global load.
+template <int KI, int NI, int LOADS>
 __device__ __forceinline__ void interleave() {
 #pragma unroll
     for (int j = 0; j < KI; ++j) {
-        __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);        // VALU
-        __builtin_amdgcn_sched_group_barrier(0x008, NI, 0);       // MFMA
-        __builtin_amdgcn_sched_group_barrier(0x100, (2 * NI + KI + KI - 1) / KI, 0);   // LDS reads
+        __builtin_amdgcn_sched_group_barrier(0x002, 4 + 2 * NI / KI, 0);             // VALU
+        __builtin_amdgcn_sched_group_barrier(0x008, NI, 0);                          // MFMA
+        __builtin_amdgcn_sched_group_barrier(0x100, (2 * NI + KI + KI - 1) / KI, 0); // LDS reads
+        if (j * ((LOADS + KI - 1) / KI) < LOADS)
+            __builtin_amdgcn_sched_group_barrier(0x020, (LOADS + KI - 1) / KI, 0);   // global loads
     }
 }
 
@@ -289,13 +299,13 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
             code_off[i] = (uint32_t)(code_row(i) * a.hidden + (k0 + col < a.hidden ? col : 0));
         }
     }
-    auto load_direct = [&](int64_t t, uint8_t *buf) {
+    [[maybe_unused]] const char *next_dy = dy + (t0 * a.lddy + n0) * 2, *next_codes = codes + t0 * a.hidden + k0;
+    auto load_direct = [&](uint8_t *buf) {
 #if defined(__HIP_DEVICE_COMPILE__)      // the host pass does not know the resource type
         // 0x00020000: raw 32-bit data; every offset is inside the operand.
-        const auto rd = __builtin_amdgcn_make_buffer_rsrc(
-            (void *)(dy + (t * a.lddy + n0) * 2), 0, 0x7FFFFFFF, 0x00020000);
-        const auto rc = __builtin_amdgcn_make_buffer_rsrc(
-            (void *)(codes + t * a.hidden + k0), 0, 0x7FFFFFFF, 0x00020000);
+        const auto rd = __builtin_amdgcn_make_buffer_rsrc((void *)next_dy, 0, 0x7FFFFFFF, 0x00020000);
+        const auto rc =
+            __builtin_amdgcn_make_buffer_rsrc((void *)next_codes, 0, 0x7FFFFFFF, 0x00020000);
 #pragma unroll
         for (int i = 0; i < DY_LOADS; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -348,11 +358,10 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
     // then + 4) or 8 g + r / 2 (codes); the read hands it column r of them.
     // A wave's units differ in their low bits only, so fragment i's unit is
     // the first one's XOR i.
-    static_assert((NI & (NI - 1)) == 0 && (KI & (KI - 1)) == 0, "units of a wave");
     int dy_at, code_at;
     {
         const int t = 8 * place.g + (place.r >> 2);
-        dy_at = t * BN * 2 + (((place.wn * NI) ^ turn_dy<BN>(t)) * 32) + (place.r & 3) * 8;
+        dy_at = t * BN * 2 + (((place.wn * NI + place.wk * S::NB) ^ turn_dy<BN>(t)) * 32) + (place.r & 3) * 8;
     }
     {
         const int t = 8 * place.g + (place.r >> 1);
@@ -385,11 +394,13 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
                 (__attribute__((address_space(3))) i2v *)(buf + (c ^ (j * 16)) + half * 32 * BK));
     };
 
+    constexpr int NB = S::NB;
     f4v sum[KI][NI];
-    float db[NI];
+    float db[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) db[i] = 0.0f;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-        db[i] = 0.0f;
 #pragma unroll
         for (int j = 0; j < KI; ++j) sum[j][i] = (f4v){0.0f, 0.0f, 0.0f, 0.0f};
     }
@@ -405,7 +416,7 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
             for (int i = 0; i < NI; ++i) sum[j][i] = M::run(u.v, f.dy[i], sum[j][i]);
         }
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
+        for (int i = 0; i < NB; ++i) {
             union { typename M::v8 v; typename M::v2 h[4]; } u;
             u.v = f.dy[i];
 #pragma unroll
@@ -418,27 +429,33 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
     if (DIRECT && full > 0) {
         // Past the last full tile the loads fetch that tile again, into LDS that
         // is not read any more: every step issues the same number of loads.
-        auto load = [&](int s, uint8_t *buf) {
-            load_direct(t0 + (int64_t)(s < full ? s : full - 1) * kDepth, buf);
+        const int64_t dy_step = (int64_t)kDepth * a.lddy * 2, code_step = (int64_t)kDepth * a.hidden;
+        auto advance = [&](bool more) {
+            next_dy += more ? dy_step : 0;
+            next_codes += more ? code_step : 0;
         };
-        load(0, lds0);
-        load(1, lds1);
-        load(2, lds2);
+        load_direct(lds0);
+        advance(full > 1);
+        load_direct(lds1);
+        advance(full > 2);
+        load_direct(lds2);
+        advance(full > 3);
         asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(2 * LOADS) : "memory");
         read(lds0, 0, fa);
         // Tile s in `cur`: its first half's fragments are in fa (or arriving).
         auto step = [&](int s, uint8_t *cur, uint8_t *next) {
             read(cur, 1, fb);
             multiply(fa);
-            interleave<KI, NI>();
+            interleave<KI, NI, 0>();
             __builtin_amdgcn_sched_barrier(0);
             // This wave has read all of cur, and its part of the next tile is
             // there (the one after may be on its way); then so for all waves.
             asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LOADS) : "memory");
-            load(s + 3, cur);
+            load_direct(cur);
             read(next, 0, fa);
             multiply(fb);
-            interleave<KI, NI>();
+            advance(s + 4 < full);
+            interleave<KI, NI, LOADS>();
             __builtin_amdgcn_sched_barrier(0);
         };
         int s = 0;
@@ -475,7 +492,7 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
 
     // Column sums: a lane holds those of its rows' group g.
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
+    for (int i = 0; i < NB; ++i) {
         db[i] += __shfl_xor(db[i], 16);
         db[i] += __shfl_xor(db[i], 32);
     }
@@ -486,18 +503,25 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
 #pragma unroll
             for (int i = 0; i < NI; ++i)
                 *reinterpret_cast<f4v *>(slab + ((j * NI + i) * THREADS + tid) * 4) = sum[j][i];
-        if (place.wk == 0 && place.g == 0) {
+        if (place.g == 0) {
 #pragma unroll
-            for (int i = 0; i < NI; ++i) slab[BN * BK + place.n(i)] = db[i];
+            for (int i = 0; i < NB; ++i) slab[BN * BK + place.n(i)] = db[i];
         }
         return;
     }
-    const Finish<E> finish(a);
-    if (a.dbias && tile.k == 0 && place.wk == 0 && place.g == 0) {
+    // Every wave needs those of all its columns.
+    float *const shared_db = reinterpret_cast<float *>(lds0);
+    __syncthreads();
+    if (place.g == 0) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
-            if (n0 + place.n(i) < a.out_features) a.dbias[n0 + place.n(i)] = db[i];
+        for (int i = 0; i < NB; ++i) {
+            shared_db[place.n(i)] = db[i];
+            if (a.dbias && tile.k == 0 && n0 + place.n(i) < a.out_features)
+                a.dbias[n0 + place.n(i)] = db[i];
+        }
     }
+    __syncthreads();
+    const Finish<E> finish(a);
 #pragma unroll
     for (int j = 0; j < KI; ++j) {
         const int k = k0 + place.k(j);
@@ -506,7 +530,7 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const int n = n0 + place.n(i);
-            if (n < a.out_features) finish.store(n, k, sum[j][i], sc, b, db[i]);
+            if (n < a.out_features) finish.store(n, k, sum[j][i], sc, b, shared_db[place.n(i)]);
         }
     }
 }
