@@ -15,13 +15,13 @@
 //    all start on one bank: the 32-byte (dY) or 16-byte (codes) units of row
 //    t are stored at unit index XOR f(t), with f such that the rows a half
 //    wave reads together fall on different banks.
-//  * Global loads go straight to LDS (16 bytes per lane, no registers) into
-//    three tiles in turn, so a tile's loads have two tiles' time to arrive.
-//    The next half tile's fragments are read while the current one is
-//    multiplied, and the one barrier per tile sits where both the finished
-//    tile's last fragments and the next tile's data are already there.
-//    Rows that do not start on 16-byte boundaries, and the last rows of a
-//    tensor, pass through registers with every element checked.
+//  * Global loads go straight to LDS (16 bytes per lane, no registers) into a
+//    ring of tiles; rows past the last are out of the loads' bounds and
+//    arrive as zeros.  Fragments are read a few products ahead of their use,
+//    and one barrier per tile serves both ends of the ring: the next tile has
+//    arrived, and the one before the current has been read, by all waves.
+//    Rows that do not start on 16-byte boundaries pass through registers,
+//    with the ends of rows checked.
 //  * db, the column sums of dY, comes from the same fragments (dot products
 //    with ones), so dY is read by one kernel only.
 //  * Tiles beyond a whole number per CU are split along t and their partial
@@ -43,7 +43,7 @@ typedef int i2v __attribute__((ext_vector_type(2)));
 typedef short s4v __attribute__((ext_vector_type(4)));
 
 constexpr int kWave = 64;
-constexpr int kDepth = 64;             // t per tile
+constexpr int kDepth = 32;             // t per tile: one matrix instruction's
 
 template <typename E>
 struct Mfma;
@@ -124,6 +124,17 @@ struct Schedule {
 
 struct Tile { int n, k; };
 
+// f(Int<0>{}), ..., f(Int<N - 1>{}): loop bodies that need their index constant.
+template <int I>
+struct Int { static constexpr int value = I; };
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void for_each(F &&f) {
+    if constexpr (I < N) {
+        f(Int<I>{});
+        for_each<N, I + 1>(f);
+    }
+}
+
 // Tile number t of an order in which neighbours share operands: strips of
 // four tile rows, each walked column by column.
 __device__ __forceinline__ Tile tile_at(const Schedule &s, int t) {
@@ -188,10 +199,12 @@ struct Finish {
     }
 };
 
-// Shape of a work-group's tile: BN x BK outputs by WN x WK waves.
-template <int BN_, int BK_, int WN_, int WK_>
+// Shape of a work-group's tile: BN x BK outputs by WN x WK waves, RING tiles
+// of both operands in LDS.
+template <int BN_, int BK_, int WN_, int WK_, int RING_>
 struct Shape {
-    static constexpr int BN = BN_, BK = BK_, WN = WN_, WK = WK_;
+    static constexpr int BN = BN_, BK = BK_, WN = WN_, WK = WK_, RING = RING_;
+    static_assert(RING % 2 == 0 && RING >= 4, "fragments alternate between two sets");
     static constexpr int THREADS = WN * WK * kWave;
     static constexpr int NI = BN / WN / 16, KI = BK / WK / 16;    // fragments of a wave
     // The waves that share columns of dY share their column sums: each adds up
@@ -218,21 +231,6 @@ struct Place {
     __device__ __forceinline__ int k(int j) const { return (wk * S::KI + j) * 16 + 4 * g; }
 };
 
-// Order of the instructions of one half tile: for each code fragment its
-// conversion, its products, the LDS reads of a fragment of the next half, and
-// (the first `LOADS` times) a global load.
-template <int KI, int NI, int LOADS>
-__device__ __forceinline__ void interleave() {
-#pragma unroll
-    for (int j = 0; j < KI; ++j) {
-        __builtin_amdgcn_sched_group_barrier(0x002, 4 + 2 * NI / KI, 0);             // VALU
-        __builtin_amdgcn_sched_group_barrier(0x008, NI, 0);                          // MFMA
-        __builtin_amdgcn_sched_group_barrier(0x100, (2 * NI + KI + KI - 1) / KI, 0); // LDS reads
-        if (j * ((LOADS + KI - 1) / KI) < LOADS)
-            __builtin_amdgcn_sched_group_barrier(0x020, (LOADS + KI - 1) / KI, 0);   // global loads
-    }
-}
-
 template <typename E, typename S, bool DIRECT>
 __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule plan,
                                                           float *slabs) {
@@ -242,11 +240,21 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
     constexpr int LOADS = DY_LOADS + CODE_LOADS;
     constexpr int DY_CHUNKS = BN / 8, CODE_CHUNKS = BK / 16;      // 16-byte chunks of a row
     using M = Mfma<E>;
-    // Three variables, not one: the compiler then knows that a load into one
-    // tile does not touch the fragments being read from another.
-    __shared__ __align__(1024) uint8_t lds0[DY_BYTES + CODE_BYTES];
-    __shared__ __align__(1024) uint8_t lds1[DY_BYTES + CODE_BYTES];
-    __shared__ __align__(1024) uint8_t lds2[DY_BYTES + CODE_BYTES];
+    // A variable for each tile of the ring, not one for all: the compiler then
+    // knows that a load into one does not touch the fragments being read from
+    // another, and does not wait for it.
+    constexpr int TILE = DY_BYTES + CODE_BYTES, RING = DIRECT ? S::RING : 2;
+    __shared__ __align__(1024) uint8_t lds0[TILE], lds1[TILE], lds2[RING > 2 ? TILE : 1],
+        lds3[RING > 3 ? TILE : 1], lds4[RING > 4 ? TILE : 1], lds5[RING > 5 ? TILE : 1];
+    auto ring = [&](auto index) -> uint8_t * {
+        constexpr int i = decltype(index)::value % RING;
+        if constexpr (i == 0) return lds0;
+        else if constexpr (i == 1) return lds1;
+        else if constexpr (i == 2) return lds2;
+        else if constexpr (i == 3) return lds3;
+        else if constexpr (i == 4) return lds4;
+        else return lds5;
+    };
 
     const int tid = threadIdx.x;
     [[maybe_unused]] const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -283,42 +291,54 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
         return 16 * (((i * THREADS + tid) % CODE_CHUNKS) ^ turn_codes<BK>(code_row(i)));
     };
 
-    // Straight to LDS: every row exists; a chunk past the last column reads
-    // the tile's first one instead (its sums are never stored).  Offsets from
-    // the tile's first element fit 32 bits (the launcher sees to it).
-    uint32_t dy_off[DY_LOADS], code_off[CODE_LOADS];
+    // Straight to LDS: rows past t1 are out of the resource's bounds, which
+    // makes them zero; a chunk past the last column reads the tile's first one
+    // instead (its sums are never stored).  A tile's offsets from its first
+    // element fit 31 bits (the launcher sees to it).
+    static_assert(DY_LOADS == 2 && CODE_LOADS == 1, "loads of a tile");
+    [[maybe_unused]] uint32_t dy_off[2], code_off;
     if constexpr (DIRECT) {
 #pragma unroll
-        for (int i = 0; i < DY_LOADS; ++i) {
+        for (int i = 0; i < 2; ++i) {
             const int col = dy_col(i);
             dy_off[i] = (uint32_t)(dy_row(i) * (int)a.lddy + (n0 + col < a.out_features ? col : 0)) * 2u;
         }
-#pragma unroll
-        for (int i = 0; i < CODE_LOADS; ++i) {
-            const int col = code_col(i);
-            code_off[i] = (uint32_t)(code_row(i) * a.hidden + (k0 + col < a.hidden ? col : 0));
-        }
+        const int col = code_col(0);
+        code_off = (uint32_t)(code_row(0) * a.hidden + (k0 + col < a.hidden ? col : 0));
     }
-    [[maybe_unused]] const char *next_dy = dy + (t0 * a.lddy + n0) * 2, *next_codes = codes + t0 * a.hidden + k0;
+    // The next tile to load: its first elements, and how many tiles remain, the
+    // last of them with fewer rows.
+    [[maybe_unused]] const char *next_dy = dy + (t0 * a.lddy + n0) * 2;
+    [[maybe_unused]] const char *next_codes = codes + t0 * a.hidden + k0;
+    // (readfirstlane: these are the same for all lanes, and have to be kept so)
+    const int steps = __builtin_amdgcn_readfirstlane((int)((t1 - t0 + kDepth - 1) / kDepth));
+    [[maybe_unused]] int tiles_left = steps;
+    [[maybe_unused]] const int last_rows =
+        __builtin_amdgcn_readfirstlane((int)(t1 - t0 - (int64_t)(steps - 1) * kDepth));
+    [[maybe_unused]] const int dy_pitch = (int)a.lddy * 2;
     auto load_direct = [&](uint8_t *buf) {
 #if defined(__HIP_DEVICE_COMPILE__)      // the host pass does not know the resource type
-        // 0x00020000: raw 32-bit data; every offset is inside the operand.
-        const auto rd = __builtin_amdgcn_make_buffer_rsrc((void *)next_dy, 0, 0x7FFFFFFF, 0x00020000);
-        const auto rc =
-            __builtin_amdgcn_make_buffer_rsrc((void *)next_codes, 0, 0x7FFFFFFF, 0x00020000);
+        // Rows of this tile (none past the last tile).  Every column read exists,
+        // so the bounds need to be right for whole rows only.
+        const int two = tiles_left < 2 ? tiles_left : 2, sum_rows = (two - 1) * kDepth + last_rows;
+        const int rows = __builtin_amdgcn_readfirstlane(
+            sum_rows < 0 ? 0 : sum_rows < kDepth ? sum_rows : kDepth);
+        // 0x00020000: raw 32-bit data.
+        const auto rd = __builtin_amdgcn_make_buffer_rsrc((void *)next_dy, 0, rows * dy_pitch, 0x00020000);
+        const auto rc = __builtin_amdgcn_make_buffer_rsrc((void *)next_codes, 0, rows * a.hidden, 0x00020000);
 #pragma unroll
         for (int i = 0; i < DY_LOADS; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 rd,
                 (__attribute__((address_space(3))) void *)(buf + (i * THREADS + wave * kWave) * 16),
                 16, dy_off[i], 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < CODE_LOADS; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rc,
-                (__attribute__((address_space(3))) void *)(buf + DY_BYTES +
-                                                           (i * THREADS + wave * kWave) * 16),
-                16, code_off[i], 0, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rc,
+            (__attribute__((address_space(3))) void *)(buf + DY_BYTES + wave * kWave * 16), 16,
+            code_off, 0, 0, 0);
+        next_dy += (int64_t)kDepth * dy_pitch;
+        next_codes += (int64_t)kDepth * a.hidden;
+        --tiles_left;
 #endif
     };
     // Through registers: rows past t1 and columns past the last are zero.
@@ -369,29 +389,27 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
                   (place.r & 1) * 8;
     }
 
-    struct Fragments {
-        typename M::v8 dy[NI];
-        i2v codes[KI];
+    // (The addresses are opaque at each use, so that they are formed again for
+    // each tile: kept, those of the whole ring would not fit the registers.)
+    auto read_dy = [&](uint8_t *buf, int i) {
+        uint8_t *p = buf + (dy_at ^ (i * 32));
+        union { s4v s[2]; typename M::v8 v; } u;
+        u.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v *)p);
+        u.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s4v *)(p + 4 * BN * 2));
+        return u.v;
     };
-    auto read = [&](uint8_t *buf, int half, Fragments &f) {
-        // Opaque here, so that the addresses are formed again for each tile:
-        // kept, those of three tiles would not fit the registers.
-        int d = dy_at, c = code_at;
-        asm volatile("" : "+v"(d), "+v"(c));
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            uint8_t *p = buf + (d ^ (i * 32)) + half * 32 * BN * 2;
-            union { s4v s[2]; typename M::v8 v; } u;
-            u.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s4v *)p);
-            u.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s4v *)(p + 4 * BN * 2));
-            f.dy[i] = u.v;
-        }
-#pragma unroll
-        for (int j = 0; j < KI; ++j)
-            f.codes[j] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                (__attribute__((address_space(3))) i2v *)(buf + (c ^ (j * 16)) + half * 32 * BK));
+    auto read_codes = [&](uint8_t *buf, int j) {
+        return __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+            (__attribute__((address_space(3))) i2v *)(buf + (code_at ^ (j * 16))));
+    };
+    auto convert = [&](i2v c) {
+        union { typename M::v2 h[4]; typename M::v8 v; } u;
+        u.h[0] = M::template codes<false>((uint32_t)c[0]);
+        u.h[1] = M::template codes<true>((uint32_t)c[0]);
+        u.h[2] = M::template codes<false>((uint32_t)c[1]);
+        u.h[3] = M::template codes<true>((uint32_t)c[1]);
+        return u.v;
     };
 
     constexpr int NB = S::NB;
@@ -404,85 +422,92 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
 #pragma unroll
         for (int j = 0; j < KI; ++j) sum[j][i] = (f4v){0.0f, 0.0f, 0.0f, 0.0f};
     }
-    auto multiply = [&](const Fragments &f) {
-#pragma unroll
-        for (int j = 0; j < KI; ++j) {
-            union { typename M::v2 h[4]; typename M::v8 v; } u;
-            u.h[0] = M::template codes<false>((uint32_t)f.codes[j][0]);
-            u.h[1] = M::template codes<true>((uint32_t)f.codes[j][0]);
-            u.h[2] = M::template codes<false>((uint32_t)f.codes[j][1]);
-            u.h[3] = M::template codes<true>((uint32_t)f.codes[j][1]);
-#pragma unroll
-            for (int i = 0; i < NI; ++i) sum[j][i] = M::run(u.v, f.dy[i], sum[j][i]);
-        }
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            union { typename M::v8 v; typename M::v2 h[4]; } u;
-            u.v = f.dy[i];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) db[i] = M::add2(u.h[e], db[i]);
-        }
+    auto add_columns = [&](const typename M::v8 &v, int i, int e) {
+        union { typename M::v8 v; typename M::v2 h[4]; } u;
+        u.v = v;
+        db[i] = M::add2(u.h[e], db[i]);
     };
 
-    Fragments fa, fb;
-    const int full = DIRECT ? (int)((t1 - t0) / kDepth) : 0;
-    if (DIRECT && full > 0) {
-        // Past the last full tile the loads fetch that tile again, into LDS that
-        // is not read any more: every step issues the same number of loads.
-        const int64_t dy_step = (int64_t)kDepth * a.lddy * 2, code_step = (int64_t)kDepth * a.hidden;
-        auto advance = [&](bool more) {
-            next_dy += more ? dy_step : 0;
-            next_codes += more ? code_step : 0;
+    if constexpr (DIRECT) {
+        // Two sets of dY fragments (this tile's and the next's), a queue of code
+        // fragments read three products ahead, and two converted ones.
+        typename M::v8 fd[2][NI], fc[2];
+        i2v queue[4];
+        for_each<RING - 1>([&](auto i) { load_direct(ring(i)); });
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((RING - 2) * LOADS) : "memory");
+#pragma unroll
+        for (int i = 0; i < NI; ++i) fd[0][i] = read_dy(lds0, i);
+#pragma unroll
+        for (int j = 0; j < 3; ++j) queue[j] = read_codes(lds0, j);
+        fc[0] = convert(queue[0]);
+        auto step = [&](auto index) {
+            constexpr int s = decltype(index)::value;
+            uint8_t *const cur = ring(Int<s>{}), *const next = ring(Int<s + 1>{});
+            constexpr int kTurn = KI / 2 - 1;        // the block with the barrier
+            constexpr int kReads = NI / (KI / 2);    // dY fragments read in each of those after
+            for_each<KI>([&](auto block) {
+                constexpr int j = decltype(block)::value;
+                if constexpr (j == kTurn) {
+                    // The next tile has arrived (those after it may be on their way)
+                    // and the previous one has been read; after the barrier, for all.
+                    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((RING - 3) * LOADS)
+                                 : "memory");
+                    load_direct(ring(Int<s + RING - 1>{}));
+                }
+                asm volatile("" : "+v"(dy_at), "+v"(code_at));
+                constexpr int ahead = j + 3;
+                queue[ahead & 3] = ahead < KI ? read_codes(cur, ahead) : read_codes(next, ahead - KI);
+                if constexpr (j >= kTurn && j < kTurn + KI / 2) {
+#pragma unroll
+                    for (int i = 0; i < kReads; ++i)
+                        fd[(s + 1) & 1][(j - kTurn) * kReads + i] =
+                            read_dy(next, (j - kTurn) * kReads + i);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                fc[(j + 1) & 1] = convert(queue[(j + 1) & 3]);
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+                    sum[j][i] = M::run(fc[j & 1], fd[s & 1][i], sum[j][i]);
+#pragma unroll
+                for (int e = j * 4 * NB / KI; e < (j + 1) * 4 * NB / KI; ++e)
+                    add_columns(fd[s & 1][e / 4], e / 4, e & 3);
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      // MFMA
+                    __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);      // VALU
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            });
         };
-        load_direct(lds0);
-        advance(full > 1);
-        load_direct(lds1);
-        advance(full > 2);
-        load_direct(lds2);
-        advance(full > 3);
-        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(2 * LOADS) : "memory");
-        read(lds0, 0, fa);
-        // Tile s in `cur`: its first half's fragments are in fa (or arriving).
-        auto step = [&](int s, uint8_t *cur, uint8_t *next) {
-            read(cur, 1, fb);
-            multiply(fa);
-            interleave<KI, NI, 0>();
-            __builtin_amdgcn_sched_barrier(0);
-            // This wave has read all of cur, and its part of the next tile is
-            // there (the one after may be on its way); then so for all waves.
-            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LOADS) : "memory");
-            load_direct(cur);
-            read(next, 0, fa);
-            multiply(fb);
-            advance(s + 4 < full);
-            interleave<KI, NI, LOADS>();
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        int s = 0;
-        for (; s + 3 <= full; s += 3) {
-            step(s, lds0, lds1);
-            step(s + 1, lds1, lds2);
-            step(s + 2, lds2, lds0);
-        }
-        if (s < full) step(s, lds0, lds1);
-        if (s + 1 < full) step(s + 1, lds1, lds2);
+        // A whole ring at a time, so that every LDS address is a constant; the
+        // tiles past the last row are zero.
+        for (int s = 0; s < steps; s += RING) for_each<RING>(step);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    }
-    // What is not read directly: the last rows, or all of them.
-    int64_t t = t0 + (int64_t)full * kDepth;
-    if (t < t1) {
-        load_held(t);
-        __syncthreads();                    // every earlier fragment has been read
+    } else {
+        load_held(t0);
         store_held(lds0);
+        load_held(t0 + kDepth);
         __syncthreads();
-        for (uint8_t *cur = lds0, *next = lds1; t < t1; t += kDepth) {
-            const bool more = t + kDepth < t1;
-            if (more) load_held(t + kDepth);
-            read(cur, 0, fa);
-            read(cur, 1, fb);
-            multiply(fa);
-            multiply(fb);
-            if (more) store_held(next);
+        uint8_t *cur = lds0, *next = lds1;
+        for (int64_t t = t0; t < t1; t += kDepth) {
+            store_held(next);
+            load_held(t + 2 * kDepth);              // nothing past t1
+            typename M::v8 fd[NI];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                fd[i] = read_dy(cur, i);
+                if (i < NB) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) add_columns(fd[i], i, e);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < KI; ++j) {
+                const typename M::v8 fc = convert(read_codes(cur, j));
+#pragma unroll
+                for (int i = 0; i < NI; ++i) sum[j][i] = M::run(fc, fd[i], sum[j][i]);
+            }
+            // The next tile is in LDS, and this one has been read by all.
             __syncthreads();
             uint8_t *const swap = cur;
             cur = next;
@@ -559,8 +584,8 @@ __global__ __launch_bounds__(S::THREADS) void join_kernel(WeightGrad a, Schedule
 
 // ---------------------------------------------------------------- host ----
 
-using Large = Shape<256, 256, 4, 2>;
-using Small = Shape<128, 128, 2, 2>;
+using Large = Shape<256, 256, 4, 2, 6>;
+using Small = Shape<128, 128, 2, 2, 4>;
 
 struct Plan {
     bool large;
@@ -602,8 +627,8 @@ Plan plan_for(int64_t rows, int64_t n, int64_t k, int slots, double step_us, dou
 Plan plan(int64_t rows, int64_t n, int64_t k) {
     double large_us, small_us;
     // One large tile fills a CU's LDS; two small ones share it.
-    const Plan large = plan_for<Large>(rows, n, k, 256, 1.2, 0.12, &large_us);
-    const Plan small = plan_for<Small>(rows, n, k, 512, 0.9, 0.03, &small_us);
+    const Plan large = plan_for<Large>(rows, n, k, 256, 0.6, 0.12, &large_us);
+    const Plan small = plan_for<Small>(rows, n, k, 512, 0.45, 0.03, &small_us);
     return large_us <= small_us ? large : small;
 }
 
