@@ -40,6 +40,10 @@ NORM_SOURCES = [os.path.join(CSRC, f) for f in
                 ("taco_norm_abi.hip", "taco_norm_bf16.hip", "taco_norm_f16.hip",
                  "taco_norm_f32.hip", "taco_norm_weight_grad.hip")]
 NORM_LIB = os.path.join(PKG, "libtaco_norm.so")
+#: Its fast path from torch (host code only), a Python extension module.
+NORM_TORCH_SOURCE = os.path.join(CSRC, "taco_norm_torch.cpp")
+NORM_TORCH = os.path.join(PKG, "_norm_torch.so")
+CXX = os.environ.get("CXX", "g++")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -111,9 +115,26 @@ def build(verbose: bool = False, out: str | None = None) -> str:
     return lib
 
 
+def _norm_torch_command(out: str) -> list:
+    """Compile command of the torch module: torch's headers and libraries, and
+    NORM_LIB from the folder the module lies in."""
+    import sysconfig
+    from torch.utils.cpp_extension import include_paths, library_paths
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
+           "-DUSE_ROCM", "-I", os.path.join(ROOT, "include")]
+    for path in [sysconfig.get_paths()["include"], *include_paths(),
+                 os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include")]:
+        cmd += ["-isystem", path]
+    cmd += [NORM_TORCH_SOURCE, "-o", out]
+    for path in library_paths():
+        cmd += ["-L", path]
+    return cmd + ["-L", PKG, "-l:libtaco_norm.so", "-Wl,-rpath,$ORIGIN", "-ltorch_python",
+                  "-ltorch_hip", "-ltorch_cpu", "-lc10_hip", "-lc10"]
+
+
 def build_norm(verbose: bool = False) -> str:
-    """Compile NORM_SOURCES (in parallel) and link NORM_LIB; always
-    recompiles.  Returns NORM_LIB."""
+    """Compile NORM_SOURCES (in parallel), link NORM_LIB and NORM_TORCH;
+    always recompiles.  Returns NORM_LIB."""
     from concurrent.futures import ThreadPoolExecutor
     tag = f".tmp{os.getpid()}"
     objs = [src + tag + ".o" for src in NORM_SOURCES]
@@ -124,10 +145,13 @@ def build_norm(verbose: bool = False) -> str:
                     for src, obj in zip(NORM_SOURCES, objs)]
             for j in jobs:
                 j.result()
-        _run([HIPCC, "--offload-arch=gfx950", "-shared", *objs, "-o", NORM_LIB + tag], verbose)
+        _run([HIPCC, "--offload-arch=gfx950", "-shared", "-Wl,-soname,libtaco_norm.so", *objs,
+              "-o", NORM_LIB + tag], verbose)
         os.replace(NORM_LIB + tag, NORM_LIB)
+        _run(_norm_torch_command(NORM_TORCH + tag), verbose)
+        os.replace(NORM_TORCH + tag, NORM_TORCH)
     finally:
-        for path in objs + [NORM_LIB + tag]:
+        for path in objs + [NORM_LIB + tag, NORM_TORCH + tag]:
             if os.path.exists(path):
                 os.remove(path)
     return NORM_LIB

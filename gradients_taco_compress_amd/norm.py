@@ -39,6 +39,15 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
+# The usual calls, without the interpreter between them and the C ABI: each
+# function takes tensors only and returns None for what is not usual (the code
+# below then takes over, and words the errors).
+try:
+    from . import _norm_torch as _fast
+except ImportError as e:
+    raise ImportError(f"the torch module of libtaco_norm is not built ({e}); run "
+                      "`python gradients_taco_compress_amd/build.py`") from e
+
 _P, _I64, _I32, _F32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
 _STATUS = ctypes.c_int
 _SIGNATURES = {
@@ -208,6 +217,10 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, mean=None
                stream=None):
     """Layer norm over the last dimension: (y, mean, rstd), the statistics
     float32 [rows], as the backward pass takes them."""
+    if out is None and mean is None and rstd is None and stream is None:
+        done = _fast.layer_norm(x, weight, bias, eps)
+        if done is not None:
+            return done
     rows, hidden, ldx = _pitch(x, "x")
     w, b = _param(weight, hidden, x.dtype, "weight"), _param(bias, hidden, x.dtype, "bias")
     ptype = _param_type(weight, bias, x.dtype)
@@ -234,6 +247,10 @@ def layer_norm_checkpoint(x, weight=None, bias=None, eps: float = 1e-5, out=None
     """Layer norm that also writes its 8-bit checkpoint: (y, codes, rstd) with
     codes uint8 [..., hidden] (E4M3 of checkpoint_scale(hidden) times the
     normalised row) and rstd float32 [rows]."""
+    if out is None and codes is None and rstd is None and stream is None:
+        done = _fast.layer_norm_checkpoint(x, weight, bias, eps)
+        if done is not None:
+            return done
     rows, hidden, ldx = _pitch(x, "x")
     w, b = _param(weight, hidden, x.dtype, "weight"), _param(bias, hidden, x.dtype, "bias")
     ptype = _param_type(weight, bias, x.dtype)
@@ -262,6 +279,10 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, param_grads: bo
     """Gradients of layer_norm: (dx, dweight, dbias), the last two of
     param_dtype (weight's type; float32 without a weight), or None without
     param_grads.  dx may be dy (in place)."""
+    if dx is None and param_grads and param_dtype is None and stream is None:
+        done = _fast.layer_norm_backward(dy, x, mean, rstd, weight)
+        if done is not None:
+            return done
     rows, hidden, lddy = _pitch(dy, "dy")
     ldx = _same_rows(x, "x", dy.dtype, rows, hidden)
     m, r = _vector(mean, rows, "mean"), _vector(rstd, rows, "rstd")
@@ -288,6 +309,10 @@ def layer_norm_checkpoint_backward(dy, codes, rstd, weight=None, dx=None,
                                    param_grads: bool = True, param_dtype=None, stream=None):
     """Gradients of layer_norm_checkpoint from its checkpoint: as
     layer_norm_backward, with codes in the place of the saved input."""
+    if dx is None and param_grads and param_dtype is None and stream is None:
+        done = _fast.layer_norm_checkpoint_backward(dy, codes, rstd, weight)
+        if done is not None:
+            return done
     rows, hidden, lddy = _pitch(dy, "dy")
     c, r = _vector(codes, rows * hidden, "codes", torch.uint8), _vector(rstd, rows, "rstd")
     w, ptype = _backward_param(weight, hidden, dy.dtype, param_dtype)
@@ -309,6 +334,12 @@ def checkpoint_weight_grad(dy, codes, weight=None, bias=None, out=None, dtype=No
     dy: bf16 or fp16 [..., out_features]; codes [..., hidden].  dW is of
     ``dtype`` (dy's type by default, or float32); with ``accumulate`` it is
     added to ``out``, a float32 tensor."""
+    if bias_grad and stream is None:
+        result = dtype or (out.dtype if out is not None else None)
+        done = _fast.checkpoint_weight_grad(dy, codes, weight, bias, out,
+                                            result is torch.float32, bool(accumulate))
+        if done is not None and (result is None or done[0].dtype is result):
+            return done
     rows, features, lddy = _pitch(dy, "dy")
     if dy.dtype == torch.float32:
         raise TypeError("dy must be torch.bfloat16 or torch.float16")

@@ -45,6 +45,7 @@ def test_norm_sources_compile_like_the_rest(monkeypatch, tmp_path):
         open(cmd[cmd.index("-o") + 1], "wb").close()
     monkeypatch.setattr(m, "_run", fake_run)
     monkeypatch.setattr(m, "NORM_LIB", str(tmp_path / "libtaco_norm.so"))
+    monkeypatch.setattr(m, "NORM_TORCH", str(tmp_path / "_norm_torch.so"))
     m.build_norm()
     compiles = [c for c in cmds if "-c" in c]
     assert sorted(c[c.index("-c") + 1] for c in compiles) == sorted(m.NORM_SOURCES)
