@@ -21,8 +21,9 @@
 //    all rows of its work-group and adds in registers; the work-groups'
 //    sums go to the workspace and a second kernel adds them in a fixed
 //    order, so results do not depend on timing.
-//  * Rows wider than 512 threads hold (16384) take the kernels at the end,
-//    which re-read the row from the cache instead of holding it.
+//  * Rows wider than the registers hold (16384 columns; 12288 of float32 in the
+//    backward pass) take the kernels at the end, which re-read the row from
+//    the cache.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -30,19 +31,12 @@
 
 #include "taco_norm.h"
 #include "taco_norm_internal.hpp"
+#include "taco_norm_device.hpp"
 
 namespace taco_norm {
 namespace {
 
-typedef unsigned int u4v __attribute__((ext_vector_type(4)));
-typedef unsigned int u2v __attribute__((ext_vector_type(2)));
-// The same at any address (gfx950 reads and writes global memory unaligned).
-typedef u4v u4v_any __attribute__((aligned(1)));
-typedef u2v u2v_any __attribute__((aligned(1)));
 typedef float f2v __attribute__((ext_vector_type(2)));
-
-constexpr int kWave = 64;
-
 // ------------------------------------------------------------ elements ----
 
 // Eight elements as they sit in memory.
@@ -66,6 +60,12 @@ __device__ __forceinline__ float elem(const Raw<T> &r, int j) {
     }
 }
 
+template <typename T>
+__device__ __forceinline__ void opaque(Raw<T> &r) {
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(T) / 2; ++i) asm volatile("" : "+v"(r.v[i]));
+}
+
 // Rounds eight float32 to T, to nearest even.
 template <typename T>
 __device__ __forceinline__ Raw<T> pack(const float *f) {
@@ -83,10 +83,11 @@ __device__ __forceinline__ Raw<T> pack(const float *f) {
     return r;
 }
 
-// Chunk at p, of which n elements (0..8) exist.  WHOLE: rows start on 16-byte
-// boundaries and hold whole chunks, so n is 0 or 8.  Missing elements are 0.
-template <typename T, bool WHOLE>
-__device__ __forceinline__ Raw<T> load_chunk(const T *p, int n) {
+// Chunk at p of a row that starts at `row`, of which n elements (0..8) exist.
+// WHOLE: rows start on 16-byte boundaries and hold whole chunks, so n is 0 or
+// 8.  TINY: a row may be shorter than 16 bytes.  Missing elements are 0.
+template <typename T, bool WHOLE, bool TINY>
+__device__ __forceinline__ Raw<T> load_chunk(const T *p, const T *row, int n) {
     Raw<T> r;
 #pragma unroll
     for (unsigned i = 0; i < sizeof(T) / 2; ++i) r.v[i] = (u4v){0u, 0u, 0u, 0u};
@@ -102,14 +103,11 @@ __device__ __forceinline__ Raw<T> load_chunk(const T *p, int n) {
             r.v[i] = reinterpret_cast<const u4v_any *>(p)[i];
     } else if (n > 0) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (j >= n) break;
-            if constexpr (sizeof(T) == 4) {
-                r.v[j >> 2][j & 3] = __builtin_bit_cast(uint32_t, p[j]);
-            } else {
-                const uint32_t h = __builtin_bit_cast(uint16_t, p[j]);
-                r.v[0][j >> 1] |= h << (16 * (j & 1));
-            }
+        for (unsigned i = 0; i < sizeof(T) / 2; ++i) {
+            const int bytes = n * (int)sizeof(T) - 16 * (int)i;
+            if (bytes > 0)
+                r.v[i] = load_tail<TINY>(reinterpret_cast<const char *>(p) + 16 * i,
+                                         reinterpret_cast<const char *>(row), bytes);
         }
     }
     return r;
@@ -138,17 +136,26 @@ __device__ __forceinline__ void store_chunk(T *p, int n, const Raw<T> &r) {
     }
 }
 
-template <bool WHOLE>
-__device__ __forceinline__ u2v load_codes(const uint8_t *p, int n) {
+template <bool WHOLE, bool TINY>
+__device__ __forceinline__ u2v load_codes(const uint8_t *p, const uint8_t *row, int n) {
     u2v r = {0u, 0u};
     if constexpr (WHOLE) {
         if (n > 0) r = *reinterpret_cast<const u2v *>(p);
     } else if (n >= 8) {
         r = *reinterpret_cast<const u2v_any *>(p);
-    } else {
+    } else if (n > 0) {
+        if (!TINY || p + n - row >= 8) {
+            // The row's last 8 bytes, moved down.
+            const u2v v = *reinterpret_cast<const u2v_any *>(p + n - 8);
+            const uint64_t w = (((uint64_t)v.y << 32) | v.x) >> (8 * (8 - n));
+            r = (u2v){(uint32_t)w, (uint32_t)(w >> 32)};
+        } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < n) r[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t c = p[j < n ? j : n - 1];
+                r[j >> 2] |= (j < n ? c : 0u) << (8 * (j & 3));
+            }
+        }
     }
     return r;
 }
@@ -193,15 +200,22 @@ __device__ __forceinline__ void decode(const u2v c, float inv_scale, float *h) {
 }
 
 // Parameters of a chunk in float32 (`missing` where there is no parameter).
-template <typename T>
+template <typename T, bool TINY>
 __device__ __forceinline__ void load_params(const void *p, bool f32, int col, int n, float missing,
                                             float *out) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        out[j] = missing;
-        if (p && j < n)
-            out[j] = f32 ? static_cast<const float *>(p)[col + j]
-                         : (float)static_cast<const T *>(p)[col + j];
+    for (int j = 0; j < 8; ++j) out[j] = missing;
+    if (!p || n <= 0) return;
+    if (f32) {
+        const float *q = static_cast<const float *>(p);
+        const Raw<float> r = load_chunk<float, false, TINY>(q + col, q, n);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) out[j] = elem<float>(r, j);
+    } else {
+        const T *q = static_cast<const T *>(p);
+        const Raw<T> r = load_chunk<T, false, TINY>(q + col, q, n);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) out[j] = elem<T>(r, j);
     }
 }
 
@@ -241,7 +255,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 template <int TPR>
-constexpr int block_threads() { return TPR < 256 ? 256 : TPR; }
+constexpr int block_threads() { return TPR <= kWave ? 256 : TPR; }
 
 __device__ __forceinline__ int chunk_len(int hidden, int col) {
     const int n = hidden - col;
@@ -262,30 +276,35 @@ __global__ __launch_bounds__(block_threads<TPR>()) void forward_kernel(Forward a
     T *const y = static_cast<T *>(a.y);
 
     int len[NV];
-    float w[NV][8], b[NV][8];
     float count = 0.0f;
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-        const int col = 8 * (c * TPR + t);
-        len[c] = chunk_len(hidden, col);
+        len[c] = chunk_len(hidden, 8 * (c * TPR + t));
         count += (float)len[c];
-        load_params<T>(a.weight, a.params_f32, col, len[c], 1.0f, w[c]);
-        load_params<T>(a.bias, a.params_f32, col, len[c], 0.0f, b[c]);
     }
-    // Elements of the row this wave holds (of the 16 lanes, with TPR = 16).
-    const float n_wave = wave_sum<TPR>(count);
-    const float inv_n_wave = n_wave > 0.0f ? 1.0f / n_wave : 0.0f;
-    const float n_row = (float)hidden;
-
     const int64_t stride = (int64_t)gridDim.x * RPB;
     int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
     Raw<T> raw[NV];
     auto load = [&](int64_t r) {
 #pragma unroll
         for (int c = 0; c < NV; ++c)
-            raw[c] = load_chunk<T, WHOLE>(x + r * a.ldx + 8 * (c * TPR + t), len[c]);
+            raw[c] = load_chunk<T, WHOLE, TPR == 16>(x + r * a.ldx + 8 * (c * TPR + t),
+                                                     x + r * a.ldx, len[c]);
     };
+    // The row first: its statistics are needed before the parameters are.
     if (row < a.rows) load(row);
+    float w[NV][8], b[NV][8];
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        const int col = 8 * (c * TPR + t);
+        load_params<T, TPR == 16>(a.weight, a.params_f32, col, len[c], 1.0f, w[c]);
+        load_params<T, TPR == 16>(a.bias, a.params_f32, col, len[c], 0.0f, b[c]);
+    }
+    // Elements of the row this wave holds (of the 16 lanes, with TPR = 16).
+    const float n_wave = wave_sum<TPR>(count);
+    const float inv_n_wave = n_wave > 0.0f ? 1.0f / n_wave : 0.0f;
+    const float n_row = (float)hidden;
+
     for (int turn = 0; row < a.rows; row += stride, turn ^= 1) {
         float v[NV][8];
         float sum = 0.0f;
@@ -383,53 +402,71 @@ __global__ __launch_bounds__(block_threads<TPR>()) void backward_kernel(Backward
     for (int c = 0; c < NV; ++c) {
         const int col = 8 * (c * TPR + t);
         len[c] = chunk_len(hidden, col);
-        load_params<T>(a.weight, a.params_f32, col, len[c], 1.0f, w[c]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[c][j] = db[c][j] = 0.0f;
     }
     const float n_row = (float)hidden;
     const int64_t stride = (int64_t)gridDim.x * RPB;
     int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
-    Raw<T> raw_dy[NV], raw_x[CODES ? 1 : NV];
-    u2v raw_c[CODES ? NV : 1];
-    float mean = 0.0f, rstd = 0.0f;
-    auto load = [&](int64_t r) {
+    // Rows as they are in memory: the current one and the next.  A short row's
+    // values are kept in float32 until they are written, and its registers take
+    // the row after the next at once (4096x4096 from the checkpoint: 25.1 us
+    // with one row ahead, 23.7 us with two); a long one is unpacked again.
+    constexpr bool kKeep = NV <= 2;
+    struct Row {
+        Raw<T> dy[NV], x[CODES ? 1 : NV];
+        u2v codes[CODES ? NV : 1];
+        float mean, rstd;
+    };
+    Row held[2];
+    auto load = [&](int64_t r, Row &to) {
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
             const int col = 8 * (c * TPR + t);
-            raw_dy[c] = load_chunk<T, WHOLE>(dy + r * a.lddy + col, len[c]);
+            to.dy[c] = load_chunk<T, WHOLE, TPR == 16>(dy + r * a.lddy + col, dy + r * a.lddy, len[c]);
             if constexpr (CODES)
-                raw_c[c] = load_codes<WHOLE>(a.codes + r * hidden + col, len[c]);
+                to.codes[c] = load_codes<WHOLE, TPR == 16>(a.codes + r * hidden + col,
+                                                           a.codes + r * hidden, len[c]);
             else
-                raw_x[c] = load_chunk<T, WHOLE>(x + r * a.ldx + col, len[c]);
+                to.x[c] = load_chunk<T, WHOLE, TPR == 16>(x + r * a.ldx + col, x + r * a.ldx, len[c]);
         }
-        rstd = a.rstd[r];
-        if constexpr (!CODES) mean = a.mean[r];
+        to.rstd = a.rstd[r];
+        to.mean = CODES ? 0.0f : a.mean[r];
     };
-    if (row < a.rows) load(row);
-    for (int turn = 0; row < a.rows; row += stride, turn ^= 1) {
-        float g[NV][8], h[NV][8];
-        const float r = rstd;
+    // h of a chunk.  A missing element has dy = 0; its h must be finite too.
+    auto normalised = [&](const Row &in, int c, float *h) {
+        if constexpr (CODES) {
+            decode(in.codes[c], a.inv_scale, h);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                h[j] = (elem<T>(in.x[c], j) - in.mean) * in.rstd;
+                if (!(WHOLE ? len[c] > 0 : j < len[c])) h[j] = 0.0f;
+            }
+        }
+    };
+    auto process = [&](Row &in, Row &next, int turn) {
+        if constexpr (!kKeep)
+            if (row + stride < a.rows) load(row + stride, next);
+        float g[kKeep ? NV : 1][8], h[kKeep ? NV : 1][8];
+        const float r = in.rstd;
         float c1 = 0.0f, c2 = 0.0f;
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
-            if constexpr (CODES) decode(raw_c[c], a.inv_scale, h[c]);
+            float *const gc = g[kKeep ? c : 0], *const hc = h[kKeep ? c : 0];
+            normalised(in, c, hc);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float d = elem<T>(raw_dy[c], j);
-                if constexpr (!CODES) {
-                    h[c][j] = (elem<T>(raw_x[c], j) - mean) * r;
-                    // A missing element has dy = 0; its h must be finite too.
-                    if (!(WHOLE ? len[c] > 0 : j < len[c])) h[c][j] = 0.0f;
-                }
-                dw[c][j] = __builtin_fmaf(d, h[c][j], dw[c][j]);
+                const float d = elem<T>(in.dy[c], j);
+                dw[c][j] = __builtin_fmaf(d, hc[j], dw[c][j]);
                 db[c][j] += d;
-                g[c][j] = d * w[c][j];
-                c1 += g[c][j];
-                c2 = __builtin_fmaf(g[c][j], h[c][j], c2);
+                gc[j] = d * w[c][j];
+                c1 += gc[j];
+                c2 = __builtin_fmaf(gc[j], hc[j], c2);
             }
         }
-        if (row + stride < a.rows) load(row + stride);
+        if constexpr (kKeep)
+            if (row + 2 * stride < a.rows) load(row + 2 * stride, in);
 
         c1 = wave_sum<TPR>(c1);
         c2 = wave_sum<TPR>(c2);
@@ -450,12 +487,32 @@ __global__ __launch_bounds__(block_threads<TPR>()) void backward_kernel(Backward
         c2 /= n_row;
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
+            float *const gc = g[kKeep ? c : 0], *const hc = h[kKeep ? c : 0];
+            if constexpr (!kKeep) {
+                // Opaque, or the compiler keeps the values after all.
+                opaque(in.dy[c]);
+                if constexpr (CODES) asm volatile("" : "+v"(in.codes[c]));
+                else opaque(in.x[c]);
+                normalised(in, c, hc);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) gc[j] = elem<T>(in.dy[c], j) * w[c][j];
+            }
             float o[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                o[j] = r * __builtin_fmaf(-h[c][j], c2, g[c][j] - c1);
+            for (int j = 0; j < 8; ++j) o[j] = r * __builtin_fmaf(-hc[j], c2, gc[j] - c1);
             store_chunk<T, WHOLE>(dx + row * a.lddx + 8 * (c * TPR + t), len[c], pack<T>(o));
         }
+        row += stride;
+    };
+    if (row < a.rows) load(row, held[0]);
+    if (kKeep && row + stride < a.rows) load(row + stride, held[1]);
+#pragma unroll
+    for (int c = 0; c < NV; ++c)
+        load_params<T, TPR == 16>(a.weight, a.params_f32, 8 * (c * TPR + t), len[c], 1.0f, w[c]);
+    while (row < a.rows) {
+        process(held[0], held[1], 0);
+        if (row >= a.rows) break;
+        process(held[1], held[0], 1);
     }
 
     if (!a.partial) return;
@@ -655,9 +712,33 @@ __global__ __launch_bounds__(256) void params_wide_kernel(Backward a) {
 
 // ---------------------------------------------------------------- host ----
 
-// Threads per row and chunks per thread by row length.
+// Threads per row and chunks per thread by row length: a wave to a row as long
+// as it can hold it (no barrier, and the parameters are loaded once for many
+// rows); measured at 16384x3584, a wave of 7 chunks 43 us, 256 threads of 2
+// 45-49 us, and at 8192x2560 17.5 against 21.5 us.
 template <typename F>
-taco_status for_width(int hidden, F &&f) {
+taco_status for_forward_width(int hidden, F &&f) {
+    const int chunks = (hidden + 7) / 8;
+    if (chunks <= 16) return f.template run<16, 1>();
+    if (chunks <= 32) return f.template run<16, 2>();
+    if (chunks <= 64) return f.template run<64, 1>();
+    if (chunks <= 128) return f.template run<64, 2>();
+    if (chunks <= 192) return f.template run<64, 3>();
+    if (chunks <= 256) return f.template run<64, 4>();
+    if (chunks <= 320) return f.template run<64, 5>();
+    if (chunks <= 384) return f.template run<64, 6>();
+    if (chunks <= 448) return f.template run<64, 7>();
+    if (chunks <= 512) return f.template run<64, 8>();
+    if (chunks <= 768) return f.template run<256, 3>();
+    if (chunks <= 1024) return f.template run<256, 4>();
+    if (chunks <= 1536) return f.template run<256, 6>();
+    return f.template run<256, 8>();
+}
+// The backward pass holds twice the row and the sums of its columns, so the
+// work-group takes over earlier: waves of their own rows are faster up to 1024
+// columns only.
+template <typename F>
+taco_status for_backward_width(int hidden, F &&f) {
     const int chunks = (hidden + 7) / 8;
     if (chunks <= 16) return f.template run<16, 1>();
     if (chunks <= 64) return f.template run<64, 1>();
@@ -666,8 +747,8 @@ taco_status for_width(int hidden, F &&f) {
     if (chunks <= 512) return f.template run<256, 2>();
     if (chunks <= 768) return f.template run<256, 3>();
     if (chunks <= 1024) return f.template run<512, 2>();
-    if (chunks <= 1536) return f.template run<512, 3>();
-    return f.template run<512, 4>();
+    if (chunks <= 1536 || F::kMaxHeld <= 1536 * 8) return f.template run<512, 3>();
+    if constexpr (F::kMaxHeld > 1536 * 8) return f.template run<512, 4>();
 }
 
 inline bool on16(const void *p, int64_t ld, int64_t size) {
@@ -686,8 +767,12 @@ struct ForwardLaunch {
     bool whole;
     template <int TPR, int NV, bool WHOLE> taco_status go() const {
         constexpr int threads = block_threads<TPR>();
-        // Enough work-groups to fill the 2048 threads of each of 256 CUs.
-        const unsigned grid = grid_rows(a.rows, threads / TPR, 256 * (2048 / threads));
+        // Threads for each of the 256 CUs: fewer where a thread holds more, so
+        // that a wave takes several rows for one load of the parameters and
+        // 16-32 KiB of rows are on their way to a CU (measured at 8192x2560:
+        // 512 threads 17.6 us, 1024 19.3 us, 2048 20.8 us).
+        constexpr int per_cu = 2048 / NV < 512 ? 512 : 2048 / NV;
+        const unsigned grid = grid_rows(a.rows, threads / TPR, 256 * (per_cu / threads));
         if (a.codes)
             return launch(reinterpret_cast<const void *>(&forward_kernel<T, TPR, NV, WHOLE, true>),
                           dim3(grid), threads, stream, a);
@@ -701,6 +786,8 @@ struct ForwardLaunch {
 
 template <typename T>
 struct BackwardLaunch {
+    // Four chunks of float32, their sums and the next row's would not fit.
+    static constexpr int kMaxHeld = sizeof(T) == 4 ? 512 * 24 : 512 * 32;
     Backward a;
     hipStream_t stream;
     bool whole;
@@ -735,7 +822,7 @@ taco_status Rows<K>::forward(const Forward &a, hipStream_t stream) {
     const bool whole = a.hidden % 8 == 0 && on16(a.x, a.ldx, sizeof(T)) &&
                        on16(a.y, a.ldy, sizeof(T)) &&
                        (reinterpret_cast<uintptr_t>(a.codes) & 7u) == 0;
-    return for_width(a.hidden, ForwardLaunch<T>{a, stream, whole});
+    return for_forward_width(a.hidden, ForwardLaunch<T>{a, stream, whole});
 }
 
 template <typename K>
@@ -743,7 +830,7 @@ taco_status Rows<K>::backward(const Backward &a, hipStream_t stream) {
     using T = typename K::type;
     const int64_t parts = backward_parts(a.rows, a.hidden);
     taco_status st;
-    if (a.hidden > kMaxHeld) {
+    if (a.hidden > BackwardLaunch<T>::kMaxHeld) {
         if (a.partial) {
             const dim3 grid((unsigned)((a.hidden + 255) / 256), (unsigned)parts);
             st = launch(a.codes ? reinterpret_cast<const void *>(&params_wide_kernel<T, true>)
@@ -759,7 +846,7 @@ taco_status Rows<K>::backward(const Backward &a, hipStream_t stream) {
                            on16(a.dx, a.lddx, sizeof(T)) &&
                            (a.codes ? (reinterpret_cast<uintptr_t>(a.codes) & 7u) == 0
                                     : on16(a.x, a.ldx, sizeof(T)));
-        st = for_width(a.hidden, BackwardLaunch<T>{a, stream, whole, parts});
+        st = for_backward_width(a.hidden, BackwardLaunch<T>{a, stream, whole, parts});
     }
     if (st != TACO_OK || !a.partial) return st;
     return launch(reinterpret_cast<const void *>(&parts_kernel<T>),

@@ -31,18 +31,15 @@
 
 #include "taco_norm.h"
 #include "taco_norm_internal.hpp"
+#include "taco_norm_device.hpp"
 
 namespace taco_norm {
 namespace {
 
-typedef unsigned int u4v __attribute__((ext_vector_type(4)));
-typedef unsigned int u2v __attribute__((ext_vector_type(2)));
-typedef u4v u4v_any __attribute__((aligned(1)));
 typedef float f4v __attribute__((ext_vector_type(4)));
 typedef int i2v __attribute__((ext_vector_type(2)));
 typedef short s4v __attribute__((ext_vector_type(4)));
 
-constexpr int kWave = 64;
 constexpr int kDepth = 32;             // t per tile: one matrix instruction's
 
 template <typename E>
@@ -89,28 +86,6 @@ __device__ __forceinline__ int turn_dy(int t) {
 template <int BK>
 __device__ __forceinline__ int turn_codes(int t) {
     return BK == 256 ? (t & 15) : ((t >> 1) & 7);
-}
-
-// 16 bytes at p, of which the first n (1..16) belong to a row that starts at
-// `row`: the others are zero, and nothing outside the row is read.
-__device__ __forceinline__ u4v load_tail(const char *p, const char *row, int n) {
-    if (n >= 16) return *reinterpret_cast<const u4v_any *>(p);
-    if (p + n - row >= 16) {
-        // The row's last 16 bytes, moved down.
-        const u4v v = *reinterpret_cast<const u4v_any *>(p + n - 16);
-        const uint64_t lo = ((uint64_t)v.y << 32) | v.x, hi = ((uint64_t)v.w << 32) | v.z;
-        const int sh = 8 * (16 - n);
-        const uint64_t a = sh >= 64 ? hi >> (sh - 64) : (lo >> sh) | (hi << (64 - sh));
-        const uint64_t b = sh >= 64 ? 0 : hi >> sh;
-        return (u4v){(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)};
-    }
-    u4v v = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        const uint32_t c = (uint8_t)p[j < n ? j : n - 1];
-        v[j >> 2] |= (j < n ? c : 0u) << (8 * (j & 3));
-    }
-    return v;
 }
 
 // Which output tile and which rows a work-group takes.  The first `whole`
@@ -351,7 +326,7 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
             held_dy[i] = (u4v){0u, 0u, 0u, 0u};
             if (n > 0) {
                 const char *row = dy + (t + dy_row(i)) * a.lddy * 2;
-                held_dy[i] = load_tail(row + col * 2, row, n < 8 ? 2 * n : 16);
+                held_dy[i] = load_tail<true>(row + col * 2, row, n < 8 ? 2 * n : 16);
             }
         }
 #pragma unroll
@@ -361,7 +336,7 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
             held_codes[i] = (u4v){0u, 0u, 0u, 0u};
             if (n > 0) {
                 const char *row = codes + (t + code_row(i)) * a.hidden;
-                held_codes[i] = load_tail(row + col, row, n < 16 ? n : 16);
+                held_codes[i] = load_tail<true>(row + col, row, n < 16 ? n : 16);
             }
         }
     };
