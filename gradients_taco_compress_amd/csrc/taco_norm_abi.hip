@@ -225,10 +225,16 @@ taco_status taco_norm_checkpoint_backward(const void *dy, int64_t lddy, const ui
                     stream);
 }
 
-int64_t taco_norm_weight_grad_workspace(int64_t rows, int64_t out_features, int64_t hidden) {
-    if (!valid_hidden(hidden) || !valid_hidden(out_features) || !valid_rows(rows, hidden, hidden))
+int64_t taco_norm_weight_grad_workspace(const void *dy, int64_t lddy, const uint8_t *codes,
+                                        int64_t rows, int64_t out_features, int64_t hidden) {
+    if (!valid_hidden(hidden) || !valid_hidden(out_features) ||
+        !valid_rows(rows, out_features, lddy) || !valid_rows(rows, hidden, hidden))
         return -1;
-    return rows == 0 ? 0 : weight_grad_workspace(rows, out_features, hidden);
+    if (rows == 0) return 0;
+    WeightGrad a = {};
+    a.dy = dy; a.lddy = lddy; a.codes = codes; a.rows = rows;
+    a.out_features = (int32_t)out_features; a.hidden = (int32_t)hidden;
+    return weight_grad_workspace(a);
 }
 
 taco_status taco_norm_weight_grad(const void *dy, int64_t lddy, const uint8_t *codes,
@@ -258,7 +264,8 @@ taco_status taco_norm_weight_grad(const void *dy, int64_t lddy, const uint8_t *c
         st = accumulate ? TACO_OK : fill_zero(dw, out_features * hidden, dw_dtype, stream);
         return st != TACO_OK || !dbias ? st : fill_zero(dbias, out_features, TACO_NORM_F32, stream);
     }
-    const int64_t need = weight_grad_workspace(rows, out_features, hidden);
+    const int64_t need =
+        taco_norm_weight_grad_workspace(dy, lddy, codes, rows, out_features, hidden);
     if (!dy || !codes || (need && !workspace)) return TACO_ERR_NULL;
     if (!aligned(dy, 2) || !aligned(weight, p) || !aligned(bias, p) || !aligned(dw, d) ||
         !aligned(dbias, 4) || (need && !aligned(workspace, 16)))

@@ -88,11 +88,12 @@ struct WeightGrad {
     float *dbias;                  // may be null
     float *workspace;
     int64_t lddy, rows;
+    int64_t ldcodes;               // set by the launcher
     int32_t out_features, hidden;
     int32_t params_f32, dw_f32, accumulate;
     float inv_scale;
 };
-int64_t weight_grad_workspace(int64_t rows, int64_t out_features, int64_t hidden);
+int64_t weight_grad_workspace(const WeightGrad &a);
 taco_status weight_grad(const WeightGrad &a, taco_norm_dtype dtype, hipStream_t stream);
 
 // The status is the launch's own (not an earlier error left in the runtime).

@@ -254,7 +254,9 @@ PyObject *checkpoint_weight_grad(PyObject *, PyObject *const *args, Py_ssize_t n
         const at::Tensor *given = tensor(args[4]);
         if (args[4] != Py_None && !vector(given, in.dev, in.r.n * hidden, dw_type)) return none();
         if (accumulate && (!given || !f32)) return none();
-        const int64_t bytes = taco_norm_weight_grad_workspace(in.r.rows, in.r.n, hidden);
+        const int64_t bytes = taco_norm_weight_grad_workspace(
+            in.t->data_ptr(), in.r.ld, static_cast<const uint8_t *>(codes->data_ptr()), in.r.rows,
+            in.r.n, hidden);
         if (bytes < 0) return none();
         at::Tensor made;
         if (!given) made = make({in.r.n, hidden}, dw_type, in.dev);

@@ -20,8 +20,9 @@
 //    arrive as zeros.  Fragments are read a few products ahead of their use,
 //    and one barrier per tile serves both ends of the ring: the next tile has
 //    arrived, and the one before the current has been read, by all waves.
-//    Rows that do not start on 16-byte boundaries pass through registers,
-//    with the ends of rows checked.
+//    Operands whose rows do not start on 16-byte boundaries are first copied
+//    to where they do (measured at 8191x2555x2559: the copies 25 us of 150 us;
+//    loading such rows through registers instead took 220 us).
 //  * db, the column sums of dY, comes from the same fragments (dot products
 //    with ones), so dY is read by one kernel only.
 //  * Tiles beyond a whole number per CU are split along t and their partial
@@ -206,7 +207,7 @@ struct Place {
     __device__ __forceinline__ int k(int j) const { return (wk * S::KI + j) * 16 + 4 * g; }
 };
 
-template <typename E, typename S, bool DIRECT>
+template <typename E, typename S>
 __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule plan,
                                                           float *slabs) {
     constexpr int BN = S::BN, BK = S::BK, NI = S::NI, KI = S::KI, THREADS = S::THREADS;
@@ -218,7 +219,7 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
     // A variable for each tile of the ring, not one for all: the compiler then
     // knows that a load into one does not touch the fragments being read from
     // another, and does not wait for it.
-    constexpr int TILE = DY_BYTES + CODE_BYTES, RING = DIRECT ? S::RING : 2;
+    constexpr int TILE = DY_BYTES + CODE_BYTES, RING = S::RING;
     __shared__ __align__(1024) uint8_t lds0[TILE], lds1[TILE], lds2[RING > 2 ? TILE : 1],
         lds3[RING > 3 ? TILE : 1], lds4[RING > 4 ? TILE : 1], lds5[RING > 5 ? TILE : 1];
     auto ring = [&](auto index) -> uint8_t * {
@@ -272,19 +273,16 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
     // element fit 31 bits (the launcher sees to it).
     static_assert(DY_LOADS == 2 && CODE_LOADS == 1, "loads of a tile");
     [[maybe_unused]] uint32_t dy_off[2], code_off;
-    if constexpr (DIRECT) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int col = dy_col(i);
-            dy_off[i] = (uint32_t)(dy_row(i) * (int)a.lddy + (n0 + col < a.out_features ? col : 0)) * 2u;
-        }
-        const int col = code_col(0);
-        code_off = (uint32_t)(code_row(0) * a.hidden + (k0 + col < a.hidden ? col : 0));
+    for (int i = 0; i < 2; ++i) {
+        const int col = dy_col(i);
+        dy_off[i] = (uint32_t)(dy_row(i) * (int)a.lddy + (n0 + col < a.out_features ? col : 0)) * 2u;
     }
+    code_off = (uint32_t)(code_row(0) * (int)a.ldcodes + (k0 + code_col(0) < a.hidden ? code_col(0) : 0));
     // The next tile to load: its first elements, and how many tiles remain, the
     // last of them with fewer rows.
     [[maybe_unused]] const char *next_dy = dy + (t0 * a.lddy + n0) * 2;
-    [[maybe_unused]] const char *next_codes = codes + t0 * a.hidden + k0;
+    [[maybe_unused]] const char *next_codes = codes + t0 * a.ldcodes + k0;
     // (readfirstlane: these are the same for all lanes, and have to be kept so)
     const int steps = __builtin_amdgcn_readfirstlane((int)((t1 - t0 + kDepth - 1) / kDepth));
     [[maybe_unused]] int tiles_left = steps;
@@ -300,7 +298,7 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
             sum_rows < 0 ? 0 : sum_rows < kDepth ? sum_rows : kDepth);
         // 0x00020000: raw 32-bit data.
         const auto rd = __builtin_amdgcn_make_buffer_rsrc((void *)next_dy, 0, rows * dy_pitch, 0x00020000);
-        const auto rc = __builtin_amdgcn_make_buffer_rsrc((void *)next_codes, 0, rows * a.hidden, 0x00020000);
+        const auto rc = __builtin_amdgcn_make_buffer_rsrc((void *)next_codes, 0, rows * (int)a.ldcodes, 0x00020000);
 #pragma unroll
         for (int i = 0; i < DY_LOADS; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -312,43 +310,10 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
             (__attribute__((address_space(3))) void *)(buf + DY_BYTES + wave * kWave * 16), 16,
             code_off, 0, 0, 0);
         next_dy += (int64_t)kDepth * dy_pitch;
-        next_codes += (int64_t)kDepth * a.hidden;
+        next_codes += (int64_t)kDepth * a.ldcodes;
         --tiles_left;
 #endif
     };
-    // Through registers: rows past t1 and columns past the last are zero.
-    u4v held_dy[DY_LOADS], held_codes[CODE_LOADS];
-    auto load_held = [&](int64_t t) {
-#pragma unroll
-        for (int i = 0; i < DY_LOADS; ++i) {
-            const int col = n0 + dy_col(i);
-            const int n = t + dy_row(i) < t1 ? a.out_features - col : 0;
-            held_dy[i] = (u4v){0u, 0u, 0u, 0u};
-            if (n > 0) {
-                const char *row = dy + (t + dy_row(i)) * a.lddy * 2;
-                held_dy[i] = load_tail<true>(row + col * 2, row, n < 8 ? 2 * n : 16);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < CODE_LOADS; ++i) {
-            const int col = k0 + code_col(i);
-            const int n = t + code_row(i) < t1 ? a.hidden - col : 0;
-            held_codes[i] = (u4v){0u, 0u, 0u, 0u};
-            if (n > 0) {
-                const char *row = codes + (t + code_row(i)) * a.hidden;
-                held_codes[i] = load_tail<true>(row + col, row, n < 16 ? n : 16);
-            }
-        }
-    };
-    auto store_held = [&](uint8_t *buf) {
-#pragma unroll
-        for (int i = 0; i < DY_LOADS; ++i)
-            *reinterpret_cast<u4v *>(buf + (i * THREADS + tid) * 16) = held_dy[i];
-#pragma unroll
-        for (int i = 0; i < CODE_LOADS; ++i)
-            *reinterpret_cast<u4v *>(buf + DY_BYTES + (i * THREADS + tid) * 16) = held_codes[i];
-    };
-
     // Fragment addresses: lane (g, r) reads 8 bytes of row 8 g + r / 4 (dY;
     // then + 4) or 8 g + r / 2 (codes); the read hands it column r of them.
     // A wave's units differ in their low bits only, so fragment i's unit is
@@ -403,92 +368,60 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
         db[i] = M::add2(u.h[e], db[i]);
     };
 
-    if constexpr (DIRECT) {
-        // Two sets of dY fragments (this tile's and the next's), a queue of code
-        // fragments read three products ahead, and two converted ones.
-        typename M::v8 fd[2][NI], fc[2];
-        i2v queue[4];
-        for_each<RING - 1>([&](auto i) { load_direct(ring(i)); });
-        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((RING - 2) * LOADS) : "memory");
+    // Two sets of dY fragments (this tile's and the next's), a queue of code
+    // fragments read three products ahead, and two converted ones.
+    typename M::v8 fd[2][NI], fc[2];
+    i2v queue[4];
+    for_each<RING - 1>([&](auto i) { load_direct(ring(i)); });
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((RING - 2) * LOADS) : "memory");
 #pragma unroll
-        for (int i = 0; i < NI; ++i) fd[0][i] = read_dy(lds0, i);
+    for (int i = 0; i < NI; ++i) fd[0][i] = read_dy(lds0, i);
 #pragma unroll
-        for (int j = 0; j < 3; ++j) queue[j] = read_codes(lds0, j);
-        fc[0] = convert(queue[0]);
-        auto step = [&](auto index) {
-            constexpr int s = decltype(index)::value;
-            uint8_t *const cur = ring(Int<s>{}), *const next = ring(Int<s + 1>{});
-            constexpr int kTurn = KI / 2 - 1;        // the block with the barrier
-            constexpr int kReads = NI / (KI / 2);    // dY fragments read in each of those after
-            for_each<KI>([&](auto block) {
-                constexpr int j = decltype(block)::value;
-                if constexpr (j == kTurn) {
-                    // The next tile has arrived (those after it may be on their way)
-                    // and the previous one has been read; after the barrier, for all.
-                    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((RING - 3) * LOADS)
-                                 : "memory");
-                    load_direct(ring(Int<s + RING - 1>{}));
-                }
-                asm volatile("" : "+v"(dy_at), "+v"(code_at));
-                constexpr int ahead = j + 3;
-                queue[ahead & 3] = ahead < KI ? read_codes(cur, ahead) : read_codes(next, ahead - KI);
-                if constexpr (j >= kTurn && j < kTurn + KI / 2) {
+    for (int j = 0; j < 3; ++j) queue[j] = read_codes(lds0, j);
+    fc[0] = convert(queue[0]);
+    auto step = [&](auto index) {
+        constexpr int s = decltype(index)::value;
+        uint8_t *const cur = ring(Int<s>{}), *const next = ring(Int<s + 1>{});
+        constexpr int kTurn = KI / 2 - 1;        // the block with the barrier
+        constexpr int kReads = NI / (KI / 2);    // dY fragments read in each of those after
+        for_each<KI>([&](auto block) {
+            constexpr int j = decltype(block)::value;
+            if constexpr (j == kTurn) {
+                // The next tile has arrived (those after it may be on their way)
+                // and the previous one has been read; after the barrier, for all.
+                asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((RING - 3) * LOADS)
+                             : "memory");
+                load_direct(ring(Int<s + RING - 1>{}));
+            }
+            asm volatile("" : "+v"(dy_at), "+v"(code_at));
+            constexpr int ahead = j + 3;
+            queue[ahead & 3] = ahead < KI ? read_codes(cur, ahead) : read_codes(next, ahead - KI);
+            if constexpr (j >= kTurn && j < kTurn + KI / 2) {
 #pragma unroll
-                    for (int i = 0; i < kReads; ++i)
-                        fd[(s + 1) & 1][(j - kTurn) * kReads + i] =
-                            read_dy(next, (j - kTurn) * kReads + i);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-                fc[(j + 1) & 1] = convert(queue[(j + 1) & 3]);
+                for (int i = 0; i < kReads; ++i)
+                    fd[(s + 1) & 1][(j - kTurn) * kReads + i] =
+                        read_dy(next, (j - kTurn) * kReads + i);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            fc[(j + 1) & 1] = convert(queue[(j + 1) & 3]);
 #pragma unroll
-                for (int i = 0; i < NI; ++i)
-                    sum[j][i] = M::run(fc[j & 1], fd[s & 1][i], sum[j][i]);
+            for (int i = 0; i < NI; ++i)
+                sum[j][i] = M::run(fc[j & 1], fd[s & 1][i], sum[j][i]);
 #pragma unroll
-                for (int e = j * 4 * NB / KI; e < (j + 1) * 4 * NB / KI; ++e)
-                    add_columns(fd[s & 1][e / 4], e / 4, e & 3);
-#pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      // MFMA
-                    __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);      // VALU
-                }
-                __builtin_amdgcn_sched_barrier(0);
-            });
-        };
-        // A whole ring at a time, so that every LDS address is a constant; the
-        // tiles past the last row are zero.
-        for (int s = 0; s < steps; s += RING) for_each<RING>(step);
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    } else {
-        load_held(t0);
-        store_held(lds0);
-        load_held(t0 + kDepth);
-        __syncthreads();
-        uint8_t *cur = lds0, *next = lds1;
-        for (int64_t t = t0; t < t1; t += kDepth) {
-            store_held(next);
-            load_held(t + 2 * kDepth);              // nothing past t1
-            typename M::v8 fd[NI];
+            for (int e = j * 4 * NB / KI; e < (j + 1) * 4 * NB / KI; ++e)
+                add_columns(fd[s & 1][e / 4], e / 4, e & 3);
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                fd[i] = read_dy(cur, i);
-                if (i < NB) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) add_columns(fd[i], i, e);
-                }
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      // MFMA
+                __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);      // VALU
             }
-#pragma unroll
-            for (int j = 0; j < KI; ++j) {
-                const typename M::v8 fc = convert(read_codes(cur, j));
-#pragma unroll
-                for (int i = 0; i < NI; ++i) sum[j][i] = M::run(fc, fd[i], sum[j][i]);
-            }
-            // The next tile is in LDS, and this one has been read by all.
-            __syncthreads();
-            uint8_t *const swap = cur;
-            cur = next;
-            next = swap;
-        }
-    }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    // A whole ring at a time, so that every LDS address is a constant; the
+    // tiles past the last row are zero.
+    for (int s = 0; s < steps; s += RING) for_each<RING>(step);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
     // Column sums: a lane holds those of its rows' group g.
 #pragma unroll
@@ -557,6 +490,31 @@ __global__ __launch_bounds__(S::THREADS) void join_kernel(WeightGrad a, Schedule
     if (a.dbias && tile.k == 0 && j == 0 && place.wk == 0 && place.g == 0) a.dbias[n] = db;
 }
 
+// Rows of `width` bytes, `from_pitch` apart at any address, to rows `to_pitch`
+// apart that start on 16-byte boundaries (bytes past the width: zero).
+struct Repack {
+    const char *from;
+    char *to;
+    int64_t from_pitch, to_pitch;
+    int32_t width;
+    int32_t lanes_log2;            // threads to a row
+};
+__global__ __launch_bounds__(256) void repack_kernel(Repack one, Repack two, int64_t rows) {
+    const Repack r = blockIdx.y ? two : one;
+    if (!r.from) return;
+    const int lanes = 1 << r.lanes_log2, lane = threadIdx.x & (lanes - 1);
+    const int per = 256 >> r.lanes_log2;
+    for (int64_t row = (int64_t)blockIdx.x * per + (threadIdx.x >> r.lanes_log2); row < rows;
+         row += (int64_t)gridDim.x * per) {
+        const char *from = r.from + row * r.from_pitch;
+        char *to = r.to + row * r.to_pitch;
+        for (int at = lane * 16; at < r.to_pitch; at += lanes * 16) {
+            const int n = r.width - at;
+            *reinterpret_cast<u4v *>(to + at) = load_tail<true>(from + at, from, n < 16 ? n : 16);
+        }
+    }
+}
+
 // ---------------------------------------------------------------- host ----
 
 using Large = Shape<256, 256, 4, 2, 6>;
@@ -570,23 +528,44 @@ struct Plan {
 
 int64_t up(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
-// Splits of the tiles left over after a whole number for each of `slots`
-// places: the number that takes least time, counting a tile's depth in steps,
-// and what writing, reading and joining a part costs.
+// What a plan's parts cost in microseconds, as measured on an MI355X: a
+// work-group's beginning and end, a step (kDepth rows) of a tile while every
+// place of the GPU has one and where a work-group has its CU to itself, and a
+// part's sums, written, read and joined.
+struct Cost {
+    int places;            // work-groups that run at once
+    double fixed, step, alone, part;
+};
+// A large tile's ring fills a CU's LDS (8192 x 8192x8192: 1024 tiles of 256
+// steps in 875 us); two small ones keep a CU busy (2048 x 2560x2560: 400 tiles
+// of 64 steps in 39 us).
+constexpr Cost kLargeCost = {256, 8.0, 0.82, 0.82, 0.11};
+constexpr Cost kSmallCost = {512, 4.0, 0.55, 0.30, 0.03};
+constexpr double kJoinUs = 4.0;        // the second launch
+
 template <typename S>
-Plan plan_for(int64_t rows, int64_t n, int64_t k, int slots, double step_us, double slab_us,
-              double *us) {
+double groups_us(const Cost &c, int64_t groups, int64_t steps) {
+    steps = up(steps, S::RING) * S::RING;
+    const int64_t left = groups % c.places;
+    return (double)(groups / c.places) * (c.fixed + (double)steps * c.step) +
+           (left == 0 ? 0.0 : c.fixed + (double)steps * (left <= 256 ? c.alone : c.step));
+}
+
+// The tiles left over after a whole number for each place are split along the
+// rows into as many parts as take least time.
+template <typename S>
+Plan plan_for(int64_t rows, int64_t n, int64_t k, const Cost &cost, double *us) {
     Plan p = {};
     p.large = S::BN == 256;
     const int64_t tn = up(n, S::BN), tk = up(k, S::BK), tiles = tn * tk;
-    const int64_t steps = up(rows, kDepth);
-    const int64_t left = tiles % slots;
-    double best = (double)up(tiles, slots) * steps * step_us;
+    const int64_t steps = up(rows, kDepth), left = tiles % cost.places;
+    double best = groups_us<S>(cost, tiles, steps);
     int64_t split = 1;
-    for (int64_t s = 2; left > 0 && s <= 16 && s * 2 <= steps; ++s) {
-        const double t = (double)(tiles / slots) * steps * step_us +
-                         (double)up(left * s, slots) * up(steps, s) * step_us +
-                         (double)(left * s) * slab_us + 4.0;
+    for (int64_t s : {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128}) {
+        if (left == 0 || s * 4 > steps) break;
+        const double t = groups_us<S>(cost, tiles - left, steps) +
+                         groups_us<S>(cost, left * s, up(steps, s)) +
+                         (double)(left * s) * cost.part + kJoinUs;
         if (t < best) best = t, split = s;
     }
     p.schedule.tiles_n = (int32_t)tn;
@@ -601,26 +580,43 @@ Plan plan_for(int64_t rows, int64_t n, int64_t k, int slots, double step_us, dou
 
 Plan plan(int64_t rows, int64_t n, int64_t k) {
     double large_us, small_us;
-    // One large tile fills a CU's LDS; two small ones share it.
-    const Plan large = plan_for<Large>(rows, n, k, 256, 0.6, 0.12, &large_us);
-    const Plan small = plan_for<Small>(rows, n, k, 512, 0.45, 0.03, &small_us);
+    const Plan large = plan_for<Large>(rows, n, k, kLargeCost, &large_us);
+    const Plan small = plan_for<Small>(rows, n, k, kSmallCost, &small_us);
     return large_us <= small_us ? large : small;
 }
 
-int64_t slab_floats(const Plan &p) {
-    return p.split_tiles * p.schedule.split * (p.large ? Large::SLAB : Small::SLAB);
+// Bytes of the parts' sums, and of the operands' copies (0 where the operand
+// can be read as it is), each a multiple of 16.
+struct Workspace {
+    int64_t slabs, dy, codes;
+    int64_t dy_pitch, code_pitch;          // bytes between the copies' rows
+};
+Workspace workspace(const Plan &p, const WeightGrad &a) {
+    Workspace w = {};
+    w.slabs = p.split_tiles * p.schedule.split *
+              (int64_t)(p.large ? Large::SLAB : Small::SLAB) * (int64_t)sizeof(float);
+    // 16-byte loads of whole chunks of a row, 31-bit offsets inside a tile.
+    const bool dy_direct =
+        ((reinterpret_cast<uintptr_t>(a.dy) | (uintptr_t)(a.lddy * 2)) & 15u) == 0 &&
+        a.out_features % 8 == 0 && a.lddy < (INT64_C(1) << 24);
+    const bool codes_direct = ((reinterpret_cast<uintptr_t>(a.codes) | (uintptr_t)a.hidden) & 15u) == 0;
+    if (!dy_direct) {
+        w.dy_pitch = up((int64_t)a.out_features * 2, 16) * 16;
+        w.dy = a.rows * w.dy_pitch;
+    }
+    if (!codes_direct) {
+        w.code_pitch = up(a.hidden, 16) * 16;
+        w.codes = a.rows * w.code_pitch;
+    }
+    return w;
 }
 
 template <typename E, typename S>
 taco_status launch_grad(const WeightGrad &a, const Plan &p, hipStream_t stream) {
-    const bool direct = ((reinterpret_cast<uintptr_t>(a.dy) | (uintptr_t)(a.lddy * 2) |
-                          reinterpret_cast<uintptr_t>(a.codes) | (uintptr_t)a.hidden) & 15u) == 0 &&
-                        a.out_features % 8 == 0 && a.lddy < (INT64_C(1) << 24);
     const int64_t groups = p.schedule.whole + p.split_tiles * p.schedule.split;
-    const taco_status st =
-        launch(direct ? reinterpret_cast<const void *>(&grad_kernel<E, S, true>)
-                      : reinterpret_cast<const void *>(&grad_kernel<E, S, false>),
-               dim3((unsigned)groups), S::THREADS, stream, a, p.schedule, a.workspace);
+    const taco_status st = launch(reinterpret_cast<const void *>(&grad_kernel<E, S>),
+                                  dim3((unsigned)groups), S::THREADS, stream, a, p.schedule,
+                                  a.workspace);
     if (st != TACO_OK || p.split_tiles == 0) return st;
     return launch(reinterpret_cast<const void *>(&join_kernel<E, S>),
                   dim3((unsigned)p.split_tiles, S::NI * S::KI), S::THREADS, stream, a, p.schedule,
@@ -628,15 +624,43 @@ taco_status launch_grad(const WeightGrad &a, const Plan &p, hipStream_t stream) 
 }
 
 template <typename E>
-taco_status run(const WeightGrad &a, hipStream_t stream) {
+taco_status run(WeightGrad a, hipStream_t stream) {
     const Plan p = plan(a.rows, a.out_features, a.hidden);
+    const Workspace w = workspace(p, a);
+    a.ldcodes = a.hidden;
+    if (w.dy || w.codes) {
+        char *const copies = reinterpret_cast<char *>(a.workspace) + w.slabs;
+        auto repack = [&](const void *from, int64_t from_pitch, char *to, int64_t to_pitch,
+                          int32_t width) {
+            int32_t log2 = 0;
+            while (log2 < 8 && (INT64_C(16) << log2) < to_pitch) ++log2;
+            return Repack{static_cast<const char *>(from), to, from_pitch, to_pitch, width, log2};
+        };
+        Repack dy = {}, codes = {};
+        if (w.dy) {
+            dy = repack(a.dy, a.lddy * 2, copies, w.dy_pitch, a.out_features * 2);
+            a.dy = dy.to;
+            a.lddy = w.dy_pitch / 2;
+        }
+        if (w.codes) {
+            codes = repack(a.codes, a.hidden, copies + w.dy, w.code_pitch, a.hidden);
+            a.codes = reinterpret_cast<const uint8_t *>(codes.to);
+            a.ldcodes = w.code_pitch;
+        }
+        const int64_t groups = up((w.dy > w.codes ? w.dy : w.codes) / 16, 256);
+        const taco_status st = launch(reinterpret_cast<const void *>(&repack_kernel),
+                                      dim3((unsigned)(groups < 2048 ? groups : 2048), 2), 256, stream,
+                                      dy, codes, a.rows);
+        if (st != TACO_OK) return st;
+    }
     return p.large ? launch_grad<E, Large>(a, p, stream) : launch_grad<E, Small>(a, p, stream);
 }
 
 }  // namespace
 
-int64_t weight_grad_workspace(int64_t rows, int64_t out_features, int64_t hidden) {
-    return slab_floats(plan(rows, out_features, hidden)) * (int64_t)sizeof(float);
+int64_t weight_grad_workspace(const WeightGrad &a) {
+    const Workspace w = workspace(plan(a.rows, a.out_features, a.hidden), a);
+    return w.slabs + w.dy + w.codes;
 }
 
 taco_status weight_grad(const WeightGrad &a, taco_norm_dtype dtype, hipStream_t stream) {

@@ -61,7 +61,7 @@ _SIGNATURES = {
                             _P, _P, _I64, _P], _STATUS),
     "taco_norm_checkpoint_backward": ([_P, _I64, _P, _P, _P, _I64, _I64, _I32, _I32, _P, _I64, _P,
                                        _P, _P, _I64, _P], _STATUS),
-    "taco_norm_weight_grad_workspace": ([_I64, _I64, _I64], _I64),
+    "taco_norm_weight_grad_workspace": ([_P, _I64, _P, _I64, _I64, _I64], _I64),
     "taco_norm_weight_grad": ([_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _P, _I32, _P, _I32, _I32,
                                _P, _P, _I64, _P], _STATUS),
 }
@@ -362,7 +362,8 @@ def checkpoint_weight_grad(dy, codes, weight=None, bias=None, out=None, dtype=No
     out = at.empty((features, hidden), dtype) if out is None else out
     o = _vector(out, features * hidden, "out", dtype)
     db = at.empty(features, torch.float32) if bias_grad else None
-    ws = at.workspace(_lib.taco_norm_weight_grad_workspace(rows, features, hidden))
+    ws = at.workspace(_lib.taco_norm_weight_grad_workspace(dy.data_ptr(), lddy, c, rows, features,
+                                                           hidden))
     at.call(_lib.taco_norm_weight_grad, "taco_norm_weight_grad", dy.data_ptr(), lddy, c, rows,
             features, hidden, DTYPES[dy.dtype], w, b, DTYPES[ptype], o, DTYPES[dtype],
             int(accumulate), _ptr(db), _ptr(ws), 0 if ws is None else ws.numel())

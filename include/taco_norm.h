@@ -120,9 +120,13 @@ taco_status taco_norm_checkpoint_backward(const void *dy, int64_t lddy, const ui
                                           void *dweight, void *dbias, void *workspace,
                                           int64_t workspace_bytes, hipStream_t stream);
 
-/* Bytes of workspace of taco_norm_weight_grad (0 where it needs none, -1 for
- * a bad shape). */
-int64_t taco_norm_weight_grad_workspace(int64_t rows, int64_t out_features, int64_t hidden);
+/* Bytes of workspace of taco_norm_weight_grad for these operands (0 where it
+ * needs none, -1 for a bad shape).  The pointers are looked at for their
+ * alignment only: an operand whose rows do not all start on 16-byte boundaries
+ * (or, dy, that has a number of columns other than a multiple of 8) is
+ * copied, which takes its size. */
+int64_t taco_norm_weight_grad_workspace(const void *dy, int64_t lddy, const uint8_t *codes,
+                                        int64_t rows, int64_t out_features, int64_t hidden);
 
 /*
  * Weight gradient of z = y W^T (+ a bias) from the checkpoint of y's norm:

@@ -156,7 +156,7 @@ def weight_grad(dy=A, lddy=64, codes=2 * A, rows=4096, features=64, hidden=64, d
                 b=4 * A, pdtype=F32, dw=5 * A, dwtype=BF16, accumulate=0, db=6 * A, ws=7 * A,
                 nbytes=None):
     if nbytes is None:
-        nbytes = norm.taco_norm_weight_grad_workspace(rows, features, hidden)
+        nbytes = norm.taco_norm_weight_grad_workspace(dy, lddy, codes, rows, features, hidden)
     return norm.taco_norm_weight_grad(dy, lddy, codes, rows, features, hidden, dtype, w, b, pdtype,
                                       dw, dwtype, accumulate, db, ws, nbytes, 0)
 
@@ -174,11 +174,23 @@ def test_weight_grad_refusals():
     assert weight_grad(ws=7 * A + 4) == ALIGN and weight_grad(db=6 * A + 2) == ALIGN
     assert weight_grad(dw=A + 64) == ALIAS and weight_grad(db=5 * A) == ALIAS
     assert weight_grad(ws=2 * A) == ALIAS
-    need = norm.taco_norm_weight_grad_workspace(4096, 64, 64)      # one tile, split
+    f = norm.taco_norm_weight_grad_workspace
+    need = f(A, 64, 2 * A, 4096, 64, 64)                           # one tile, split
     assert need > 0 and weight_grad(nbytes=need - 1) == PARAM
     assert weight_grad(rows=4, nbytes=-1) == PARAM                 # needs none
+    assert f(A, 64, 2 * A, 0, 64, 64) == 0 and f(A, 64, 2 * A, 4, 64, 64) == 0
+    assert f(A, 0, 2 * A, 4, 0, 64) == f(A, 64, 2 * A, 4, 64, 0) == -1
+    assert f(A, 64, 2 * A, -1, 64, 64) == f(A, 63, 2 * A, 4, 64, 64) == -1
+
+
+def test_weight_grad_copies_operands_that_are_not_aligned():
     f = norm.taco_norm_weight_grad_workspace
-    assert f(0, 64, 64) == 0 and f(4, 0, 64) == f(4, 64, 0) == f(-1, 64, 64) == -1
+    assert f(A + 2, 64, 2 * A, 4, 64, 64) == 4 * 128               # dy off by an element
+    assert f(A, 65, 2 * A, 4, 64, 64) == 4 * 128                   # its rows
+    assert f(A, 80, 2 * A, 4, 63, 64) == 4 * 128                   # its width
+    assert f(A, 64, 2 * A + 1, 4, 64, 64) == 4 * 64                # codes
+    assert f(A, 64, 2 * A, 4, 64, 40) == 4 * 48
+    assert f(A, 65, 2 * A, 4, 65, 65) == 4 * (144 + 80)
 
 
 def test_torch_layer_refuses_host_tensors():
