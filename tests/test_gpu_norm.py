@@ -392,6 +392,22 @@ def test_weight_grad_holds_every_code(norm):
         assert torch.equal(got, want) and torch.equal(db, torch.full_like(db, 0.5))
 
 
+@pytest.mark.parametrize("dtype", [BF, F16])
+def test_weight_grad_of_subnormal_gradients(norm, dtype):
+    """The smallest values of the type are not flushed to zero."""
+    announce(f"weight grad, subnormal {dtype}")
+    codes = torch.full((256, 16), 0x38, device="cuda", dtype=torch.uint8)          # 1.0
+    dy = torch.zeros(256, 256, device="cuda", dtype=dtype)
+    info = torch.finfo(dtype)
+    value = info.tiny * info.eps * torch.arange(1, 257, device="cuda", dtype=torch.float64)
+    dy.copy_(torch.diag(value))
+    got, db = norm.checkpoint_weight_grad(dy, codes, dtype=F32)
+    want = value / norm.checkpoint_scale(16)
+    # bf16 subnormals are float32 subnormals: exact down to float32's own steps.
+    within(got, want[:, None].expand(256, 16), torch.finfo(F32).tiny * U32 * 2, "dW")
+    within(db, value, torch.finfo(F32).tiny * U32 * 2, "db")
+
+
 def test_weight_grad_nan_stays_in_its_place(norm):
     announce("weight grad, NaN")
     codes, w, b = codes_of(norm, 70, 300, 121)
@@ -529,6 +545,57 @@ def test_norm_linear_autograd(norm, dtype, ptype):
         assert g.shape == r.shape
         # Two roundings to the type (dy and the result), in the 2-norm.
         assert float((g.double() - r).norm() / r.norm()) <= 2 * half_step(dtype), name
+
+
+def test_general_path_equals_the_usual_one(norm):
+    """With a stream given, the calls take the Python path to the C ABI."""
+    announce("general path")
+    for args in (inputs(), inputs(33, 77, 19)):
+        want = all_operators(norm, *args)
+        got = all_operators(norm, *args, stream=torch.cuda.current_stream())
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_refusals_on_the_device(norm):
+    announce("refusals")
+    x = rows_of(4, 64, BF, 171)
+    w, b = params(64, F32, 18)
+    y, codes, rstd = norm.layer_norm_checkpoint(x, w, b)
+    for call in (lambda: norm.layer_norm(x.double()), lambda: norm.layer_norm(x, w[:63]),
+                 lambda: norm.layer_norm(x, w, b.to(BF)), lambda: norm.layer_norm(x[:, ::2]),
+                 lambda: norm.layer_norm(x[:1].expand(4, 64)),
+                 lambda: norm.layer_norm(x, w, b, out=y[:3]),
+                 lambda: norm.layer_norm_backward(y, x, rstd[:3], rstd),
+                 lambda: norm.layer_norm_checkpoint_backward(y, codes[:3], rstd),
+                 lambda: norm.layer_norm_checkpoint_backward(y, codes, rstd, param_dtype=F16),
+                 lambda: norm.checkpoint_weight_grad(x.float(), codes),
+                 lambda: norm.checkpoint_weight_grad(x, codes, accumulate=True),
+                 lambda: norm.checkpoint_weight_grad(x, codes, dtype=F16),
+                 lambda: norm.checkpoint_weight_grad(x, codes, out=torch.empty(64, 63, device="cuda",
+                                                                              dtype=BF))):
+        with pytest.raises((TypeError, ValueError)):
+            call()
+    for call in (lambda: norm.layer_norm(x, w, b, eps=-1.0),
+                 lambda: norm.layer_norm(x, w, b, eps=float("nan")),
+                 lambda: norm.layer_norm(x, out=x),
+                 lambda: norm.layer_norm(torch.empty(4, 0, device="cuda", dtype=BF)),
+                 lambda: norm.layer_norm_backward(y, x, rstd, rstd, dx=x)):
+        with pytest.raises(norm.TacoError):
+            call()
+
+
+def test_example_trains_like_the_usual_layers(norm):
+    announce("example")
+    from gradients_taco_compress_amd import checkpointed_mlp as mlp
+    plain, _ = mlp.train(512, 256, 12, False)
+    ours, _ = mlp.train(512, 256, 12, True)
+    assert ours[-1] < 0.9 * ours[0] and plain[-1] < 0.9 * plain[0]
+    assert abs(ours[-1] - plain[-1]) <= 0.02 * plain[-1]
+    p = mlp.parameters(256, 1024, 0)
+    x = torch.randn(512, 256, device="cuda").to(BF).requires_grad_()
+    # One byte an element and four a row, in the allocator's 512-byte steps.
+    assert mlp.kept_bytes(x, p, True) <= 512 * 256 + 4 * 512 + 1024
+    assert mlp.kept_bytes(x, p, False) >= 4 * 512 * 256
 
 
 def test_norm_linear_keeps_one_byte_per_element(norm):
