@@ -635,17 +635,14 @@ __global__ __launch_bounds__(kWideThreads) void forward_wide_kernel(Forward a) {
         float s = 0.0f;
         for (int i = threadIdx.x; i < a.hidden; i += kWideThreads) s += (float)x[i];
         const float mean = group_sum(s, lds) / n;
+        // Deviations from the mean as it is rounded, which is the one that h is
+        // formed with: the sum of h^2 cannot pass hidden, whatever the rounding.
         s = 0.0f;
-        float e = 0.0f;
         for (int i = threadIdx.x; i < a.hidden; i += kWideThreads) {
             const float d = (float)x[i] - mean;
             s = __builtin_fmaf(d, d, s);
-            e += d;
         }
-        // The mean's own rounding: subtract n (mean of the deviations)^2.
-        const float m2 = group_sum(s, lds);
-        const float off = group_sum(e, lds) / n;
-        const float rstd = 1.0f / sqrtf(m2 / n - off * off + a.eps);
+        const float rstd = 1.0f / sqrtf(group_sum(s, lds) / n + a.eps);
         if (threadIdx.x == 0) {
             if (a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;

@@ -189,6 +189,23 @@ def test_special_rows(norm, hidden):
     assert bad[0][5:].isnan().all() and ((bad[1][5:] & 0x7F) == 0x7F).all()
 
 
+@pytest.mark.parametrize("hidden", [40, 520, 2560, 12288, 16392, 20000, 65537])
+def test_rows_within_their_mean_s_rounding(norm, hidden):
+    """float32 rows whose spread is at or below the rounding of their mean: h
+    is made of rounding alone, yet its squares stay within the row's length,
+    so no code overflows.  An element's squared deviation is at most twice
+    what the merged sums hold of it, hence the factors of 1.5."""
+    announce(f"rows within their mean's rounding {hidden}")
+    values = torch.tensor([3.3, 1e6 / 3, 1e9 / 3, 1e9 / 7, 1e12 / 7, -2.2e9], device="cuda")
+    x = values[:, None].expand(-1, hidden).contiguous()
+    x = torch.cat([x, x])
+    x[6:, hidden // 3] = torch.nextafter(values, values + values.abs())
+    h, codes, rstd = norm.layer_norm_checkpoint(x, None, None)
+    assert rstd.isfinite().all() and ((codes & 0x7F) != 0x7F).all()
+    assert float(h[:6].abs().max()) <= 1.5
+    assert float(h[6:].abs().max()) <= 1.5 * hidden ** 0.5
+
+
 def test_eps_enters(norm):
     x = rows_of(4, 256, F32, 41, 1e-3)
     for eps in (0.0, 1e-12, 1e-2, 3.0):
