@@ -25,10 +25,13 @@
 //    loading such rows through registers instead took 220 us).
 //  * db, the column sums of dY, comes from the same fragments (dot products
 //    with ones), so dY is read by one kernel only.
-//  * Tiles beyond a whole number per CU are split along t and their partial
-//    sums joined, in order, by a second kernel.
+//  * Tiles beyond a whole number per CU are split along t, evenly or into one
+//    share for each CU, and their partial sums joined, in order, by a second
+//    kernel.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <numeric>
 
 #include "taco_norm.h"
 #include "taco_norm_internal.hpp"
@@ -90,12 +93,29 @@ __device__ __forceinline__ int turn_codes(int t) {
 }
 
 // Which output tile and which rows a work-group takes.  The first `whole`
-// work-groups take a tile each; the others share the remaining tiles, `split`
-// to a tile.
+// work-groups take a tile each.  The steps (kDepth rows) of the remaining
+// tiles stand behind one another, `pitch` for each tile, and are cut every
+// `share` steps; where a share goes over into the next tile, its two pieces are
+// work-groups of their own.
 struct Schedule {
     int32_t tiles_n, tiles_k;
-    int32_t whole, split;
-    int64_t slice;             // rows of a split, a multiple of kDepth
+    int32_t whole;
+    int32_t uneven;            // pitch is not a multiple of share
+    int64_t share, pitch;      // pitch >= share
+    // Where the piece of share q in tile t (from the first split one) keeps
+    // its sums.  Consecutive pieces have different q + t.
+    __host__ __device__ __forceinline__ int64_t slab(int64_t t, int64_t q) const {
+        return q + (uneven ? t : 0);
+    }
+};
+// Of uneven pieces, the order in which they start, longest first: a CU that
+// is done early takes a short one next.  An entry is the share, and in the top
+// bit whether it is the share's second piece.  (Small tiles have no uneven
+// plans: the longer arguments alone cost their short launches 0.4 us.)
+template <bool LARGE>
+struct Order {
+    static constexpr int kMost = LARGE ? 512 : 1;
+    uint16_t at[kMost];
 };
 
 struct Tile { int n, k; };
@@ -209,7 +229,7 @@ struct Place {
 
 template <typename E, typename S>
 __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule plan,
-                                                          float *slabs) {
+                                                          float *slabs, Order<S::BN == 256> order) {
     constexpr int BN = S::BN, BK = S::BK, NI = S::NI, KI = S::KI, THREADS = S::THREADS;
     constexpr int DY_BYTES = kDepth * BN * 2, CODE_BYTES = kDepth * BK;
     constexpr int DY_LOADS = DY_BYTES / 16 / THREADS, CODE_LOADS = CODE_BYTES / 16 / THREADS;
@@ -244,11 +264,20 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
         const int xcd = blockIdx.x % 8, q = plan.whole / 8, rem = plan.whole % 8;
         t_index = xcd * q + (xcd < rem ? xcd : rem) + blockIdx.x / 8;
     } else {
-        part = blockIdx.x - plan.whole;
-        t_index = plan.whole + part / plan.split;
-        t0 = (int64_t)(part % plan.split) * plan.slice;
-        t1 = t0 + plan.slice < a.rows ? t0 + plan.slice : a.rows;
-        if (t0 > t1) t0 = t1;
+        int64_t q = blockIdx.x - plan.whole;
+        int second = 0;
+        if (BN == 256 && plan.uneven) {
+            const int piece = order.at[q];
+            second = piece >> 15;
+            q = piece & 0x7FFF;
+        }
+        const int64_t begin = q * plan.share, t = begin / plan.pitch + second;
+        const int64_t from = t * plan.pitch, end = begin + plan.share;
+        t0 = (begin > from ? begin - from : 0) * kDepth;
+        t1 = (end < from + plan.pitch ? end - from : plan.pitch) * kDepth;
+        if (t1 > a.rows) t1 = a.rows;
+        part = (int)plan.slab(t, q);
+        t_index = plan.whole + (int)t;
     }
     const Tile tile = tile_at(plan, t_index);
     const int n0 = tile.n * BN, k0 = tile.k * BK;
@@ -478,10 +507,14 @@ __global__ __launch_bounds__(S::THREADS) void join_kernel(WeightGrad a, Schedule
     const Tile tile = tile_at(plan, plan.whole + blockIdx.x);
     const int n = tile.n * S::BN + place.n(i), k = tile.k * S::BK + place.k(j);
     if (n >= a.out_features || k >= a.hidden) return;
-    const float *p = slabs + (int64_t)blockIdx.x * plan.split * S::SLAB;
+    // The tile's pieces: the shares from the one that its first step is in to
+    // the one that its last is in.
+    const int64_t from = blockIdx.x * plan.pitch;
+    const int64_t first = from / plan.share, last = (from + plan.pitch - 1) / plan.share;
+    const float *p = slabs + plan.slab(blockIdx.x, first) * S::SLAB;
     f4v sum = {0.0f, 0.0f, 0.0f, 0.0f};
     float db = 0.0f;
-    for (int s = 0; s < plan.split; ++s, p += S::SLAB) {
+    for (int64_t q = first; q <= last; ++q, p += S::SLAB) {
         sum += *reinterpret_cast<const f4v *>(p + (blockIdx.y * S::THREADS + threadIdx.x) * 4);
         db += p[S::BN * S::BK + place.n(i)];
     }
@@ -523,23 +556,23 @@ using Small = Shape<128, 128, 2, 2, 4>;
 struct Plan {
     bool large;
     Schedule schedule;
-    int64_t split_tiles;
+    int64_t split_tiles, pieces, slabs;
 };
 
 int64_t up(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
 // What a plan's parts cost in microseconds, as measured on an MI355X: a
 // work-group's beginning and end, a step (kDepth rows) of a tile while every
-// place of the GPU has one and where a work-group has its CU to itself, and a
-// part's sums, written, read and joined.
+// place of the GPU has one and where there are no more work-groups than CUs,
+// and a part's sums, written, read and joined.
 struct Cost {
     int places;            // work-groups that run at once
     double fixed, step, alone, part;
 };
 // A large tile's ring fills a CU's LDS (8192 x 8192x8192: 1024 tiles of 256
-// steps in 875 us); two small ones keep a CU busy (2048 x 2560x2560: 400 tiles
+// steps in 875 us; 16384 x 3584x3584: 196 tiles of 512 in 390 us); two small ones keep a CU busy (2048 x 2560x2560: 400 tiles
 // of 64 steps in 39 us).
-constexpr Cost kLargeCost = {256, 8.0, 0.82, 0.82, 0.11};
+constexpr Cost kLargeCost = {256, 8.0, 0.82, 0.74, 0.11};
 constexpr Cost kSmallCost = {512, 4.0, 0.55, 0.30, 0.03};
 constexpr double kJoinUs = 4.0;        // the second launch
 
@@ -552,7 +585,12 @@ double groups_us(const Cost &c, int64_t groups, int64_t steps) {
 }
 
 // The tiles left over after a whole number for each place are split along the
-// rows into as many parts as take least time.
+// rows: each into the same number of parts, or all of them into one share for
+// each place, whichever takes least time.  Shares against the best equal parts:
+// 8192 x 5120x5120 (144 tiles left) 415 against 431 us, 16384 x 4096x1536 (96
+// tiles) 212 against 228 us, 20000 x 1700x5000 (140) 445 against 462 us; at 196
+// tiles they gain nothing over leaving 60 CUs idle (417 against 400 us), whose
+// power the other CUs turn into clock: Cost::alone.
 template <typename S>
 Plan plan_for(int64_t rows, int64_t n, int64_t k, const Cost &cost, double *us) {
     Plan p = {};
@@ -560,22 +598,67 @@ Plan plan_for(int64_t rows, int64_t n, int64_t k, const Cost &cost, double *us) 
     const int64_t tn = up(n, S::BN), tk = up(k, S::BK), tiles = tn * tk;
     const int64_t steps = up(rows, kDepth), left = tiles % cost.places;
     double best = groups_us<S>(cost, tiles, steps);
-    int64_t split = 1;
-    for (int64_t s : {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128}) {
-        if (left == 0 || s * 4 > steps) break;
-        const double t = groups_us<S>(cost, tiles - left, steps) +
-                         groups_us<S>(cost, left * s, up(steps, s)) +
-                         (double)(left * s) * cost.part + kJoinUs;
-        if (t < best) best = t, split = s;
+    Schedule &s = p.schedule;
+    s.tiles_n = (int32_t)tn;
+    s.tiles_k = (int32_t)tk;
+    auto take = [&](double parts_us, int64_t parts, int64_t share, int64_t pitch, int64_t slabs) {
+        const double t = groups_us<S>(cost, tiles - left, steps) + parts_us +
+                         (double)parts * cost.part + kJoinUs;
+        if (t >= best) return;
+        best = t;
+        s.share = share;
+        s.pitch = pitch;
+        s.uneven = pitch % share != 0;
+        p.split_tiles = left;
+        p.pieces = parts;
+        p.slabs = slabs;
+    };
+    for (int64_t split : {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128}) {
+        if (left == 0 || split * 4 > steps) break;
+        const int64_t share = up(steps, split), parts = up(steps, share);
+        take(groups_us<S>(cost, left * parts, share), left * parts, share, parts * share,
+             left * parts);
     }
-    p.schedule.tiles_n = (int32_t)tn;
-    p.schedule.tiles_k = (int32_t)tk;
-    p.split_tiles = split > 1 ? left : 0;
-    p.schedule.whole = (int32_t)(tiles - p.split_tiles);
-    p.schedule.slice = up(steps, split) * kDepth;
-    p.schedule.split = (int32_t)up(steps, up(steps, split));
+    const int64_t share = up(left * steps, cost.places);
+    if (p.large && share >= 4 && share < steps && steps % share != 0) {
+        // A tile's end inside a share makes two pieces of it.
+        const int64_t shares = up(left * steps, share);
+        const int64_t cuts = left - 1 - (left - 1) / (share / std::gcd(share, steps));
+        take(2 * cost.fixed + (double)(share + S::RING) * cost.step, shares + cuts, share, steps,
+             shares + left);
+    }
+    s.whole = (int32_t)(tiles - p.split_tiles);
     *us = best;
     return p;
+}
+
+// The pieces of an uneven plan, about longest first (by sixty-fourths of a share).
+Order<true> order_of(const Plan &p) {
+    Order<true> order;
+    const Schedule &s = p.schedule;
+    const int64_t total = p.split_tiles * s.pitch;
+    int32_t at[65] = {};
+    for (int pass = 0; pass < 2; ++pass) {
+        for (int64_t q = 0; q * s.share < total; ++q) {
+            const int64_t begin = q * s.share;
+            const int64_t end = begin + s.share < total ? begin + s.share : total;
+            const int64_t cut = (begin / s.pitch + 1) * s.pitch;
+            const int64_t length[2] = {(cut < end ? cut : end) - begin, cut < end ? end - cut : 0};
+            for (int second = 0; second < 2; ++second) {
+                if (length[second] == 0) continue;
+                int32_t &place = at[64 - length[second] * 64 / s.share];
+                if (pass == 0) ++place;
+                else order.at[place++] = (uint16_t)(q | second << 15);
+            }
+        }
+        if (pass == 0)
+            for (int32_t i = 0, sum = 0; i < 65; ++i) {
+                const int32_t count = at[i];
+                at[i] = sum;
+                sum += count;
+            }
+    }
+    return order;
 }
 
 Plan plan(int64_t rows, int64_t n, int64_t k) {
@@ -593,8 +676,7 @@ struct Workspace {
 };
 Workspace workspace(const Plan &p, const WeightGrad &a) {
     Workspace w = {};
-    w.slabs = p.split_tiles * p.schedule.split *
-              (int64_t)(p.large ? Large::SLAB : Small::SLAB) * (int64_t)sizeof(float);
+    w.slabs = p.slabs * (int64_t)(p.large ? Large::SLAB : Small::SLAB) * (int64_t)sizeof(float);
     // 16-byte loads of whole chunks of a row, 31-bit offsets inside a tile.
     const bool dy_direct =
         ((reinterpret_cast<uintptr_t>(a.dy) | (uintptr_t)(a.lddy * 2)) & 15u) == 0 &&
@@ -613,10 +695,14 @@ Workspace workspace(const Plan &p, const WeightGrad &a) {
 
 template <typename E, typename S>
 taco_status launch_grad(const WeightGrad &a, const Plan &p, hipStream_t stream) {
-    const int64_t groups = p.schedule.whole + p.split_tiles * p.schedule.split;
+    static_assert(2 * kLargeCost.places <= Order<true>::kMost, "two pieces of every share");
+    const int64_t groups = p.schedule.whole + p.pieces;
+    Order<S::BN == 256> order = {};
+    if constexpr (S::BN == 256)
+        if (p.schedule.uneven) order = order_of(p);
     const taco_status st = launch(reinterpret_cast<const void *>(&grad_kernel<E, S>),
                                   dim3((unsigned)groups), S::THREADS, stream, a, p.schedule,
-                                  a.workspace);
+                                  a.workspace, order);
     if (st != TACO_OK || p.split_tiles == 0) return st;
     return launch(reinterpret_cast<const void *>(&join_kernel<E, S>),
                   dim3((unsigned)p.split_tiles, S::NI * S::KI), S::THREADS, stream, a, p.schedule,

@@ -385,6 +385,18 @@ def test_weight_grad(norm, rows, features, hidden, dtype):
     check_weight_grad(norm, dy, codes, None, b.float(), dtype=F32, accumulate=True)
 
 
+@pytest.mark.parametrize("rows,features,hidden", [(16999, 411, 5478), (10889, 5475, 809),
+                                                  (16992, 2944, 1824), (6000, 4160, 5664)])
+def test_weight_grad_with_tiles_cut_unevenly(norm, rows, features, hidden):
+    """Long sums over tiles that do not divide among the CUs: 44, 88, 96 and
+    256 + 135 tiles, whose steps are shared out across their borders."""
+    announce(f"weight grad, tiles cut unevenly {rows} {features} {hidden}")
+    codes, w, b = codes_of(norm, rows, hidden, 103)
+    dy = rows_of(rows, features, BF, 104, 0.1)
+    got = check_weight_grad(norm, dy, codes, w, b)
+    assert torch.equal(got, norm.checkpoint_weight_grad(dy, codes, w, b)[0])
+
+
 @pytest.mark.parametrize("pitch,offset", [(8, 0), (5, 0), (0, 1), (16, 8)])
 def test_weight_grad_strides(norm, pitch, offset):
     for rows, features, hidden in ((130, 136, 144), (70, 4096, 2560)):
