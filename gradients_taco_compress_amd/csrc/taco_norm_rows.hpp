@@ -307,27 +307,28 @@ __global__ __launch_bounds__(block_threads<TPR>()) void forward_kernel(Forward a
 
     for (int turn = 0; row < a.rows; row += stride, turn ^= 1) {
         float v[NV][8];
-        float sum = 0.0f;
+        // Four sums each: shorter chains of additions, which round less.
+        float sums[4] = {}, squares[4] = {};
 #pragma unroll
         for (int c = 0; c < NV; ++c)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 v[c][j] = elem<T>(raw[c], j);
-                sum += v[c][j];
+                sums[j & 3] += v[c][j];
             }
         if (row + stride < a.rows) load(row + stride);
 
-        sum = wave_sum<TPR>(sum);
+        float sum = wave_sum<TPR>((sums[0] + sums[1]) + (sums[2] + sums[3]));
         const float mean_wave = sum * inv_n_wave;
-        float m2 = 0.0f;
 #pragma unroll
         for (int c = 0; c < NV; ++c)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float d = v[c][j] - mean_wave;
-                if (WHOLE ? len[c] > 0 : j < len[c]) m2 = __builtin_fmaf(d, d, m2);
+                if (WHOLE ? len[c] > 0 : j < len[c])
+                    squares[j & 3] = __builtin_fmaf(d, d, squares[j & 3]);
             }
-        m2 = wave_sum<TPR>(m2);
+        float m2 = wave_sum<TPR>((squares[0] + squares[1]) + (squares[2] + squares[3]));
         float mean;
         if constexpr (WPR > 1) {
             // Sum of squared deviations from the row's mean: each wave's from
