@@ -576,11 +576,13 @@ struct Cost {
     double fixed, step, alone, part;
 };
 // A large tile's ring fills a CU's LDS (8192 x 8192x8192: 1024 tiles of 256
-// steps in 875 us; 16384 x 3584x3584: 196 tiles of 512 in 390 us); two small ones keep a CU busy (2048 x 2560x2560: 400 tiles
-// of 64 steps in 39 us).
+// steps in 875 us; 16384 x 3584x3584: 196 tiles of 512 in 390 us).  Two small ones
+// keep a CU busy (2048 x 2560x2560: 400 tiles of 64 steps in 39 us; one to a CU,
+// 8192 x 512x512: 16 tiles of 256 steps in 91 us).
 constexpr Cost kLargeCost = {256, 8.0, 0.82, 0.74, 0.11};
-constexpr Cost kSmallCost = {512, 4.0, 0.55, 0.30, 0.03};
-constexpr double kJoinUs = 4.0;        // the second launch
+constexpr Cost kSmallCost = {512, 5.5, 0.56, 0.335, 0.01};
+// The second launch, and each part that a thread of it adds up.
+constexpr double kJoinUs = 5.0, kJoinPartUs = 0.3;
 
 template <typename S>
 double groups_us(const Cost &c, int64_t groups, int64_t steps) {
@@ -609,7 +611,8 @@ Plan plan_for(int64_t rows, int64_t n, int64_t k, const Cost &cost, double *us) 
     s.tiles_k = (int32_t)tk;
     auto take = [&](double parts_us, int64_t parts, int64_t share, int64_t pitch, int64_t slabs) {
         const double t = groups_us<S>(cost, tiles - left, steps) + parts_us +
-                         (double)parts * cost.part + kJoinUs;
+                         (double)parts * cost.part + kJoinUs +
+                         (double)up(steps, share) * kJoinPartUs;
         if (t >= best) return;
         best = t;
         s.share = share;
