@@ -37,6 +37,8 @@ namespace taco_norm {
 namespace {
 
 typedef float f2v __attribute__((ext_vector_type(2)));
+typedef float f4v __attribute__((ext_vector_type(4)));
+
 // ------------------------------------------------------------ elements ----
 
 // Eight elements as they sit in memory.
@@ -389,7 +391,7 @@ __global__ __launch_bounds__(block_threads<TPR>()) void backward_kernel(Backward
     constexpr int WPR = TPR / kWave;
     __shared__ float merge[2][WPR > 1 ? WPR : 1][2];
     // Work-groups of several rows add their threads' column sums here.
-    __shared__ float sums[RPB > 1 ? 2 : 1][RPB > 1 ? TPR * NV * 8 : 1];
+    __shared__ f4v sums[RPB > 1 ? 2 : 1][RPB > 1 ? TPR * NV * 2 : 1];
     const int t = threadIdx.x % TPR;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int hidden = a.hidden;
@@ -525,15 +527,12 @@ __global__ __launch_bounds__(block_threads<TPR>()) void backward_kernel(Backward
 #pragma unroll
                 for (int c = 0; c < NV; ++c)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int i = (c * 8 + j) * TPR + t;
-                        if (group == 0) {
-                            sums[0][i] = dw[c][j];
-                            sums[1][i] = db[c][j];
-                        } else {
-                            sums[0][i] += dw[c][j];
-                            sums[1][i] += db[c][j];
-                        }
+                    for (int j = 0; j < 8; j += 4) {
+                        const int i = (c * 2 + j / 4) * TPR + t;
+                        const f4v w4 = {dw[c][j], dw[c][j + 1], dw[c][j + 2], dw[c][j + 3]};
+                        const f4v b4 = {db[c][j], db[c][j + 1], db[c][j + 2], db[c][j + 3]};
+                        sums[0][i] = group == 0 ? w4 : sums[0][i] + w4;
+                        sums[1][i] = group == 0 ? b4 : sums[1][i] + b4;
                     }
             }
             __syncthreads();
@@ -543,8 +542,8 @@ __global__ __launch_bounds__(block_threads<TPR>()) void backward_kernel(Backward
         for (int c = 0; c < NV; ++c)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                dw[c][j] = sums[0][(c * 8 + j) * TPR + t];
-                db[c][j] = sums[1][(c * 8 + j) * TPR + t];
+                dw[c][j] = sums[0][(c * 2 + j / 4) * TPR + t][j % 4];
+                db[c][j] = sums[1][(c * 2 + j / 4) * TPR + t][j % 4];
             }
     }
 #pragma unroll
