@@ -28,6 +28,12 @@
 //  * Tiles beyond a whole number per CU are split along t, evenly or into one
 //    share for each CU, and their partial sums joined, in order, by a second
 //    kernel.
+//
+// Measured, bf16: 32768 x 1536x12288 990 us (1250 TFLOP/s), 8192 x 10240x2560
+// 395 us (1090), 2048 x 1024x1024 20 us.  Large products are bound by the matrix
+// cores and the power they draw: 57 % of the cycles busy at a clock of 1.7 GHz.
+// Small ones are bound by the latency of a tile's steps on one or two
+// work-groups per CU.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
