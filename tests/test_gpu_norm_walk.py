@@ -1,12 +1,18 @@
-"""The kernels of layer norm where a work-group takes several rows: every forward
-kernel over three turns at least.  What lies between rows is NaN.
+"""The kernels of layer norm where a work-group takes several rows: every
+forward kernel over three turns at least, and the backward kernels' walk with its
+two rows in flight.
+
+Where a sum over rows is checked, its terms are small whole numbers and powers
+of two, so that float32 holds every partial sum exactly and a lost, doubled or
+misplaced row cannot hide in a tolerance.  What lies between rows is NaN.
 """
 from __future__ import annotations
 
 import pytest
 import torch
 
-from test_gpu_norm import BF, F16, F32, announce, check_forward, norm, params, rows_of  # noqa: F401
+from test_gpu_norm import (BF, F16, F32, announce, backward64, check_forward, gen, norm,  # noqa: F401
+                           params, rounding, rows_of, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +57,72 @@ def test_forward_where_its_kernel_changes(norm, rows, hidden, dtype, ptype):  # 
     announce(f"forward {rows}x{hidden} {dtype} {ptype}")
     w, b = params(hidden, ptype, 3)
     check_forward(norm, rows_of(rows, hidden, dtype, 11), w, b)
+
+
+# -------------------------------------------------------------- backward --
+
+BACKWARD = [40, 77, 128, 136, 500, 512, 1001, 1024, 1111, 2048, 2571, 4096, 6001, 6144, 8191, 8192,
+            12287, 12288, 16383, 16384, 16400]
+LONG = [(41000, 96), (33000, 1001), (8500, 2560), (8500, 4096)]        # parts of 512 work-groups
+
+
+def several_turns(hidden):
+    """Rows for five and a half turns of the backward pass's work-groups."""
+    per = 16 if hidden <= 128 else 4 if hidden <= 1024 else 1
+    return 5 * 256 * per + 128 * per + 3
+
+
+def whole(rows, hidden, dtype, seed, values):
+    """[rows, hidden] of the given values, in five columns more of NaN."""
+    at = torch.randint(0, len(values), (rows, hidden), device="cuda", generator=gen(seed))
+    return nan_between(torch.tensor(values, device="cuda")[at].to(dtype))
+
+
+# E4M3 codes of the given numbers.
+CODE_OF = {0.5: 0x30, 1.0: 0x38, 2.0: 0x40, -1.0: 0xB8, -2.0: 0xC0}
+
+
+def codes_and_values(rows, hidden, seed):
+    value = torch.tensor(list(CODE_OF), device="cuda")
+    code = torch.tensor(list(CODE_OF.values()), device="cuda", dtype=torch.uint8)
+    at = torch.randint(0, len(CODE_OF), (rows, hidden), device="cuda", generator=gen(seed))
+    return code[at], value[at]
+
+
+@pytest.mark.parametrize("dtype,ptype", [(BF, F32), (F16, F16), (F32, F32)])
+@pytest.mark.parametrize("rows,hidden", [(several_turns(h), h) for h in BACKWARD] + LONG)
+def test_backward_takes_several_rows(norm, rows, hidden, dtype, ptype):  # noqa: F811
+    """dx within float32's bounds, dw and db exact (float32) or rounded once."""
+    announce(f"backward {rows}x{hidden} {dtype} {ptype}")
+    dy = whole(rows, hidden, dtype, hidden, [-2.0, -1.0, 1.0, 2.0])
+    rstd = torch.empty(rows, device="cuda").uniform_(0.5, 2.0, generator=gen(3))
+    w, _ = params(hidden, ptype, 8)
+
+    def check(got, h, r, what):
+        want, bound = backward64(dy, h, r, w)
+        within(got[0], want[0], bound[0] + rounding(want[0], dtype), f"dx {what}")
+        assert torch.equal(got[1], want[1].to(ptype)), f"dw {what}"
+        assert torch.equal(got[2], want[2].to(ptype)), f"db {what}"
+
+    # h = (x - m) r is whole too, with r = 1.
+    x = whole(rows, hidden, dtype, hidden + 1, [-3.0, -2.0, -1.0, 1.0, 2.0, 4.0])
+    mean = torch.randint(-2, 3, (rows,), device="cuda", generator=gen(4)).float()
+    one = torch.ones(rows, device="cuda")
+    from_x = norm.layer_norm_backward(dy, x, mean, one, w)
+    check(from_x, x.double() - mean.double()[:, None], one, "from x")
+
+    codes, value = codes_and_values(rows, hidden, 5)
+    from_codes = norm.layer_norm_checkpoint_backward(dy, codes, rstd, w)
+    check(from_codes, value.double() / norm.checkpoint_scale(hidden), rstd, "from codes")
+
+    # Whole chunks, where the width has them; and dx over dy.
+    check(norm.layer_norm_backward(dy.contiguous(), x.contiguous(), mean, one, w),
+          x.double() - mean.double()[:, None], one, "from x, contiguous")
+    check(norm.layer_norm_checkpoint_backward(dy.contiguous(), codes, rstd, w),
+          value.double() / norm.checkpoint_scale(hidden), rstd, "from codes, contiguous")
+    before = dy.clone()
+    got = norm.layer_norm_checkpoint_backward(dy, codes, rstd, w, dx=dy)
+    assert got[0] is dy and all(torch.equal(a, b) for a, b in zip(got, from_codes))
+    dy.copy_(before)
+    got = norm.layer_norm_backward(dy, x, mean, one, w, dx=dy)
+    assert got[0] is dy and all(torch.equal(a, b) for a, b in zip(got, from_x))
