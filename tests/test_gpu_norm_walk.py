@@ -1,6 +1,6 @@
-"""The kernels of layer norm where a work-group takes several rows: every
-forward kernel over three turns at least, and the backward kernels' walk with its
-two rows in flight.
+"""The kernels of layer norm where a work-group takes several rows or pieces:
+every forward kernel over at least three turns, the backward kernels' walk with
+its two rows in flight, and the cut points of the sums over rows.
 
 Where a sum over rows is checked, its terms are small whole numbers and powers
 of two, so that float32 holds every partial sum exactly and a lost, doubled or
@@ -126,3 +126,37 @@ def test_backward_takes_several_rows(norm, rows, hidden, dtype, ptype):  # noqa:
     dy.copy_(before)
     got = norm.layer_norm_backward(dy, x, mean, one, w, dx=dy)
     assert got[0] is dy and all(torch.equal(a, b) for a, b in zip(got, from_x))
+
+
+# ----------------------------------------------------------- weight grad --
+
+# Rows on both sides of a tile's depth (32), of a ring of small tiles (4 of them)
+# and of large ones (6), over few small tiles, many, and large ones.
+DEPTHS = [1, 31, 32, 33, 63, 64, 65, 127, 128, 129, 191, 192, 193, 383, 384, 385, 639]
+EXACT = ([(r, 40, 48) for r in DEPTHS] + [(r, 300, 261) for r in DEPTHS]
+         + [(r, 4096, 4112) for r in DEPTHS]
+         # Sums split evenly, and shares cut across the tiles' borders.
+         + [(4096, 136, 144), (4099, 1024, 1024), (20001, 40, 33), (32767, 64, 80), (2048, 1024, 1024),
+            (9999, 513, 1000)]
+         + [(16999, 411, 5478), (10889, 5475, 809), (16992, 2944, 1824), (6000, 4160, 5664)])
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("rows,features,hidden", EXACT)
+def test_weight_grad_loses_no_row(norm, rows, features, hidden, dtype):  # noqa: F811
+    announce(f"weight grad {rows} {features} {hidden} {dtype}")
+    codes, value = codes_and_values(rows, hidden, 21)
+    dy = whole(rows, features, dtype, 22, [-2.0, -1.0, 1.0, 2.0])
+    want = (dy.double().t().contiguous() @ value.double()) / norm.checkpoint_scale(hidden)
+    assert float(want.abs().max()) * norm.checkpoint_scale(hidden) < 2 ** 23
+    db = dy.double().sum(0)
+    # Rows on 16-byte boundaries where the width allows, with NaN behind them, and off them.
+    wide = torch.full((rows, (features + 15) // 8 * 8), float("nan"), device="cuda", dtype=dtype)
+    wide[:, :features] = dy
+    for rows_as in (dy, wide[:, :features]):
+        got, got_db = norm.checkpoint_weight_grad(rows_as, codes, dtype=F32)
+        assert torch.equal(got.double(), want) and torch.equal(got_db.double(), db)
+    acc = torch.full((features, hidden), 3.0, device="cuda")
+    norm.checkpoint_weight_grad(wide[:, :features], codes, out=acc, accumulate=True)
+    assert torch.equal(acc.double(), want + 3.0)
+
