@@ -86,6 +86,12 @@ bool vector(const at::Tensor *t, c10::Device dev, int64_t n, ScalarType dtype) {
     return on_device(t, dev) && t->scalar_type() == dtype && t->numel() == n && t->is_contiguous();
 }
 
+// A checkpoint [..., hidden] of `rows` rows.
+bool codes_of(const at::Tensor *t, c10::Device dev, int64_t rows, int64_t hidden) {
+    return vector(t, dev, rows * hidden, at::kByte) && t->dim() > 0 &&
+           t->size(t->dim() - 1) == hidden;
+}
+
 at::Tensor make(at::IntArrayRef sizes, ScalarType dtype, c10::Device dev) {
     return at::Tensor(at::detail::empty_cuda(sizes, dtype, dev, std::nullopt));
 }
@@ -206,7 +212,7 @@ PyObject *backward(PyObject *const *args, Py_ssize_t n, bool checkpoint) {
         const at::Tensor *mean = checkpoint ? nullptr : tensor(args[2]);
         const at::Tensor *rstd = tensor(args[checkpoint ? 2 : 3]);
         RowsOf rx;
-        if (checkpoint ? !vector(saved, in.dev, in.r.rows * in.r.n, at::kByte)
+        if (checkpoint ? !codes_of(saved, in.dev, in.r.rows, in.r.n)
                        : !same_rows(saved, in, &rx) || !vector(mean, in.dev, in.r.rows, at::kFloat))
             return none();
         if (!vector(rstd, in.dev, in.r.rows, at::kFloat)) return none();
@@ -253,7 +259,7 @@ PyObject *checkpoint_weight_grad(PyObject *, PyObject *const *args, Py_ssize_t n
         const at::Tensor *codes = tensor(args[1]);
         if (dtype == at::kFloat || !codes || !codes->defined() || codes->dim() == 0) return none();
         const int64_t hidden = codes->size(codes->dim() - 1);
-        if (!vector(codes, in.dev, in.r.rows * hidden, at::kByte)) return none();
+        if (!codes_of(codes, in.dev, in.r.rows, hidden)) return none();
         ScalarType ptype = dtype;
         bool typed = false;
         const void *w, *b;
@@ -263,7 +269,10 @@ PyObject *checkpoint_weight_grad(PyObject *, PyObject *const *args, Py_ssize_t n
         const bool f32 = args[5] == Py_True, accumulate = args[6] == Py_True;
         const ScalarType dw_type = f32 ? at::kFloat : dtype;
         const at::Tensor *given = tensor(args[4]);
-        if (args[4] != Py_None && !vector(given, in.dev, in.r.n * hidden, dw_type)) return none();
+        if (args[4] != Py_None &&
+            (!vector(given, in.dev, in.r.n * hidden, dw_type) || given->dim() != 2 ||
+             given->size(0) != in.r.n))
+            return none();
         if (accumulate && (!given || !f32)) return none();
         const int64_t bytes = taco_norm_weight_grad_workspace(
             in.t->data_ptr(), in.r.ld, static_cast<const uint8_t *>(codes->data_ptr()), in.r.rows,

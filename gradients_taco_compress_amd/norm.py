@@ -159,6 +159,15 @@ def _vector(t, n, name, dtype=torch.float32):
     return t.data_ptr()
 
 
+def _codes(t, rows, hidden):
+    """Checks a checkpoint [..., hidden] of `rows` rows; returns its device
+    pointer.  (Not by its size alone: a [hidden, rows] tensor has that, too.)"""
+    p = _vector(t, rows * hidden, "codes", torch.uint8)
+    if t.dim() == 0 or t.shape[-1] != hidden:
+        raise ValueError(f"codes must hold rows of {hidden}, got {list(t.shape)}")
+    return p
+
+
 class _Launch:
     """Where a call runs: its stream, and the allocation of what it returns.
 
@@ -261,7 +270,7 @@ def layer_norm_checkpoint(x, weight=None, bias=None, eps: float = 1e-5, out=None
     ldy = _same_rows(out, "out", x.dtype, rows, hidden)
     at.call(_lib.taco_norm_checkpoint, "taco_norm_checkpoint", x.data_ptr(), ldx, rows, hidden,
             DTYPES[x.dtype], w, b, DTYPES[ptype], eps, out.data_ptr(), ldy,
-            _vector(codes, rows * hidden, "codes", torch.uint8), _vector(rstd, rows, "rstd"))
+            _codes(codes, rows, hidden), _vector(rstd, rows, "rstd"))
     return out, codes, rstd
 
 
@@ -314,7 +323,7 @@ def layer_norm_checkpoint_backward(dy, codes, rstd, weight=None, dx=None,
         if done is not None:
             return done
     rows, hidden, lddy = _pitch(dy, "dy")
-    c, r = _vector(codes, rows * hidden, "codes", torch.uint8), _vector(rstd, rows, "rstd")
+    c, r = _codes(codes, rows, hidden), _vector(rstd, rows, "rstd")
     w, ptype = _backward_param(weight, hidden, dy.dtype, param_dtype)
     at = _Launch(stream, (dy, codes, rstd, weight, dx))
     dx, lddx, dw, db, ws = _gradients(at, dy, dx, hidden, ptype, rows, param_grads)
@@ -333,7 +342,7 @@ def checkpoint_weight_grad(dy, codes, weight=None, bias=None, out=None, dtype=No
 
     dy: bf16 or fp16 [..., out_features]; codes [..., hidden].  dW is of
     ``dtype`` (dy's type by default, or float32); with ``accumulate`` it is
-    added to ``out``, a float32 tensor."""
+    added to ``out``, a float32 tensor.  ``out``: [out_features, hidden]."""
     if bias_grad and stream is None:
         result = dtype or (out.dtype if out is not None else None)
         done = _fast.checkpoint_weight_grad(dy, codes, weight, bias, out,
@@ -346,7 +355,7 @@ def checkpoint_weight_grad(dy, codes, weight=None, bias=None, out=None, dtype=No
     if not isinstance(codes, torch.Tensor) or codes.dim() == 0:
         raise TypeError("codes must be a CUDA/HIP torch tensor [..., hidden]")
     hidden = codes.shape[-1]
-    c = _vector(codes, rows * hidden, "codes", torch.uint8)
+    c = _codes(codes, rows, hidden)
     w, b = _param(weight, hidden, dy.dtype, "weight"), _param(bias, hidden, dy.dtype, "bias")
     ptype = _param_type(weight, bias, dy.dtype)
     if accumulate and out is None:
@@ -361,6 +370,8 @@ def checkpoint_weight_grad(dy, codes, weight=None, bias=None, out=None, dtype=No
     at = _Launch(stream, (dy, codes, weight, bias, out))
     out = at.empty((features, hidden), dtype) if out is None else out
     o = _vector(out, features * hidden, "out", dtype)
+    if out.shape != (features, hidden):
+        raise ValueError(f"out must be [{features}, {hidden}], got {list(out.shape)}")
     db = at.empty(features, torch.float32) if bias_grad else None
     ws = at.workspace(_lib.taco_norm_weight_grad_workspace(dy.data_ptr(), lddy, c, rows, features,
                                                            hidden))
