@@ -343,11 +343,13 @@ def checkpoint_weight_grad(dy, codes, weight=None, bias=None, out=None, dtype=No
     dy: bf16 or fp16 [..., out_features]; codes [..., hidden].  dW is of
     ``dtype`` (dy's type by default, or float32); with ``accumulate`` it is
     added to ``out``, a float32 tensor.  ``out``: [out_features, hidden]."""
-    if bias_grad and stream is None:
-        result = dtype or (out.dtype if out is not None else None)
-        done = _fast.checkpoint_weight_grad(dy, codes, weight, bias, out,
-                                            result is torch.float32, bool(accumulate))
-        if done is not None and (result is None or done[0].dtype is result):
+    if dtype is None:
+        dtype = getattr(dy if out is None else out, "dtype", None)
+    # (The fast path writes at once, so it gets no type that is refused below.)
+    if bias_grad and stream is None and dtype in (torch.float32, getattr(dy, "dtype", None)):
+        done = _fast.checkpoint_weight_grad(dy, codes, weight, bias, out, dtype is torch.float32,
+                                            bool(accumulate))
+        if done is not None:
             return done
     rows, features, lddy = _pitch(dy, "dy")
     if dy.dtype == torch.float32:
@@ -360,9 +362,6 @@ def checkpoint_weight_grad(dy, codes, weight=None, bias=None, out=None, dtype=No
     ptype = _param_type(weight, bias, dy.dtype)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    if out is not None:
-        dtype = out.dtype if dtype is None else dtype
-    dtype = dy.dtype if dtype is None else dtype
     if dtype != dy.dtype and dtype != torch.float32:
         raise TypeError(f"dtype must be {dy.dtype} or torch.float32, got {dtype}")
     if accumulate and dtype != torch.float32:

@@ -53,3 +53,21 @@ def test_a_tensor_of_the_right_size_and_the_wrong_shape_is_refused(norm, other_s
     out = torch.zeros(24, 64, device="cuda")
     got, _ = norm.checkpoint_weight_grad(dz.view(2, 3, 24), codes, out=out, stream=stream)
     assert got is out and torch.equal(out, norm.checkpoint_weight_grad(dz, codes, dtype=F32)[0])
+
+
+@pytest.mark.parametrize("dy_type,wanted", [(BF, F16), (F16, BF)])
+def test_a_refused_type_leaves_out_alone(norm, dy_type, wanted):
+    """dtype names a type that dW cannot have: nothing is written or launched."""
+    announce(f"refused type {wanted}")
+    _, codes, _ = norm.layer_norm_checkpoint(randn(6, 64))
+    dz = randn(6, 24, dtype=dy_type)
+    out = torch.full((24, 64), 7.0, device="cuda", dtype=dy_type)
+    with pytest.raises(TypeError, match="dtype must be"):
+        norm.checkpoint_weight_grad(dz, codes, out=out, dtype=wanted)
+    assert bool(out.eq(7.0).all())
+    with pytest.raises(TypeError, match="dtype must be"):
+        norm.checkpoint_weight_grad(dz, codes, dtype=wanted)
+    # out of another type than the one named.
+    with pytest.raises(TypeError, match="out must be"):
+        norm.checkpoint_weight_grad(dz, codes, out=out, dtype=F32)
+    assert bool(out.eq(7.0).all())
