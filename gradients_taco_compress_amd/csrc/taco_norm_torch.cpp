@@ -15,6 +15,7 @@
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "taco_norm.h"
@@ -136,11 +137,12 @@ bool same_rows(const at::Tensor *t, const Input &in, RowsOf *r) {
 PyObject *none() { Py_RETURN_NONE; }
 
 PyObject *wrap(const at::Tensor &t) { return THPVariable_Wrap(t); }
-PyObject *pack(std::array<PyObject *, 3> v) {
-    PyObject *out = PyTuple_New(3);
-    for (int i = 0; i < 3; ++i) {
+template <size_t N>
+PyObject *pack(std::array<PyObject *, N> v) {
+    PyObject *out = PyTuple_New(N);
+    for (size_t i = 0; i < N; ++i) {
         if (!out || !v[i]) {
-            for (int j = i; j < 3; ++j) Py_XDECREF(v[j]);
+            for (size_t j = i; j < N; ++j) Py_XDECREF(v[j]);
             Py_XDECREF(out);
             return nullptr;
         }
@@ -149,15 +151,13 @@ PyObject *pack(std::array<PyObject *, 3> v) {
     return out;
 }
 
-// Runs f, turning a C++ exception (no memory, say) into a Python one.
+// Runs f, turning a C++ exception into the Python one that torch's own calls
+// raise for it (torch.OutOfMemoryError where there is no memory).
 template <typename F>
 PyObject *guarded(F &&f) {
-    try {
-        return f();
-    } catch (const std::exception &e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-        return nullptr;
-    }
+    HANDLE_TH_ERRORS
+    return f();
+    END_HANDLE_TH_ERRORS
 }
 
 // (x, weight, bias, eps)
@@ -191,7 +191,7 @@ PyObject *forward(PyObject *const *args, Py_ssize_t n, bool checkpoint) {
                                     static_cast<float *>(other.data_ptr()),
                                     static_cast<float *>(rstd.data_ptr()), in.stream);
         if (st != TACO_OK) return none();
-        return pack({wrap(y), wrap(other), wrap(rstd)});      // y, mean or codes, rstd
+        return pack<3>({wrap(y), wrap(other), wrap(rstd)});      // y, mean or codes, rstd
     });
 }
 PyObject *layer_norm(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -240,7 +240,7 @@ PyObject *backward(PyObject *const *args, Py_ssize_t n, bool checkpoint) {
                                      in.r.n, in.type.id, pt, dx.data_ptr(), in.r.n, dw.data_ptr(),
                                      db.data_ptr(), ws.data_ptr(), bytes, in.stream);
         if (st != TACO_OK) return none();
-        return pack({wrap(dx), wrap(dw), wrap(db)});
+        return pack<3>({wrap(dx), wrap(dw), wrap(db)});
     });
 }
 PyObject *layer_norm_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -290,12 +290,8 @@ PyObject *checkpoint_weight_grad(PyObject *, PyObject *const *args, Py_ssize_t n
             type_of(dw_type).id, accumulate, static_cast<float *>(db.data_ptr()),
             bytes ? ws.data_ptr() : nullptr, bytes, in.stream);
         if (st != TACO_OK) return none();
-        PyObject *out = PyTuple_New(2);
-        if (!out) return nullptr;
         if (given) Py_INCREF(args[4]);
-        PyTuple_SET_ITEM(out, 0, given ? args[4] : wrap(dw));
-        PyTuple_SET_ITEM(out, 1, wrap(db));
-        return out;
+        return pack<2>({given ? args[4] : wrap(dw), wrap(db)});
     });
 }
 

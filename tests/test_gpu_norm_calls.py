@@ -71,3 +71,13 @@ def test_a_refused_type_leaves_out_alone(norm, dy_type, wanted):
     with pytest.raises(TypeError, match="out must be"):
         norm.checkpoint_weight_grad(dz, codes, out=out, dtype=F32)
     assert bool(out.eq(7.0).all())
+
+
+def test_running_out_of_memory_has_its_own_type(norm):
+    """Callers catch torch.OutOfMemoryError: half a tebibyte of dW is not there."""
+    announce("out of memory")
+    n = 1 << 19
+    dz = torch.zeros(1, n, device="cuda", dtype=BF)
+    codes = torch.zeros(1, n, device="cuda", dtype=torch.uint8)
+    with pytest.raises(torch.OutOfMemoryError):
+        norm.checkpoint_weight_grad(dz, codes)
