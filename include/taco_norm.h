@@ -41,7 +41,8 @@
  *     (FORMAT); sizes and row pitches (SHAPE); eps (PARAM); required
  *     pointers (NULL); alignment (ALIGN); overlaps (ALIAS); workspace size
  *     (PARAM); the launch (HIP).  On an error found by a check nothing is
- *     launched or written.
+ *     launched or written; after a launch that failed (HIP) the outputs are
+ *     unspecified, and a call must not be made again on one that it adds to.
  *   - rows == 0: forward calls are no-ops; gradients of parameters are sums
  *     over no rows, so the backward calls write zeros to them (and the
  *     weight gradient adds nothing when it accumulates).

@@ -2,6 +2,11 @@
 refuses, what a refused call leaves alone, and what it raises."""
 from __future__ import annotations
 
+import os
+import shutil
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -81,3 +86,59 @@ def test_running_out_of_memory_has_its_own_type(norm):
     codes = torch.zeros(1, n, device="cuda", dtype=torch.uint8)
     with pytest.raises(torch.OutOfMemoryError):
         norm.checkpoint_weight_grad(dz, codes)
+
+
+STUB = r"""
+#include <stdint.h>
+int stub_calls = 0;
+#define FAILS(name) int name(void) { ++stub_calls; return 7; }
+FAILS(taco_norm_forward) FAILS(taco_norm_checkpoint) FAILS(taco_norm_backward)
+FAILS(taco_norm_checkpoint_backward) FAILS(taco_norm_weight_grad)
+float taco_norm_checkpoint_scale(int64_t hidden) { (void)hidden; return 1.0f; }
+int64_t taco_norm_backward_workspace(int64_t rows, int64_t hidden) { return 16 + 0 * rows * hidden; }
+int64_t taco_norm_weight_grad_workspace(void) { return 16; }
+"""
+
+CHILD = r"""
+import ctypes
+import torch
+from gradients_taco_compress_amd import norm
+calls = ctypes.c_int.in_dll(norm._lib, "stub_calls")
+x = torch.ones(4, 64, device="cuda", dtype=torch.bfloat16)
+one = torch.ones(4, device="cuda")
+codes = torch.zeros(4, 64, device="cuda", dtype=torch.uint8)
+acc = torch.zeros(64, 64, device="cuda")
+for name, call in (("taco_norm_forward", lambda: norm.layer_norm(x)),
+                   ("taco_norm_checkpoint", lambda: norm.layer_norm_checkpoint(x)),
+                   ("taco_norm_backward", lambda: norm.layer_norm_backward(x, x, one, one)),
+                   ("taco_norm_checkpoint_backward",
+                    lambda: norm.layer_norm_checkpoint_backward(x, codes, one)),
+                   ("taco_norm_weight_grad", lambda: norm.checkpoint_weight_grad(
+                       x, codes, out=acc, accumulate=True))):
+    calls.value = 0
+    try:
+        call()
+        print(name, "returned", flush=True)
+    except norm.TacoError as e:
+        print(name, e.status, calls.value, name in str(e), flush=True)
+"""
+
+
+def test_a_failed_launch_is_reported_and_not_made_again(norm, tmp_path):
+    """A launch that fails may follow one that did not (a gradient that is
+    already added to): the call is over.  The library is a stub here whose calls
+    all report TACO_ERR_HIP and launch nothing."""
+    announce("failed launch")
+    package = tmp_path / "gradients_taco_compress_amd"
+    package.mkdir()
+    for f in os.listdir(norm.PKG):
+        if f.endswith((".py", ".so")) and f != "libtaco_norm.so":
+            shutil.copy(os.path.join(norm.PKG, f), package / f)
+    (tmp_path / "stub.c").write_text(STUB)
+    subprocess.run(["gcc", "-shared", "-fPIC", "-w", "-Wl,-soname,libtaco_norm.so",
+                    str(tmp_path / "stub.c"), "-o", str(package / "libtaco_norm.so")], check=True)
+    out = subprocess.run([sys.executable, "-c", CHILD], cwd=tmp_path, capture_output=True, text=True,
+                         timeout=110, env={**os.environ, "PYTHONPATH": str(tmp_path)})
+    assert out.returncode == 0, out.stderr
+    names = ("forward", "checkpoint", "backward", "checkpoint_backward", "weight_grad")
+    assert out.stdout.split("\n")[:-1] == [f"taco_norm_{n} 7 1 True" for n in names]
