@@ -28,18 +28,25 @@ bool valid_rows(int64_t rows, int64_t width, int64_t ld) {
     return rows == 0 || ld <= kMaxElements / rows;
 }
 
-// A buffer that a call touches.
+// A buffer that a call touches: rows of `width` bytes, `pitch` apart, over
+// `bytes` in all (pitch 0: one row).
 struct Span {
     const void *p;
     int64_t bytes;
+    int64_t width, pitch;
 };
 Span rows_span(const void *p, int64_t rows, int64_t width, int64_t ld, int64_t size) {
-    return {p, rows > 0 ? ((rows - 1) * ld + width) * size : 0};
+    return {p, rows > 0 ? ((rows - 1) * ld + width) * size : 0, width * size, ld * size};
 }
 bool overlap(const Span &a, const Span &b) {
     if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + (uintptr_t)b.bytes && b0 < a0 + (uintptr_t)a.bytes;
+    if (a0 >= b0 + (uintptr_t)b.bytes || b0 >= a0 + (uintptr_t)a.bytes) return false;
+    // Columns of one wider tensor: with one pitch, the rows lie the same in
+    // every stretch of that length.
+    if (a.pitch == 0 || a.pitch != b.pitch) return true;
+    const int64_t pitch = a.pitch, d = (int64_t)(b0 - a0) % pitch, from = d < 0 ? d + pitch : d;
+    return from < a.width || from + b.width > pitch;
 }
 // Whether an output overlaps an input or another output.
 template <int NO, int NI>
@@ -141,8 +148,8 @@ taco_status backward(const void *dy, int64_t lddy, bool checkpoint, const void *
     const Span outs[] = {rows_span(dx, rows, hidden, lddx, e), {dweight, hidden * p},
                          {dbias, hidden * p}, {sums ? workspace : nullptr, need}};
     const Span dy_span = rows_span(dy, rows, hidden, lddy, e);
-    const Span ins[] = {in_place ? Span{nullptr, 0} : dy_span,
-                        {checkpoint ? nullptr : x, rows_span(x, rows, hidden, ldx, e).bytes},
+    const Span ins[] = {in_place ? Span{} : dy_span,
+                        rows_span(checkpoint ? nullptr : x, rows, hidden, ldx, e),
                         {checkpoint ? codes : nullptr, rows * hidden},
                         {checkpoint ? nullptr : mean, rows * 4},
                         {rstd, rows * 4}, {weight, hidden * p}};

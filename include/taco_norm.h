@@ -49,7 +49,9 @@
  *   - NaN and infinities propagate as the formulas say, within their row
  *     (and, for parameter gradients, their column).
  *   - An output may not overlap an input or another output, except that dx
- *     may be dy itself (same pointer and pitch).
+ *     may be dy itself (same pointer and pitch).  Rows of one pitch may lie
+ *     side by side (column slices of one tensor); rows of different pitches
+ *     count as overlapping where the memory from the first to the last does.
  *   - Thread-safe; calls on different streams may overlap if their buffers
  *     (workspaces included) do not.
  */

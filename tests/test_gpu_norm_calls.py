@@ -142,3 +142,25 @@ def test_a_failed_launch_is_reported_and_not_made_again(norm, tmp_path):
     assert out.returncode == 0, out.stderr
     names = ("forward", "checkpoint", "backward", "checkpoint_backward", "weight_grad")
     assert out.stdout.split("\n")[:-1] == [f"taco_norm_{n} 7 1 True" for n in names]
+
+
+# ---------------------------------------------------- slices of one buffer --
+
+def test_interleaved_column_slices_are_apart(norm):
+    """Inputs and outputs side by side in one buffer, no element shared."""
+    announce("column slices of one buffer")
+    rows, hidden = 300, 136
+    buf = randn(rows, 4 * hidden)
+    x, y, dy, dx = (buf[:, i * hidden:(i + 1) * hidden] for i in range(4))
+    dy0 = dy.clone()
+    want = norm.layer_norm(x.contiguous())
+    got = norm.layer_norm(x, out=y)
+    assert got[0] is y and all(torch.equal(a, b) for a, b in zip(got, want))
+    _, mean, rstd = want
+    want = norm.layer_norm_backward(dy0, x.contiguous(), mean, rstd)
+    got = norm.layer_norm_backward(dy, x, mean, rstd, dx=dx)
+    assert got[0] is dx and all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.equal(dy, dy0)
+    for out in (buf[:, hidden // 2:hidden // 2 + hidden], buf[:, 1:1 + hidden], x):
+        with pytest.raises(norm.TacoError, match="ALIAS"):
+            norm.layer_norm(x, out=out)
