@@ -391,12 +391,17 @@ def _even(t):
         return t.contiguous()
 
 
+def _shape(t):
+    return None if t is None else t.shape
+
+
 class _Norm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps):
         y, mean, rstd = layer_norm(_even(x), weight, bias, eps)
         ctx.save_for_backward(x, mean, rstd, weight)
         ctx.bias_type = None if bias is None else bias.dtype
+        ctx.shapes = _shape(weight), _shape(bias)
         return y
 
     @staticmethod
@@ -407,7 +412,8 @@ class _Norm(torch.autograd.Function):
         dx, dw, db = layer_norm_backward(
             _even(dy), _even(x), mean, rstd, weight, param_grads=want_w or want_b,
             param_dtype=ctx.bias_type if weight is None else None)
-        return dx, dw if want_w else None, db if want_b else None, None
+        return (dx, dw.view(ctx.shapes[0]) if want_w else None,
+                db.view(ctx.shapes[1]) if want_b else None, None)
 
 
 class _NormLinear(torch.autograd.Function):
@@ -435,7 +441,8 @@ class _NormLinear(torch.autograd.Function):
             dx, dw, db = layer_norm_checkpoint_backward(
                 dy, codes, rstd, weight, dx=dy, param_grads=need[1] or need[2],
                 param_dtype=None if weight is not None or bias is None else bias.dtype)
-            grads[:3] = [dx, dw if need[1] else None, db if need[2] else None]
+            grads[:3] = [dx, dw.view(weight.shape) if need[1] else None,
+                         db.view(bias.shape) if need[2] else None]
         return tuple(grads)
 
 
@@ -452,4 +459,11 @@ def norm_linear(x, weight, bias, linear_weight, linear_bias=None, eps: float = 1
         raise TypeError(f"x must be bfloat16 or float16, got {x.dtype}")
     if linear_weight.dtype != x.dtype:
         raise TypeError(f"linear_weight must be {x.dtype}, got {linear_weight.dtype}")
+    hidden = x.shape[-1] if x.dim() else 0
+    if linear_weight.dim() != 2 or linear_weight.shape[1] != hidden:
+        raise ValueError(f"linear_weight must be [out_features, {hidden}], got "
+                         f"{list(linear_weight.shape)}")
+    if linear_bias is not None and linear_bias.shape != linear_weight.shape[:1]:
+        raise ValueError(f"linear_bias must be [{linear_weight.shape[0]}], got "
+                         f"{list(linear_bias.shape)}")
     return _NormLinear.apply(x, weight, bias, linear_weight, linear_bias, eps)

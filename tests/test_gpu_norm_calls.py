@@ -164,3 +164,23 @@ def test_interleaved_column_slices_are_apart(norm):
     for out in (buf[:, hidden // 2:hidden // 2 + hidden], buf[:, 1:1 + hidden], x):
         with pytest.raises(norm.TacoError, match="ALIAS"):
             norm.layer_norm(x, out=out)
+
+
+# --------------------------------------------------------------- autograd --
+
+def test_gradients_have_their_parameter_s_shape(norm):
+    announce("parameter shapes")
+    x, W, c = randn(6, 64), randn(24, 64, seed=1).requires_grad_(), randn(24, seed=2)
+    w = randn(64, dtype=F32, seed=3)
+    for shape in ((64,), (1, 64), (64, 1)):
+        weight, bias = w.view(shape).clone().requires_grad_(), w.view(shape).clone().requires_grad_()
+        for out in (norm.norm(x, weight, bias), norm.norm_linear(x, weight, bias, W)):
+            grads = torch.autograd.grad(out.float().square().sum(), (weight, bias))
+            assert all(g.shape == shape for g in grads)
+    with pytest.raises(ValueError, match="linear_weight"):
+        norm.norm_linear(x, None, None, W[0])
+    with pytest.raises(ValueError, match="linear_weight"):
+        norm.norm_linear(x, None, None, W[:, :32])
+    for bias in (c[:1], c.view(1, 24)):
+        with pytest.raises(ValueError, match="linear_bias"):
+            norm.norm_linear(x, None, None, W, bias)
