@@ -422,7 +422,8 @@ class _NormLinear(torch.autograd.Function):
         y, codes, rstd = layer_norm_checkpoint(_even(x), weight, bias, eps)
         ctx.save_for_backward(codes, rstd, weight, bias, linear_weight)
         ctx.linear_bias_type = None if linear_bias is None else linear_bias.dtype
-        return torch.nn.functional.linear(y, linear_weight, linear_bias)
+        ctx.type = x.dtype
+        return torch.nn.functional.linear(y.to(linear_weight.dtype), linear_weight, linear_bias)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -432,12 +433,15 @@ class _NormLinear(torch.autograd.Function):
         dz = _even(dz)
         grads = [None] * 6
         if need[3] or need[4]:
-            dW, db = checkpoint_weight_grad(dz, codes, weight, bias, dtype=linear_weight.dtype)
+            # The norm's parameters are of the norm's type, dz of the linear layer's.
+            params = [p if p is None or p.dtype == dz.dtype else p.float() for p in (weight, bias)]
+            dW, db = checkpoint_weight_grad(dz, codes, *params, dtype=linear_weight.dtype)
             grads[3] = dW if need[3] else None
             if need[4] and ctx.linear_bias_type is not None:
                 grads[4] = db.to(ctx.linear_bias_type)
         if any(need[:3]):
             dy = torch.mm(dz.reshape(-1, dz.shape[-1]), linear_weight).view(codes.shape)
+            dy = dy.to(ctx.type)
             dx, dw, db = layer_norm_checkpoint_backward(
                 dy, codes, rstd, weight, dx=dy, param_grads=need[1] or need[2],
                 param_dtype=None if weight is not None or bias is None else bias.dtype)
@@ -454,10 +458,21 @@ def norm(x, weight=None, bias=None, eps: float = 1e-5):
 def norm_linear(x, weight, bias, linear_weight, linear_bias=None, eps: float = 1e-5):
     """Differentiable ``linear(layer_norm(x))`` for bf16 and fp16 activations.
     For the backward pass it keeps the 8-bit checkpoint of the normalised
-    rows and one float32 per row, instead of the norm's input and output."""
-    if x.dtype not in (torch.bfloat16, torch.float16):
+    rows and one float32 per row, instead of the norm's input and output.
+
+    x and the linear layer's tensors are of one type.  Under
+    ``torch.autocast`` they need not be, and x may be float32: the norm runs
+    in x's type and the linear layer in autocast's, as torch's own does there."""
+    auto = torch.get_autocast_dtype("cuda") if torch.is_autocast_enabled("cuda") else None
+    if auto in (torch.bfloat16, torch.float16):
+        for t, name in ((x, "x"), (linear_weight, "linear_weight"), (linear_bias, "linear_bias")):
+            if t is not None and t.dtype not in DTYPES:
+                raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+        linear_weight = linear_weight.to(auto)
+        linear_bias = None if linear_bias is None else linear_bias.to(auto)
+    elif x.dtype not in (torch.bfloat16, torch.float16):
         raise TypeError(f"x must be bfloat16 or float16, got {x.dtype}")
-    if linear_weight.dtype != x.dtype:
+    elif linear_weight.dtype != x.dtype:
         raise TypeError(f"linear_weight must be {x.dtype}, got {linear_weight.dtype}")
     hidden = x.shape[-1] if x.dim() else 0
     if linear_weight.dim() != 2 or linear_weight.shape[1] != hidden:

@@ -184,3 +184,61 @@ def test_gradients_have_their_parameter_s_shape(norm):
     for bias in (c[:1], c.view(1, 24)):
         with pytest.raises(ValueError, match="linear_bias"):
             norm.norm_linear(x, None, None, W, bias)
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+@pytest.mark.parametrize("inside", [False, True])
+@pytest.mark.parametrize("dtype,ptype,leaf,auto", [(BF, F32, BF, F16), (BF, BF, F32, F16),
+                                                   (F16, F16, F32, BF), (BF, F32, F32, BF),
+                                                   (F32, F32, F32, BF), (F32, F32, F32, F16)])
+def test_norm_linear_under_autocast(norm, dtype, ptype, leaf, auto, inside):
+    """As torch's own layers there: the norm in its input's type, the linear
+    layer in autocast's, gradients in the leaves' types.  Backward inside and
+    outside of the region.
+
+    Against the formulas in 64 bits with the checkpoint's h and the linear
+    weight as cast.  A result is rounded to autocast's type, to the activation's
+    (dy) and to its leaf's: half a step each, in the 2-norm."""
+    announce(f"autocast {dtype} {leaf} under {auto}, backward {'inside' if inside else 'outside'}")
+    rows, hidden, features = 96, 160, 72
+    x = (randn(4, 24, hidden, dtype=F32, seed=5) * 1.5 + 0.3).to(dtype).requires_grad_()
+    w = (1 + 0.3 * randn(hidden, dtype=F32, seed=6)).to(ptype).requires_grad_()
+    b = randn(hidden, dtype=ptype, seed=7).requires_grad_()
+    W = (0.05 * randn(features, hidden, dtype=F32, seed=8)).to(leaf).requires_grad_()
+    c = randn(features, dtype=leaf, seed=9).requires_grad_()
+    dz = randn(4, 24, features, dtype=auto, seed=10)
+    with torch.autocast("cuda", dtype=auto):
+        z = norm.norm_linear(x, w, b, W, c)
+        assert z.dtype == auto and z.shape == dz.shape
+        if inside:
+            got = torch.autograd.grad(z, (x, w, b, W, c), dz)
+    if not inside:
+        got = torch.autograd.grad(z, (x, w, b, W, c), dz)
+    with torch.no_grad():
+        y, codes, rstd = norm.layer_norm_checkpoint(x, w, b)
+        assert torch.equal(z, torch.nn.functional.linear(y.to(auto), W.to(auto), c.to(auto)))
+        h = codes.view(torch.float8_e4m3fn).double().view(rows, hidden) / norm.checkpoint_scale(hidden)
+        d, r64 = dz.double().view(rows, features), rstd.double()[:, None]
+        g = (d @ W.to(auto).double()) * w.double()
+        dx = r64 * (g - g.mean(1, keepdim=True) - h * (g * h).mean(1, keepdim=True))
+        dy = d @ W.to(auto).double()
+        want = (dx.view(x.shape), (dy * h).sum(0), dy.sum(0),
+                d.t() @ (h * w.double() + b.double()), d.sum(0))
+    for name, leaf_t, a, r in zip("xwbWc", (x, w, b, W, c), got, want):
+        assert a.dtype == leaf_t.dtype and a.shape == leaf_t.shape
+        bound = half_step(auto) + half_step(dtype) + half_step(leaf_t.dtype)
+        assert float((a.double() - r).norm() / r.norm()) <= bound, name
+
+
+def test_norm_linear_without_autocast_wants_one_type(norm):
+    announce("types without autocast")
+    x, W = randn(6, 64), randn(24, 64, dtype=F32)
+    with pytest.raises(TypeError, match="linear_weight must be"):
+        norm.norm_linear(x, None, None, W)
+    with pytest.raises(TypeError, match="x must be"):
+        norm.norm_linear(x.float(), None, None, W)
+    with torch.autocast("cuda", enabled=False), pytest.raises(TypeError, match="linear_weight must be"):
+        norm.norm_linear(x, None, None, W)
