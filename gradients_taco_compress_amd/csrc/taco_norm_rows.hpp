@@ -718,12 +718,24 @@ __global__ __launch_bounds__(256) void params_wide_kernel(Backward a) {
 // as it can hold it (no barrier, and the parameters are loaded once for many
 // rows); measured at 16384x3584, a wave of 7 chunks 43 us, 256 threads of 2
 // 45-49 us, and at 8192x2560 17.5 against 21.5 us.  Few rows cannot fill the
-// GPU anyway, and a row is done sooner by four waves (one row of 2560: 3.2
-// against 4.2 us; 1001x1111: 5.6 against 6.9 us).
+// GPU anyway, and a row is done sooner by four waves: up to 1024 rows, or 512
+// where a quarter or more of their threads would be idle, which costs a 16-bit
+// row of whole chunks more than it gains.  Four waves against one, in us:
+//     bf16, 1 row of 2560                     2.9 and 3.5
+//     bf16, 512 / 768 / 1024 x 1536           3.8, 4.2, 4.5 and 3.4, 3.5, 3.7
+//     the same with codes                     3.5, 4.0, 4.4 and 3.5, 3.7, 3.9
+//     bf16, 512 / 768 / 1024 x 2560           4.3, 4.8, 5.3 and 4.2, 4.3, 4.6
+//     bf16, 512 / 768 / 1024 x 2048           3.9, 4.4, 5.0 and 4.3, 4.5, 4.7
+//     bf16, 512 / 1024 / 2048 x 4096          4.8, 6.2, 9.4 and 6.3, 6.9, 9.5
+//     float32, 512 / 1024 / 2048 x 2560       5.2, 7.0, 11.0 and 5.8, 6.9, 11.6
+//     bf16, ragged, 512 / 1024 / 2048 x 1535  4.2, 6.1, 9.5 and 4.7, 6.0, 7.8
+// (ragged with codes, 1024x1111: 6.2 and 6.8).
 template <typename F>
 taco_status for_forward_width(int64_t rows, int hidden, F &&f) {
     const int chunks = (hidden + 7) / 8;
-    if (rows <= 1024 && chunks > 64) {
+    const bool idle = chunks <= 192 || (chunks > 256 && chunks <= 320);
+    const int64_t few = f.size == 2 && f.whole && idle ? 512 : 1024;
+    if (rows <= few && chunks > 64) {
         if (chunks <= 256) return f.template run<256, 1>();
         if (chunks <= 512) return f.template run<256, 2>();
     }
@@ -770,6 +782,7 @@ inline unsigned grid_rows(int64_t rows, int rows_per_group, int64_t most) {
 
 template <typename T>
 struct ForwardLaunch {
+    static constexpr int size = sizeof(T);
     Forward a;
     hipStream_t stream;
     bool whole;

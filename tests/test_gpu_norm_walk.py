@@ -52,7 +52,7 @@ def test_forward_takes_several_rows(norm, flight, hidden, dtype, ptype):  # noqa
 
 @pytest.mark.parametrize("dtype,ptype", TYPES)
 @pytest.mark.parametrize("hidden", [520, 1111, 2560, 4096])
-@pytest.mark.parametrize("rows", [1024, 1025])
+@pytest.mark.parametrize("rows", [512, 513, 1024, 1025])
 def test_forward_where_its_kernel_changes(norm, rows, hidden, dtype, ptype):  # noqa: F811
     announce(f"forward {rows}x{hidden} {dtype} {ptype}")
     w, b = params(hidden, ptype, 3)
