@@ -53,8 +53,15 @@ inline int rows_per_group(int64_t hidden) { return hidden <= 128 ? 16 : hidden <
 // work-groups finish their rows sooner but leave more to write and add up:
 // half as many as turns of rows, at most one to a CU (777x2560: 256 parts
 // 11.1 us, 512 14.5 us; 256x2560: 128 parts 7.7 us, 256 9.1 us), and two only
-// for long sums over narrow rows (8192x2560: 512 parts 29.8 us, 256 33.9 us;
-// 8192x8192: 67.9 and 60.4 us).
+// for long sums over narrow rows.  256 and 512 parts, from x, in us:
+//     bf16     2048 / 4096 / 8192 x 1536  11.7, 17.1, 27.5 and 12.6, 16.2, 23.2
+//     bf16     2048 / 4096 / 8192 x 2560  15.3, 23.3, 36.7 and 16.8, 23.0, 32.2
+//     bf16     2048 / 8192 / 16384 x 4096 18.5, 41.7, 74.3 and 22.6, 45.5, 78.4
+//     float32  2048 / 8192 / 16384 x 2560 19.8, 57.3, 108.3 and 21.8, 57.2, 107.7
+//     float32  2048 / 8192 / 16384 x 4096 27.2, 82.3, 160.4 and 31.5, 84.5, 158.2
+// So the rule is not the best one everywhere: bf16 rows of up to 2560 columns
+// would gain from 512 parts from about 4096 turns on (up to 15 % at 8191), and
+// bf16 rows of 4096 columns lose 5 to 9 % by them.
 inline int64_t backward_parts(int64_t rows, int64_t hidden) {
     if (hidden > kMaxHeld) return rows < 64 ? rows : 64;
     const int per = rows_per_group(hidden);

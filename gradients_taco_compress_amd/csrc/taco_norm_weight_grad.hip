@@ -21,19 +21,20 @@
 //    and one barrier per tile serves both ends of the ring: the next tile has
 //    arrived, and the one before the current has been read, by all waves.
 //    Operands whose rows do not start on 16-byte boundaries are first copied
-//    to where they do (measured at 8191x2555x2559: the copies 25 us of 150 us;
-//    loading such rows through registers instead took 220 us).
+//    to where they do (measured at 8191 x 2555x2559: 145 us in all, of which the
+//    copies take 25 us; loading such rows through registers instead took 220 us).
 //  * db, the column sums of dY, comes from the same fragments (dot products
 //    with ones), so dY is read by one kernel only.
 //  * Tiles beyond a whole number per CU are split along t, evenly or into one
 //    share for each CU, and their partial sums joined, in order, by a second
 //    kernel.
 //
-// Measured, bf16: 32768 x 1536x12288 990 us (1250 TFLOP/s), 8192 x 10240x2560
-// 395 us (1090), 2048 x 1024x1024 20 us.  Large products are bound by the matrix
-// cores and the power they draw: 57 % of the cycles busy at a clock of 1.7 GHz.
-// Small ones are bound by the latency of a tile's steps on one or two
-// work-groups per CU.
+// Measured, bf16, by card and run: 32768 x 1536x12288 960-1060 us (1170-1290
+// TFLOP/s), 8192 x 10240x2560 386-417 us (1030-1110), 2048 x 1024x1024 20-21 us.
+// Large products are bound by the matrix cores and the power they draw: 57 % of
+// the cycles busy at a clock of 1.7 GHz.  Small ones are bound by the latency of
+// a tile's loads: one work-group to a CU asks for a tile two steps before it
+// needs it, and a step then takes 0.335 us, its products about 0.11 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -252,8 +253,8 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
     // knows that a load into one does not touch the fragments being read from
     // another, and does not wait for it.
     constexpr int TILE = DY_BYTES + CODE_BYTES, RING = S::RING;
-    __shared__ __align__(1024) uint8_t lds0[TILE], lds1[TILE], lds2[RING > 2 ? TILE : 1],
-        lds3[RING > 3 ? TILE : 1], lds4[RING > 4 ? TILE : 1], lds5[RING > 5 ? TILE : 1];
+    __shared__ __align__(1024) uint8_t lds0[TILE], lds1[TILE], lds2[TILE], lds3[TILE],
+        lds4[RING > 4 ? TILE : 1], lds5[RING > 5 ? TILE : 1];
     auto ring = [&](auto index) -> uint8_t * {
         constexpr int i = decltype(index)::value % RING;
         if constexpr (i == 0) return lds0;
@@ -308,10 +309,11 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
         return 16 * (((i * THREADS + tid) % CODE_CHUNKS) ^ turn_codes<BK>(code_row(i)));
     };
 
-    // Straight to LDS: rows past t1 are out of the resource's bounds, which
+    // Loads go straight to LDS: rows past t1 are out of the resource's bounds, which
     // makes them zero; a chunk past the last column reads the tile's first one
     // instead (its sums are never stored).  A tile's offsets from its first
-    // element fit 31 bits (the launcher sees to it).
+    // element fit 31 bits (the launcher sees to it).  (What only the loads use is
+    // unused in the host pass.)
     static_assert(DY_LOADS == 2 && CODE_LOADS == 1, "loads of a tile");
     [[maybe_unused]] uint32_t dy_off[2], code_off;
 #pragma unroll
@@ -330,7 +332,7 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
     [[maybe_unused]] const int last_rows =
         __builtin_amdgcn_readfirstlane((int)(t1 - t0 - (int64_t)(steps - 1) * kDepth));
     [[maybe_unused]] const int dy_pitch = (int)a.lddy * 2;
-    auto load_direct = [&](uint8_t *buf) {
+    auto load_tile = [&](uint8_t *buf) {
 #if defined(__HIP_DEVICE_COMPILE__)      // the host pass does not know the resource type
         // Rows of this tile (none past the last tile).  Every column read exists,
         // so the bounds need to be right for whole rows only.
@@ -413,7 +415,7 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
     // fragments read three products ahead, and two converted ones.
     typename M::v8 fd[2][NI], fc[2];
     i2v queue[4];
-    for_each<RING - 1>([&](auto i) { load_direct(ring(i)); });
+    for_each<RING - 1>([&](auto i) { load_tile(ring(i)); });
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((RING - 2) * LOADS) : "memory");
 #pragma unroll
     for (int i = 0; i < NI; ++i) fd[0][i] = read_dy(lds0, i);
@@ -432,7 +434,7 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(WeightGrad a, Schedule
                 // and the previous one has been read; after the barrier, for all.
                 asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((RING - 3) * LOADS)
                              : "memory");
-                load_direct(ring(Int<s + RING - 1>{}));
+                load_tile(ring(Int<s + RING - 1>{}));
             }
             asm volatile("" : "+v"(dy_at), "+v"(code_at));
             constexpr int ahead = j + 3;

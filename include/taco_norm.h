@@ -36,7 +36,9 @@
  *   - Any alignment of the elements' own size is accepted; rows that start
  *     on 16-byte boundaries (8-byte for codes) are read and written faster.
  *   - Statistics and every sum are float32; results are rounded once, to
- *     nearest even.  Results do not depend on timing: no atomics.
+ *     nearest even.  Results do not depend on timing: no atomics.  A row's
+ *     squared deviations have to fit float32: beyond 3e38 they overflow, and
+ *     with eps = 0 those below 1e-38 are lost.
  *   - Calls are asynchronous on `stream`.  Checks run in this order: types
  *     (FORMAT); sizes and row pitches (SHAPE); eps (PARAM); required
  *     pointers (NULL); alignment (ALIGN); overlaps (ALIAS); workspace size
@@ -145,9 +147,12 @@ int64_t taco_norm_weight_grad_workspace(const void *dy, int64_t lddy, const uint
  *   dbias     [out_features] float32 output db, may be NULL.
  *   workspace as above, taco_norm_weight_grad_workspace bytes (NULL where
  *             that is 0).
- * A product of a code and a bf16 or fp16 value is exact in float32, and the
- * sums are float32: the gradient of the checkpointed tensor has no rounding
- * before the last.
+ * Both operands enter unrounded: a code times a bf16 or fp16 value is exact in
+ * float32.  The sums over the rows, their joining, the scaling by w_k / S, the
+ * bias term and the accumulation round in float32 (an element is off by less
+ * than (rows + 24) 2^-24 of the sum of its terms' magnitudes), and the result
+ * once to dw_dtype.  The sums are those of dy times S h, S up to 256: dy near
+ * float32's largest values (bf16's beyond 10^35) may overflow them.
  */
 taco_status taco_norm_weight_grad(const void *dy, int64_t lddy, const uint8_t *codes,
                                   int64_t rows, int64_t out_features, int64_t hidden,
