@@ -29,8 +29,8 @@
 //    share for each CU, and their partial sums joined, in order, by a second
 //    kernel.
 //
-// Measured, bf16, by card and run: 32768 x 1536x12288 960-1060 us (1170-1290
-// TFLOP/s), 8192 x 10240x2560 386-417 us (1030-1110), 2048 x 1024x1024 20-21 us.
+// Measured, bf16, by card and run: 32768 x 1536x12288 958-1073 us (1150-1290
+// TFLOP/s), 8192 x 10240x2560 386-420 us (1020-1110), 2048 x 1024x1024 20-21 us.
 // Large products are bound by the matrix cores and the power they draw: 57 % of
 // the cycles busy at a clock of 1.7 GHz.  Small ones are bound by the latency of
 // a tile's loads: one work-group to a CU asks for a tile two steps before it
