@@ -1,4 +1,5 @@
-"""Build libtaco.so, libtaco_probe.so and libtaco_norm.so in-tree with hipcc for gfx950.
+"""Build libtaco.so, libtaco_probe.so, libtaco_norm.so and libtaco_gated.so in-tree with
+hipcc for gfx950.
 
     python gradients_taco_compress_amd/build.py
     TACO_HIPCC_FLAGS="-DTACO_WAVES_PER_GROUP=8" python gradients_taco_compress_amd/build.py
@@ -43,6 +44,12 @@ NORM_LIB = os.path.join(PKG, "libtaco_norm.so")
 #: Its fast path from torch (host code only), a Python extension module.
 NORM_TORCH_SOURCE = os.path.join(CSRC, "taco_norm_torch.cpp")
 NORM_TORCH = os.path.join(PKG, "_norm_torch.so")
+#: The gated feed-forward block, a library of its own: the C ABI, the matrix
+#: products (one unit per operand type) and the element-wise kernels.
+GATED_SOURCES = [os.path.join(CSRC, f) for f in
+                 ("taco_gated_abi.hip", "taco_gated_bf16.hip", "taco_gated_f16.hip",
+                  "taco_gated_mx.hip", "taco_gated_rows.hip")]
+GATED_LIB = os.path.join(PKG, "libtaco_gated.so")
 CXX = os.environ.get("CXX", "g++")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -132,6 +139,29 @@ def _norm_torch_command(out: str) -> list:
                   "-ltorch_hip", "-ltorch_cpu", "-lc10_hip", "-lc10"]
 
 
+def build_gated(verbose: bool = False) -> str:
+    """Compile GATED_SOURCES (in parallel) and link GATED_LIB; always recompiles.
+    Returns GATED_LIB."""
+    from concurrent.futures import ThreadPoolExecutor
+    tag = f".tmp{os.getpid()}"
+    objs = [src + tag + ".o" for src in GATED_SOURCES]
+    try:
+        with ThreadPoolExecutor(max_workers=len(objs)) as pool:
+            jobs = [pool.submit(_run, [HIPCC, *FLAGS, "-I", os.path.join(ROOT, "include"),
+                                       "-c", src, "-o", obj], verbose)
+                    for src, obj in zip(GATED_SOURCES, objs)]
+            for j in jobs:
+                j.result()
+        _run([HIPCC, "--offload-arch=gfx950", "-shared", "-Wl,-soname,libtaco_gated.so", *objs,
+              "-o", GATED_LIB + tag], verbose)
+        os.replace(GATED_LIB + tag, GATED_LIB)
+    finally:
+        for path in objs + [GATED_LIB + tag]:
+            if os.path.exists(path):
+                os.remove(path)
+    return GATED_LIB
+
+
 def build_norm(verbose: bool = False) -> str:
     """Compile NORM_SOURCES (in parallel), link NORM_LIB and NORM_TORCH;
     always recompiles.  Returns NORM_LIB."""
@@ -160,7 +190,7 @@ def build_norm(verbose: bool = False) -> str:
 if __name__ == "__main__":
     import argparse
     ap = argparse.ArgumentParser(
-        description="Build libtaco (and libtaco_probe, libtaco_norm) for gfx950.")
+        description="Build libtaco (and libtaco_probe, libtaco_norm, libtaco_gated) for gfx950.")
     ap.add_argument("-q", action="store_true", help="quiet")
     ap.add_argument("--out", default=None,
                     help="build only the operator library, to this path")
@@ -168,3 +198,4 @@ if __name__ == "__main__":
     print(build(verbose=not a.q, out=a.out))
     if not a.out:
         print(build_norm(verbose=not a.q))
+        print(build_gated(verbose=not a.q))

@@ -1,0 +1,413 @@
+// libtaco_gated C ABI (declared in include/taco_gated.h): argument validation
+// and dispatch.  Every check runs on the host before anything is launched.
+#include <stdint.h>
+#include <stddef.h>
+#include <hip/hip_runtime.h>
+
+#include "taco_gated.h"
+#include "taco_gated_internal.hpp"
+
+using namespace taco_gated;
+
+namespace {
+
+constexpr int64_t kSize = 2;           // bytes of an element
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+int64_t round_up(int64_t n, int64_t d) { return (n + d - 1) / d * d; }
+
+// Largest tensor extent accepted, in elements: byte sizes stay far inside 64
+// bits, and the largest launch inside a grid's 2^32 threads.
+constexpr int64_t kMaxElements = INT64_C(1) << 48;
+constexpr int64_t kMaxProduct = INT64_C(1) << 37;
+
+bool valid_width(int64_t n) { return n > 0 && n <= TACO_GATED_MAX_WIDTH; }
+bool valid_rows(int64_t rows, int64_t width, int64_t ld) {
+    if (rows < 0 || width <= 0 || ld < width) return false;
+    return rows == 0 || ld <= kMaxElements / rows;
+}
+bool valid_sizes(int64_t rows, int64_t hidden, int64_t features) {
+    if (rows < 0 || !valid_width(hidden) || !valid_width(features)) return false;
+    const int64_t wide = hidden > features ? hidden : features;
+    return rows <= kMaxProduct / wide && hidden <= kMaxProduct / features;
+}
+bool valid(taco_gated_activation a) {
+    return a == TACO_GATED_SILU || a == TACO_GATED_GELU || a == TACO_GATED_GELU_TANH;
+}
+bool valid(taco_norm_dtype d) { return d == TACO_NORM_BF16 || d == TACO_NORM_F16; }
+
+// A buffer that a call touches: rows of `width` bytes, `pitch` apart, over
+// `bytes` in all (pitch 0: one row).
+struct Span {
+    const void *p;
+    int64_t bytes;
+    int64_t width, pitch;
+};
+Span rows_span(const void *p, int64_t rows, int64_t width, int64_t ld) {
+    return {p, rows > 0 ? ((rows - 1) * ld + width) * kSize : 0, width * kSize, ld * kSize};
+}
+bool overlap(const Span &a, const Span &b) {
+    if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+    if (a0 >= b0 + (uintptr_t)b.bytes || b0 >= a0 + (uintptr_t)a.bytes) return false;
+    // Columns of one wider tensor: with one pitch, the rows lie the same in
+    // every stretch of that length.
+    if (a.pitch == 0 || a.pitch != b.pitch) return true;
+    const int64_t pitch = a.pitch, d = (int64_t)(b0 - a0) % pitch, from = d < 0 ? d + pitch : d;
+    return from < a.width || from + b.width > pitch;
+}
+template <int NO, int NI>
+bool any_overlap(const Span (&outs)[NO], const Span (&ins)[NI]) {
+    for (int o = 0; o < NO; ++o) {
+        for (int i = 0; i < NI; ++i)
+            if (overlap(outs[o], ins[i])) return true;
+        for (int i = 0; i < o; ++i)
+            if (overlap(outs[o], outs[i])) return true;
+    }
+    return false;
+}
+
+// An operand [rows, width]: as it is, or as a copy in the workspace whose rows
+// start on 16-byte boundaries.
+struct Operand {
+    const void *p;
+    int64_t ld, rows, width;
+    bool copied;
+    int64_t copy_pitch() const { return round_up(width * kSize, 16); }
+    int64_t copy_bytes() const { return copied ? rows * copy_pitch() : 0; }
+    int64_t pitch() const { return copied ? copy_pitch() : ld * kSize; }
+};
+Operand operand(const void *p, int64_t ld, int64_t rows, int64_t width) {
+    const bool direct = aligned(p, 16) && (ld * kSize) % 16 == 0 && width % 8 == 0 &&
+                        ld * kSize <= kMaxPitch;
+    return {p, ld, rows, width, !direct};
+}
+// Two weights that one kernel reads with one pitch.
+void alike(Operand *a, Operand *b) {
+    if (a->pitch() != b->pitch() || a->copied != b->copied) a->copied = b->copied = true;
+}
+
+// Takes pieces of the workspace, in order, and queues the copies.
+struct Arena {
+    char *at;
+    Repack copies[3];
+    int count;
+    void *take(int64_t bytes) {
+        void *const p = at;
+        at += round_up(bytes, 16);
+        return p;
+    }
+    Matrix place(const Operand &o) {
+        if (!o.copied) return {o.p, o.pitch()};
+        void *const to = take(o.copy_bytes());
+        copies[count++] = {o.p, to, o.ld * kSize, o.copy_pitch(), o.rows, o.width * kSize};
+        return {to, o.copy_pitch()};
+    }
+    taco_status copy(hipStream_t stream) const {
+        return count ? repack(copies, count, stream) : TACO_OK;
+    }
+};
+
+template <typename F>
+taco_status with_type(taco_norm_dtype dtype, F &&f) {
+    return dtype == TACO_NORM_BF16 ? f(Products<BF16>{}) : f(Products<F16>{});
+}
+
+// (A plan depends on the sizes only, not on which 16-bit type it is.)
+int64_t slabs(Kind kind, int64_t m, int64_t n, int64_t k) {
+    Product p = {};
+    p.m = m; p.n = n; p.k = k;
+    return Products<BF16>::workspace(kind, p);
+}
+
+struct ForwardOperands {
+    Operand x, gate, up;
+    int64_t slab_bytes, bytes;
+};
+ForwardOperands forward_operands(const void *x, int64_t ldx, const void *gate, int64_t ldg,
+                                 const void *up, int64_t ldu, int64_t rows, int64_t hidden,
+                                 int64_t features) {
+    ForwardOperands o = {operand(x, ldx, rows, hidden), operand(gate, ldg, features, hidden),
+                         operand(up, ldu, features, hidden), 0, 0};
+    if (rows <= kFewRows) return o;
+    alike(&o.gate, &o.up);
+    o.slab_bytes = slabs(Kind::kForward, rows, features, hidden);
+    o.bytes = o.slab_bytes + o.x.copy_bytes() + o.gate.copy_bytes() + o.up.copy_bytes();
+    return o;
+}
+
+struct BackwardOperands {
+    Operand x, gate, up;
+    int64_t slab_bytes, d_pitch, bytes;       // d_pitch: of dG and dU, in elements
+};
+BackwardOperands backward_operands(const void *x, int64_t ldx, const void *gate, int64_t ldg,
+                                   const void *up, int64_t ldu, int64_t rows, int64_t hidden,
+                                   int64_t features, bool want_dx, bool want_dw) {
+    BackwardOperands o = {operand(x, ldx, rows, hidden), operand(gate, ldg, features, hidden),
+                          operand(up, ldu, features, hidden), 0, 0, 0};
+    alike(&o.gate, &o.up);
+    o.d_pitch = round_up(features, 8);
+    if (want_dx) {
+        o.slab_bytes = slabs(Kind::kInput, rows, hidden, features);
+        o.bytes += o.gate.copy_bytes() + o.up.copy_bytes();
+    }
+    if (want_dw) {
+        // The two products follow one another and share their partial sums' place.
+        const int64_t more = slabs(Kind::kWeight, features, hidden, rows);
+        o.slab_bytes = more > o.slab_bytes ? more : o.slab_bytes;
+        o.bytes += o.x.copy_bytes();
+    }
+    o.bytes += o.slab_bytes + 2 * rows * o.d_pitch * kSize;
+    return o;
+}
+
+// Scale rows of hidden / 32 bytes, which the kernel reads four at a time.
+struct Scales {
+    const uint8_t *p;
+    int64_t rows, width;
+    bool copied;
+    int64_t copy_bytes() const { return copied ? rows * round_up(width, 16) : 0; }
+};
+Scales scales(const uint8_t *p, int64_t rows, int64_t hidden) {
+    const int64_t width = hidden / 32;
+    return {p, rows, width, width % 4 != 0 || !aligned(p, 4)};
+}
+
+bool valid_mx(int64_t rows, int64_t hidden, int64_t features) {
+    return valid_sizes(rows, hidden, features) && hidden % 32 == 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t taco_gated_forward_workspace(const void *x, int64_t ldx, const void *gate_weight,
+                                     int64_t ldg, const void *up_weight, int64_t ldu, int64_t rows,
+                                     int64_t hidden, int64_t features) {
+    if (!valid_sizes(rows, hidden, features) || !valid_rows(rows, hidden, ldx) ||
+        !valid_rows(features, hidden, ldg) || !valid_rows(features, hidden, ldu))
+        return -1;
+    if (rows == 0) return 0;
+    return forward_operands(x, ldx, gate_weight, ldg, up_weight, ldu, rows, hidden, features).bytes;
+}
+
+taco_status taco_gated_forward(const void *x, int64_t ldx, const void *gate_weight, int64_t ldg,
+                               const void *up_weight, int64_t ldu, int64_t rows, int64_t hidden,
+                               int64_t features, taco_norm_dtype dtype,
+                               taco_gated_activation activation, void *a, int64_t lda, void *gate,
+                               void *up, int64_t ldgu, void *workspace, int64_t workspace_bytes,
+                               hipStream_t stream) {
+    if (!valid(dtype)) return TACO_ERR_FORMAT;
+    const bool save = gate || up;
+    if (!valid_sizes(rows, hidden, features) || !valid_rows(rows, hidden, ldx) ||
+        !valid_rows(features, hidden, ldg) || !valid_rows(features, hidden, ldu) ||
+        !valid_rows(rows, features, lda) || (save && !valid_rows(rows, features, ldgu)))
+        return TACO_ERR_SHAPE;
+    if (!valid(activation)) return TACO_ERR_PARAM;
+    if (rows == 0) return TACO_OK;
+    const ForwardOperands o =
+        forward_operands(x, ldx, gate_weight, ldg, up_weight, ldu, rows, hidden, features);
+    if (!x || !gate_weight || !up_weight || !a || (save && (!gate || !up)) ||
+        (o.bytes && !workspace))
+        return TACO_ERR_NULL;
+    if (!aligned(x, 2) || !aligned(gate_weight, 2) || !aligned(up_weight, 2) || !aligned(a, 2) ||
+        !aligned(gate, 2) || !aligned(up, 2) || (o.bytes && !aligned(workspace, 16)))
+        return TACO_ERR_ALIGN;
+    const Span outs[] = {rows_span(a, rows, features, lda), rows_span(gate, rows, features, ldgu),
+                         rows_span(up, rows, features, ldgu), {workspace, o.bytes}};
+    const Span ins[] = {rows_span(x, rows, hidden, ldx), rows_span(gate_weight, features, hidden, ldg),
+                        rows_span(up_weight, features, hidden, ldu)};
+    if (any_overlap(outs, ins)) return TACO_ERR_ALIAS;
+    if (workspace_bytes < o.bytes) return TACO_ERR_PARAM;
+    Product p = {};
+    p.m = rows; p.n = features; p.k = hidden;
+    p.activation = activation;
+    p.out[0] = a; p.out[1] = gate; p.out[2] = up;
+    p.out_pitch[0] = lda; p.out_pitch[1] = p.out_pitch[2] = ldgu;
+    if (rows <= kFewRows) {
+        p.a[0] = {x, ldx * kSize};
+        p.b[0] = {gate_weight, ldg * kSize};
+        p.b[1] = {up_weight, ldu * kSize};
+        return with_type(dtype, [&](auto k) { return decltype(k)::few(p, stream); });
+    }
+    Arena arena = {static_cast<char *>(workspace), {}, 0};
+    p.slabs = static_cast<float *>(arena.take(o.slab_bytes));
+    p.a[0] = p.a[1] = arena.place(o.x);
+    p.b[0] = arena.place(o.gate);
+    p.b[1] = arena.place(o.up);
+    const taco_status st = arena.copy(stream);
+    if (st != TACO_OK) return st;
+    return with_type(dtype, [&](auto k) { return decltype(k)::run(Kind::kForward, p, stream); });
+}
+
+int64_t taco_gated_backward_workspace(const void *x, int64_t ldx, const void *gate_weight,
+                                      int64_t ldg, const void *up_weight, int64_t ldu,
+                                      int64_t rows, int64_t hidden, int64_t features,
+                                      int32_t want_dx, int32_t want_dw) {
+    if (!valid_sizes(rows, hidden, features) || (want_dw && !valid_rows(rows, hidden, ldx)) ||
+        (want_dx && (!valid_rows(features, hidden, ldg) || !valid_rows(features, hidden, ldu))))
+        return -1;
+    if (rows == 0 || (!want_dx && !want_dw)) return 0;
+    return backward_operands(x, ldx, gate_weight, ldg, up_weight, ldu, rows, hidden, features,
+                             want_dx, want_dw).bytes;
+}
+
+taco_status taco_gated_backward(const void *da, int64_t ldda, const void *x, int64_t ldx,
+                                const void *gate, const void *up, int64_t ldgu,
+                                const void *gate_weight, int64_t ldg, const void *up_weight,
+                                int64_t ldu, int64_t rows, int64_t hidden, int64_t features,
+                                taco_norm_dtype dtype, taco_gated_activation activation, void *dx,
+                                int64_t lddx, void *dgate_weight, void *dup_weight,
+                                void *workspace, int64_t workspace_bytes, hipStream_t stream) {
+    if (!valid(dtype)) return TACO_ERR_FORMAT;
+    const bool want_dx = dx, want_dw = dgate_weight || dup_weight;
+    if (!valid_sizes(rows, hidden, features) || !valid_rows(rows, features, ldda) ||
+        !valid_rows(rows, features, ldgu) || (want_dw && !valid_rows(rows, hidden, ldx)) ||
+        (want_dx && (!valid_rows(rows, hidden, lddx) || !valid_rows(features, hidden, ldg) ||
+                     !valid_rows(features, hidden, ldu))))
+        return TACO_ERR_SHAPE;
+    if (!valid(activation)) return TACO_ERR_PARAM;
+    if (want_dw && (!dgate_weight || !dup_weight)) return TACO_ERR_NULL;
+    if (!want_dx && !want_dw) return TACO_OK;
+    const Span dg_span = {dgate_weight, features * hidden * kSize};
+    const Span du_span = {dup_weight, features * hidden * kSize};
+    if (rows == 0) {
+        if (!want_dw) return TACO_OK;
+        if (!aligned(dgate_weight, 2) || !aligned(dup_weight, 2)) return TACO_ERR_ALIGN;
+        if (overlap(dg_span, du_span)) return TACO_ERR_ALIAS;
+        const taco_status st = fill_zero(dgate_weight, features * hidden, stream);
+        return st != TACO_OK ? st : fill_zero(dup_weight, features * hidden, stream);
+    }
+    const BackwardOperands o = backward_operands(x, ldx, gate_weight, ldg, up_weight, ldu, rows,
+                                                 hidden, features, want_dx, want_dw);
+    if (!da || !gate || !up || (want_dw && !x) || (want_dx && (!gate_weight || !up_weight)) ||
+        !workspace)
+        return TACO_ERR_NULL;
+    if (!aligned(da, 2) || !aligned(gate, 2) || !aligned(up, 2) || (want_dw && !aligned(x, 2)) ||
+        (want_dx && (!aligned(gate_weight, 2) || !aligned(up_weight, 2))) || !aligned(dx, 2) ||
+        !aligned(dgate_weight, 2) || !aligned(dup_weight, 2) || !aligned(workspace, 16))
+        return TACO_ERR_ALIGN;
+    const Span outs[] = {rows_span(dx, rows, hidden, lddx), dg_span, du_span, {workspace, o.bytes}};
+    const Span ins[] = {rows_span(da, rows, features, ldda), rows_span(gate, rows, features, ldgu),
+                        rows_span(up, rows, features, ldgu),
+                        rows_span(want_dw ? x : nullptr, rows, hidden, ldx),
+                        rows_span(want_dx ? gate_weight : nullptr, features, hidden, ldg),
+                        rows_span(want_dx ? up_weight : nullptr, features, hidden, ldu)};
+    if (any_overlap(outs, ins)) return TACO_ERR_ALIAS;
+    if (workspace_bytes < o.bytes) return TACO_ERR_PARAM;
+    Arena arena = {static_cast<char *>(workspace), {}, 0};
+    float *const slab = static_cast<float *>(arena.take(o.slab_bytes));
+    void *const dgate = arena.take(rows * o.d_pitch * kSize);
+    void *const dup = arena.take(rows * o.d_pitch * kSize);
+    const Matrix mx = want_dw ? arena.place(o.x) : Matrix{};
+    const Matrix mg = want_dx ? arena.place(o.gate) : Matrix{};
+    const Matrix mu = want_dx ? arena.place(o.up) : Matrix{};
+    taco_status st = arena.copy(stream);
+    if (st != TACO_OK) return st;
+    ActivationGrad act = {};
+    act.da = da; act.gate = gate; act.up = up; act.dgate = dgate; act.dup = dup;
+    act.ldda = ldda; act.ldgu = ldgu; act.to_pitch = o.d_pitch; act.rows = rows;
+    act.features = (int32_t)features; act.activation = activation;
+    st = activation_grad(act, dtype == TACO_NORM_F16, stream);
+    if (st != TACO_OK) return st;
+    Product p = {};
+    p.a[0] = {dgate, o.d_pitch * kSize};
+    p.a[1] = {dup, o.d_pitch * kSize};
+    p.slabs = slab;
+    if (want_dx) {
+        p.b[0] = mg; p.b[1] = mu;
+        p.out[0] = dx; p.out_pitch[0] = lddx;
+        p.m = rows; p.n = hidden; p.k = features;
+        st = with_type(dtype, [&](auto k) { return decltype(k)::run(Kind::kInput, p, stream); });
+        if (st != TACO_OK) return st;
+    }
+    if (!want_dw) return TACO_OK;
+    p.b[0] = p.b[1] = mx;
+    p.out[0] = dgate_weight; p.out[1] = dup_weight;
+    p.out_pitch[0] = p.out_pitch[1] = hidden;
+    p.m = features; p.n = hidden; p.k = rows;
+    return with_type(dtype, [&](auto k) { return decltype(k)::run(Kind::kWeight, p, stream); });
+}
+
+int64_t taco_gated_forward_mx_workspace(const uint8_t *x_scales, const uint8_t *gate_scales,
+                                        const uint8_t *up_scales, int64_t rows, int64_t hidden,
+                                        int64_t features) {
+    if (!valid_mx(rows, hidden, features)) return -1;
+    if (rows <= kFewRows) return 0;
+    Product p = {};
+    p.m = rows; p.n = features; p.k = hidden;
+    return Products<Codes>::workspace(Kind::kForward, p) + scales(x_scales, rows, hidden).copy_bytes() +
+           scales(gate_scales, features, hidden).copy_bytes() +
+           scales(up_scales, features, hidden).copy_bytes();
+}
+
+taco_status taco_gated_forward_mx(const uint8_t *x_codes, const uint8_t *x_scales,
+                                  const uint8_t *gate_codes, const uint8_t *gate_scales,
+                                  const uint8_t *up_codes, const uint8_t *up_scales, int64_t rows,
+                                  int64_t hidden, int64_t features, taco_norm_dtype dtype,
+                                  taco_gated_activation activation, void *a, int64_t lda,
+                                  void *workspace, int64_t workspace_bytes, hipStream_t stream) {
+    if (!valid(dtype)) return TACO_ERR_FORMAT;
+    if (!valid_mx(rows, hidden, features) || !valid_rows(rows, features, lda)) return TACO_ERR_SHAPE;
+    if (!valid(activation)) return TACO_ERR_PARAM;
+    if (rows == 0) return TACO_OK;
+    const int64_t need =
+        taco_gated_forward_mx_workspace(x_scales, gate_scales, up_scales, rows, hidden, features);
+    if (!x_codes || !x_scales || !gate_codes || !gate_scales || !up_codes || !up_scales || !a ||
+        (need && !workspace))
+        return TACO_ERR_NULL;
+    if (!aligned(x_codes, 16) || !aligned(gate_codes, 16) || !aligned(up_codes, 16) ||
+        !aligned(a, 2) || (need && !aligned(workspace, 16)))
+        return TACO_ERR_ALIGN;
+    const int64_t blocks = hidden / 32;
+    const Span outs[] = {rows_span(a, rows, features, lda), {workspace, need}};
+    const Span ins[] = {{x_codes, rows * hidden}, {x_scales, rows * blocks},
+                        {gate_codes, features * hidden}, {gate_scales, features * blocks},
+                        {up_codes, features * hidden}, {up_scales, features * blocks}};
+    if (any_overlap(outs, ins)) return TACO_ERR_ALIAS;
+    if (workspace_bytes < need) return TACO_ERR_PARAM;
+    Product p = {};
+    p.m = rows; p.n = features; p.k = hidden;
+    p.activation = activation;
+    p.out_f16 = dtype == TACO_NORM_F16;
+    p.out[0] = a; p.out_pitch[0] = lda;
+    p.a[0] = {x_codes, hidden};
+    p.b[0] = {gate_codes, hidden};
+    p.b[1] = {up_codes, hidden};
+    p.a_scale = {x_scales, blocks};
+    p.b_scale[0] = {gate_scales, blocks};
+    p.b_scale[1] = {up_scales, blocks};
+    if (rows <= kFewRows) return Products<Codes>::few(p, stream);
+    Arena arena = {static_cast<char *>(workspace), {}, 0};
+    p.slabs = static_cast<float *>(arena.take(Products<Codes>::workspace(Kind::kForward, p)));
+    Matrix *const to[] = {&p.a_scale, &p.b_scale[0], &p.b_scale[1]};
+    const Scales from[] = {scales(x_scales, rows, hidden), scales(gate_scales, features, hidden),
+                           scales(up_scales, features, hidden)};
+    for (int i = 0; i < 3; ++i) {
+        if (!from[i].copied) continue;
+        const int64_t pitch = round_up(blocks, 16);
+        void *const copy = arena.take(from[i].copy_bytes());
+        arena.copies[arena.count++] = {from[i].p, copy, blocks, pitch, from[i].rows, blocks};
+        *to[i] = {copy, pitch};
+    }
+    const taco_status st = arena.copy(stream);
+    return st != TACO_OK ? st : Products<Codes>::run(Kind::kForward, p, stream);
+}
+
+taco_status taco_gated_mx_encode(const void *x, int64_t ldx, int64_t rows, int64_t hidden,
+                                 taco_norm_dtype dtype, uint8_t *codes, uint8_t *scale_bytes,
+                                 hipStream_t stream) {
+    if (!valid(dtype) && dtype != TACO_NORM_F32) return TACO_ERR_FORMAT;
+    if (!valid_width(hidden) || hidden % 32 != 0 || !valid_rows(rows, hidden, ldx))
+        return TACO_ERR_SHAPE;
+    if (rows == 0) return TACO_OK;
+    if (!x || !codes || !scale_bytes) return TACO_ERR_NULL;
+    const int64_t size = dtype == TACO_NORM_F32 ? 4 : 2;
+    if (!aligned(x, size)) return TACO_ERR_ALIGN;
+    const Span outs[] = {{codes, rows * hidden}, {scale_bytes, rows * (hidden / 32)}};
+    const Span ins[] = {{x, ((rows - 1) * ldx + hidden) * size}};
+    if (any_overlap(outs, ins)) return TACO_ERR_ALIAS;
+    return encode({x, codes, scale_bytes, ldx, rows, hidden}, dtype, stream);
+}
+
+}  // extern "C"

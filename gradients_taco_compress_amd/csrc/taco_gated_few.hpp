@@ -1,0 +1,150 @@
+// Forward pass of the gated block for at most 16 rows (the tokens that a
+// serving step adds): both weights are read once, which is all the time it
+// takes, so they go from memory to the matrix instructions' registers without
+// LDS in between.
+//
+//  * A wave multiplies the rows by 16 gate and the 16 same up features.  Lane
+//    (g, r) reads chunks of feature r (and of row r of X, which stays in
+//    cache); the waves of a work-group share the summed length and add their
+//    sums in LDS, in order.
+//  * A wave's turn takes 256 bytes of each feature, all its loads issued before the
+//    products of the turn before.
+#pragma once
+
+#include <type_traits>
+
+#include "taco_gated_product.hpp"
+
+namespace taco_gated {
+namespace {
+
+template <typename E, int WAVES>
+__global__ __launch_bounds__(WAVES * kWave) void few_kernel(Product p) {
+    using El = Element<E>;
+    constexpr int SIZE = El::SIZE, TURN = 2;                     // K-tiles in a turn
+    constexpr bool SCALED = El::SCALED;
+    __shared__ f4v sums[WAVES > 1 ? WAVES - 1 : 1][2][kWave];
+    const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, r = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int64_t f0 = (int64_t)blockIdx.x * 16;
+    const int64_t f = f0 + r < p.n ? f0 + r : p.n - 1, m = r < p.m ? r : p.m - 1;
+    // Rows of gate, up and X; those past the last are repeated and not stored.
+    const char *const rows[3] = {static_cast<const char *>(p.b[0].p) + f * p.b[0].pitch,
+                                 static_cast<const char *>(p.b[1].p) + f * p.b[1].pitch,
+                                 static_cast<const char *>(p.a[0].p) + m * p.a[0].pitch};
+    [[maybe_unused]] const uint8_t *scales[3] = {};
+    if constexpr (SCALED) {
+        scales[0] = static_cast<const uint8_t *>(p.b_scale[0].p) + f * p.b_scale[0].pitch;
+        scales[1] = static_cast<const uint8_t *>(p.b_scale[1].p) + f * p.b_scale[1].pitch;
+        scales[2] = static_cast<const uint8_t *>(p.a_scale.p) + m * p.a_scale.pitch;
+    }
+    const int64_t bytes = p.k * SIZE;
+    struct Turn {
+        Fragment v[TURN][3];
+        int scale[TURN][3];
+    };
+    Turn held[2];
+    auto load = [&](int64_t turn, Turn &to) {
+        const int64_t at = turn * TURN * kDeep;
+        if (at + TURN * kDeep <= bytes) {
+#pragma unroll
+            for (int t = 0; t < TURN; ++t)
+#pragma unroll
+                for (int s = 0; s < 3; ++s) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        to.v[t][s].v[h] = *reinterpret_cast<const u4v_any *>(
+                            rows[s] + at + t * kDeep + h * 64 + g * 16);
+                    if constexpr (SCALED) to.scale[t][s] = scales[s][(at + t * kDeep) / 32 + g];
+                }
+            return;
+        }
+        // The last turn: what is past the row's end is zero.
+#pragma unroll
+        for (int t = 0; t < TURN; ++t)
+#pragma unroll
+            for (int s = 0; s < 3; ++s) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t c = at + t * kDeep + h * 64 + g * 16, left = bytes - c;
+                    to.v[t][s].v[h] = (u4v){0u, 0u, 0u, 0u};
+                    if (left > 0)
+                        to.v[t][s].v[h] = load_tail<true>(rows[s] + c, rows[s], left < 16 ? (int)left : 16);
+                }
+                if constexpr (SCALED) {
+                    const int64_t block = (at + t * kDeep) / 32 + g;
+                    to.scale[t][s] = block < p.k / 32 ? scales[s][block] : 0;
+                }
+            }
+    };
+    f4v gate = {0.0f, 0.0f, 0.0f, 0.0f}, up = gate;
+    auto multiply = [&](const Turn &in) {
+#pragma unroll
+        for (int t = 0; t < TURN; ++t) {
+            gate = El::run(in.v[t][0], in.v[t][2], gate, in.scale[t][0], in.scale[t][2]);
+            up = El::run(in.v[t][1], in.v[t][2], up, in.scale[t][1], in.scale[t][2]);
+        }
+    };
+    const int64_t turns = (bytes + TURN * kDeep - 1) / (TURN * kDeep);
+    int64_t turn = wave;
+    if (turn < turns) load(turn, held[0]);
+    while (turn < turns) {
+        if (turn + WAVES < turns) load(turn + WAVES, held[1]);
+        multiply(held[0]);
+        turn += WAVES;
+        if (turn >= turns) break;
+        if (turn + WAVES < turns) load(turn + WAVES, held[0]);
+        multiply(held[1]);
+        turn += WAVES;
+    }
+    if constexpr (WAVES > 1) {
+        if (wave > 0) {
+            sums[wave - 1][0][lane] = gate;
+            sums[wave - 1][1][lane] = up;
+        }
+        __syncthreads();
+        if (wave > 0) return;
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) {
+            gate += sums[w - 1][0][lane];
+            up += sums[w - 1][1][lane];
+        }
+    }
+    // Lane (g, r): features 4 g + (0..3) of row r.
+    const int64_t first = f0 + 4 * g, left = p.n - first;
+    if (r >= p.m || left <= 0) return;
+    float vg[4], vu[4], out[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        vg[e] = gate[e];
+        vu[e] = up[e];
+    }
+    with_activation(p.activation, [&](auto act) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[e] = vg[e] * gate_share<decltype(act)::value>(vg[e]) * vu[e];
+    });
+    auto store = [&](auto *kind) {
+        using T = typename std::remove_pointer<decltype(kind)>::type;
+        store_row<T, 4>(static_cast<T *>(p.out[0]) + r * p.out_pitch[0] + first, out, left);
+        if (p.out[1]) {
+            store_row<T, 4>(static_cast<T *>(p.out[1]) + r * p.out_pitch[1] + first, vg, left);
+            store_row<T, 4>(static_cast<T *>(p.out[2]) + r * p.out_pitch[2] + first, vu, left);
+        }
+    };
+    if constexpr (SCALED) {
+        if (p.out_f16) store(static_cast<_Float16 *>(nullptr));
+        else store(static_cast<__bf16 *>(nullptr));
+    } else {
+        store(static_cast<typename El::type *>(nullptr));
+    }
+}
+
+}  // namespace
+
+template <typename E>
+taco_status Products<E>::few(const Product &p, hipStream_t stream) {
+    const dim3 grid((unsigned)up(p.n, 16));
+    return launch(reinterpret_cast<const void *>(&few_kernel<E, 4>), grid, 4 * kWave, stream, p);
+}
+
+}  // namespace taco_gated

@@ -1,0 +1,6 @@
+// Matrix products of the gated block for E4M3 codes with block scales (one translation unit
+// per type keeps each compilation small; see taco_gated_product.hpp).
+#include "taco_gated_product.hpp"
+#include "taco_gated_few.hpp"
+
+template struct taco_gated::Products<taco_gated::Codes>;

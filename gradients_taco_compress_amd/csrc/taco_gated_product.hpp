@@ -1,0 +1,656 @@
+// The three matrix products of the gated feed-forward block (formulas in
+// taco_gated.h) for gfx950, templated on the operands' type and on the kind of
+// product.
+//
+//  * One kernel, one tile walk.  A work-group makes BM x BN outputs from
+//    K-tiles of 128 bytes of summed length (64 elements, or 128 codes).  Both
+//    operands of a K-tile are kept in LDS as two halves each (A0, A1, B0, B1),
+//    two K-tiles at a time, and a K-tile is worked off in four phases, the
+//    quadrants (A0,B0), (A0,B1), (A1,B1), (A1,B0) of the output.
+//  * The forward pass takes gate features as B0 and the same up features as
+//    B1, so that G and U of an element meet in one lane and A is formed from
+//    the float32 sums: G and U are not written unless training asks for them.
+//  * Each phase loads one half of a later K-tile straight to LDS (16 bytes a
+//    lane, no registers), reads the fragments of the next phase, multiplies,
+//    and ends with the one barrier that serves both: the half read next has
+//    arrived, the half overwritten next has been read, by all waves.  Six halves
+//    are on their way at any time.
+//  * Operands whose summed index is contiguous (X and the weights, forward)
+//    lie in LDS as rows of 128 bytes, 16-byte chunk c of row R at chunk
+//    c ^ f(R); those whose summed index is the slow one lie as they do in memory
+//    and are turned by the transposing LDS reads, 32-byte units of row t at
+//    unit u ^ turn(t).  f and turn put what is read together on different banks.
+//  * Rows and columns outside the matrices are out of the loads' bounds and
+//    arrive as zeros, so ragged edges cost no instructions in the products.
+//  * Tiles beyond a whole number per CU are split along the summed index, and
+//    a second kernel adds the parts in order and finishes them.
+//  * Codes go through the scaled matrix instruction (16x16x128).  Its scale
+//    operand of lane (g, r) is the one of 32-block g of row r, while the lane's
+//    data are the 16-byte chunks g and 4 + g of the row: the same reads as for
+//    16-bit elements.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "taco_gated_internal.hpp"
+#include "taco_gated_device.hpp"
+
+namespace taco_gated {
+namespace {
+
+typedef int i8v __attribute__((ext_vector_type(8)));
+typedef short s4v __attribute__((ext_vector_type(4)));
+
+constexpr int kDeep = 128;          // bytes of summed length in a K-tile
+
+// A fragment: 16 rows (or columns) of a K-tile.  Lane (g, r) holds of row r the
+// elements 8 g .. 8 g + 7 of each half of the K-tile (codes: 16 g ..).
+struct Fragment {
+    u4v v[2];
+};
+
+template <typename E>
+struct Element;
+template <>
+struct Element<BF16> {
+    typedef __bf16 type;
+    static constexpr int SIZE = 2;
+    static constexpr bool SCALED = false;
+    static __device__ __forceinline__ f4v run(const Fragment &a, const Fragment &b, f4v c, int, int) {
+        typedef __bf16 v8 __attribute__((ext_vector_type(8)));
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a.v[i]),
+                                                        __builtin_bit_cast(v8, b.v[i]), c, 0, 0, 0);
+        return c;
+    }
+};
+template <>
+struct Element<F16> {
+    typedef _Float16 type;
+    static constexpr int SIZE = 2;
+    static constexpr bool SCALED = false;
+    static __device__ __forceinline__ f4v run(const Fragment &a, const Fragment &b, f4v c, int, int) {
+        typedef _Float16 v8 __attribute__((ext_vector_type(8)));
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8, a.v[i]),
+                                                       __builtin_bit_cast(v8, b.v[i]), c, 0, 0, 0);
+        return c;
+    }
+};
+template <>
+struct Element<Codes> {
+    typedef uint8_t type;
+    static constexpr int SIZE = 1;
+    static constexpr bool SCALED = true;
+    static __device__ __forceinline__ f4v run(const Fragment &a, const Fragment &b, f4v c, int sa,
+                                              int sb) {
+        // 0, 0: both operands E4M3; 0: the scales' lowest byte.
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            __builtin_bit_cast(i8v, a), __builtin_bit_cast(i8v, b), c, 0, 0, 0, sa, 0, sb);
+    }
+};
+
+// Shape of a work-group: BM x BN outputs by WM x WN waves.  (Forward: BN / 2
+// features.)
+template <int BM_, int BN_, int WM_, int WN_>
+struct Shape {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+    static constexpr int THREADS = WM * WN * kWave;
+    static constexpr int HM = BM / 2, HN = BN / 2;                     // a half's rows
+    static constexpr int MF = HM / WM / 16, NF = HN / WN / 16;         // a wave's fragments of it
+    static constexpr int A_HALF = HM * kDeep, B_HALF = HN * kDeep;     // its bytes
+    static_assert(HM == HN, "halves alike: one load count for all");
+    static constexpr int LOADS = A_HALF / 16 / THREADS;                // a thread's loads of it
+    static_assert(LOADS == 2 && NF == 2, "loads and pairs of column fragments");
+    // A split's partial sums.
+    static constexpr int64_t SLAB = (int64_t)BM * BN;
+};
+using Large = Shape<256, 256, 2, 4>;
+using Small = Shape<128, 128, 2, 2>;
+
+// Which tile and which K-tiles a work-group takes.  The first `whole`
+// work-groups take a tile each; the remaining tiles are cut into `parts` parts of
+// `share` K-tiles.
+struct Plan {
+    int32_t tiles_m, tiles_n;
+    int32_t whole, parts, share;
+    int32_t depth;                 // K-tiles of a tile
+};
+
+struct Tile { int m, n; };
+
+// Tile number t of an order in which neighbours share operands: strips of
+// four tile rows, each walked column by column.
+__device__ __forceinline__ Tile tile_at(const Plan &s, int t) {
+    constexpr int kStrip = 4;
+    const int strip = t / (kStrip * s.tiles_n), in = t - strip * kStrip * s.tiles_n;
+    const int left = s.tiles_m - strip * kStrip, rows = left < kStrip ? left : kStrip;
+    return {strip * kStrip + in % rows, in / rows};
+}
+
+// Feature of LDS row R of a forward B half: of each 32 features, fragment j
+// takes 8 q + 4 j + (0..3), so that a lane's two fragments are eight neighbours.
+__device__ __forceinline__ int feature_of_row(int R) {
+    return (R & ~31) | (((R >> 2) & 3) << 3) | (((R >> 4) & 1) << 2) | (R & 3);
+}
+
+__device__ __forceinline__ int clamp(int64_t v, int most) {
+    return v < 0 ? 0 : v < most ? (int)v : most;
+}
+
+// Lane (g, r) = (lane / 16, lane % 16) of wave (wm, wn) holds, in fragments
+// (i, j) of a quadrant, row m = r and columns 4 g + (0..3).
+template <typename S>
+struct Place {
+    int g, r, wm, wn;
+    __device__ __forceinline__ explicit Place(int tid)
+        : g((tid >> 4) & 3), r(tid & 15),
+          wm(__builtin_amdgcn_readfirstlane(tid / kWave) % S::WM),
+          wn(__builtin_amdgcn_readfirstlane(tid / kWave) / S::WM) {}
+};
+
+// Writes one row fragment of a tile's outputs: v[qb][j], quadrant column qb and
+// column fragment j.
+template <typename E, Kind K, typename S>
+struct Finish {
+    const Product &p;
+    const Place<S> &place;
+    Tile tile;
+
+    template <typename T>
+    __device__ __forceinline__ void forward(int64_t m, const f4v (&v)[2][2]) const {
+        const int64_t f = (int64_t)tile.n * S::HN + place.wn * 32 + 8 * place.g;
+        const int64_t left = p.n - f;
+        if (left <= 0) return;
+        float gate[8], up[8], out[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            gate[e] = v[0][e >> 2][e & 3];
+            up[e] = v[1][e >> 2][e & 3];
+        }
+        with_activation(p.activation, [&](auto act) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                out[e] = gate[e] * gate_share<decltype(act)::value>(gate[e]) * up[e];
+        });
+        store_row<T, 8>(static_cast<T *>(p.out[0]) + m * p.out_pitch[0] + f, out, left);
+        if (p.out[1]) {
+            store_row<T, 8>(static_cast<T *>(p.out[1]) + m * p.out_pitch[1] + f, gate, left);
+            store_row<T, 8>(static_cast<T *>(p.out[2]) + m * p.out_pitch[2] + f, up, left);
+        }
+    }
+
+    __device__ __forceinline__ void operator()(int qa, int i, const f4v (&v)[2][2]) const {
+        int tm = tile.m, which = 0;
+        if constexpr (K == Kind::kWeight) {
+            // The tiles of dWg, then those of dWu.
+            const int per = (int)((p.m + S::BM - 1) / S::BM);
+            which = tm >= per;
+            tm -= which * per;
+        }
+        const int64_t m = (int64_t)tm * S::BM + qa * S::HM + place.wm * (S::HM / S::WM) + 16 * i + place.r;
+        if (m >= p.m) return;
+        if constexpr (K == Kind::kForward) {
+            if constexpr (Element<E>::SCALED) {
+                if (p.out_f16) forward<_Float16>(m, v);
+                else forward<__bf16>(m, v);
+            } else {
+                forward<typename Element<E>::type>(m, v);
+            }
+        } else {
+            using T = typename Element<E>::type;
+            T *const row = static_cast<T *>(p.out[which]) + m * p.out_pitch[which];
+#pragma unroll
+            for (int qb = 0; qb < 2; ++qb)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int64_t n = (int64_t)tile.n * S::BN + qb * S::HN + place.wn * 32 + 16 * j + 4 * place.g;
+                    if (n >= p.n) continue;
+                    const float out[4] = {v[qb][j][0], v[qb][j][1], v[qb][j][2], v[qb][j][3]};
+                    store_row<T, 4>(row + n, out, p.n - n);
+                }
+        }
+    }
+};
+
+// What a half's loads read: rows `pitch` apart from `base`, `records` bytes in
+// all, and of each row the first `limit` 16-byte chunks.
+struct Source {
+    const char *base;
+    int records, limit;
+};
+
+template <typename E, Kind K, typename S>
+__global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan plan) {
+    using El = Element<E>;
+    constexpr int HM = S::HM, HN = S::HN, MF = S::MF, NF = S::NF, THREADS = S::THREADS;
+    constexpr int SIZE = El::SIZE, KT = kDeep / SIZE;          // summed elements of a K-tile
+    constexpr bool A_TURNED = K == Kind::kWeight, B_TURNED = K != Kind::kForward;
+    constexpr bool SCALED = El::SCALED;
+    // A variable for each half, not one for all: the compiler then knows that a
+    // load into one does not touch the fragments being read from another, and
+    // does not wait for it.
+    __shared__ __align__(1024) uint8_t a00[S::A_HALF], a01[S::A_HALF], a10[S::A_HALF],
+        a11[S::A_HALF], b00[S::B_HALF], b01[S::B_HALF], b10[S::B_HALF], b11[S::B_HALF];
+    constexpr int SCALES = SCALED ? THREADS * 4 : 4;
+    __shared__ __align__(16) uint8_t s0[SCALES], s1[SCALES], s2[SCALES], s3[SCALES];
+    auto lds_a = [&](auto stage, auto half) -> uint8_t * {
+        constexpr int i = (decltype(stage)::value & 1) * 2 + decltype(half)::value;
+        return i == 0 ? a00 : i == 1 ? a01 : i == 2 ? a10 : a11;
+    };
+    auto lds_b = [&](auto stage, auto half) -> uint8_t * {
+        constexpr int i = (decltype(stage)::value & 1) * 2 + decltype(half)::value;
+        return i == 0 ? b00 : i == 1 ? b01 : i == 2 ? b10 : b11;
+    };
+    [[maybe_unused]] auto lds_s = [&](auto stage) -> uint8_t * {
+        constexpr int i = decltype(stage)::value & 3;
+        return i == 0 ? s0 : i == 1 ? s1 : i == 2 ? s2 : s3;
+    };
+
+    const int tid = threadIdx.x;
+    [[maybe_unused]] const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const Place<S> place(tid);
+
+    // Consecutive work-groups go to the 8 XCDs in turn; each XCD gets a
+    // contiguous range of the whole tiles, whose operands meet in its L2.
+    int t_index, part = -1, kt0 = 0, kt1 = plan.depth;
+    if ((int)blockIdx.x < plan.whole) {
+        const int xcd = blockIdx.x % 8, q = plan.whole / 8, rem = plan.whole % 8;
+        t_index = xcd * q + (xcd < rem ? xcd : rem) + blockIdx.x / 8;
+    } else {
+        part = (int)blockIdx.x - plan.whole;
+        const int in = part % plan.parts;
+        t_index = plan.whole + part / plan.parts;
+        kt0 = in * plan.share;
+        if (kt0 + plan.share < kt1) kt1 = kt0 + plan.share;
+    }
+    const Tile tile = tile_at(plan, t_index);
+    const int seg_depth = K == Kind::kInput ? plan.depth / 2 : plan.depth;
+
+    // Chunk i of this thread is LDS chunk i * THREADS + tid of a half: its row
+    // there, the chunk of the source row it comes from, and its offset there.
+    auto f_of = [](int R) { return (R >> 1) & 7; };
+    auto turn_of = [](int t) {
+        return HM == 128 ? ((t & 3) | (((t >> 3) & 1) << 2)) : (((t >> 1) & 1) | (((t >> 3) & 1) << 1));
+    };
+    constexpr int TURNED_CHUNKS = HM / 8;                       // 16-byte chunks of a turned row
+    auto chunk_of = [&](bool turned, int i, int *row) {
+        const int q = i * THREADS + tid;
+        if (!turned) {
+            *row = q / 8;
+            return (q % 8) ^ f_of(*row);
+        }
+        *row = q / TURNED_CHUNKS;
+        const int c = q % TURNED_CHUNKS;
+        return (((c >> 1) ^ turn_of(*row)) << 1) | (c & 1);
+    };
+    [[maybe_unused]] uint32_t off_a[2], off_b[2];
+    [[maybe_unused]] int chunk_a, chunk_b;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        // (the same chunk for both: their rows differ by a multiple of 16)
+        int row;
+        chunk_a = chunk_of(A_TURNED, i, &row);
+        off_a[i] = (uint32_t)(row * (int)p.a[0].pitch + chunk_a * 16);
+        chunk_b = chunk_of(B_TURNED, i, &row);
+        if (K == Kind::kForward) row = feature_of_row(row);
+        off_b[i] = (uint32_t)(row * (int)p.b[0].pitch + chunk_b * 16);
+    }
+
+    // Where half h of K-tile kt comes from.
+    const int per_m = (int)((p.m + S::BM - 1) / S::BM);
+    const int which = K == Kind::kWeight && tile.m >= per_m;
+    const int64_t m0 = (int64_t)(tile.m - which * per_m) * S::BM;
+    const int64_t n0 = (int64_t)tile.n * (K == Kind::kForward ? HN : S::BN);
+    auto source_a = [&](int h, int kt) -> Source {
+        const int seg = K == Kind::kInput ? kt >= seg_depth : which;
+        if (K == Kind::kInput && seg) kt -= seg_depth;
+        const char *const base = static_cast<const char *>(p.a[seg].p);
+        const int64_t pitch = p.a[0].pitch, k = (int64_t)kt * KT, m = m0 + h * HM;
+        if constexpr (A_TURNED)
+            return {base + k * pitch + m * SIZE, clamp(p.k - k, KT) * (int)pitch,
+                    clamp((p.m - m + 7) / 8, HM / 8)};
+        return {base + m * pitch + k * SIZE, clamp(p.m - m, HM) * (int)pitch,
+                clamp((p.k - k + 16 / SIZE - 1) / (16 / SIZE), 8)};
+    };
+    auto source_b = [&](int h, int kt) -> Source {
+        const int seg = K == Kind::kInput ? kt >= seg_depth : K == Kind::kForward ? h : 0;
+        if (K == Kind::kInput && seg) kt -= seg_depth;
+        const char *const base = static_cast<const char *>(p.b[seg].p);
+        const int64_t pitch = p.b[0].pitch, k = (int64_t)kt * KT;
+        if constexpr (B_TURNED) {
+            const int64_t n = n0 + h * HN;
+            return {base + k * pitch + n * SIZE, clamp(p.k - k, KT) * (int)pitch,
+                    clamp((p.n - n + 7) / 8, HN / 8)};
+        }
+        return {base + n0 * pitch + k * SIZE, clamp(p.n - n0, HN) * (int)pitch,
+                clamp((p.k - k + 16 / SIZE - 1) / (16 / SIZE), 8)};
+    };
+    // (The host pass does not know the resource type.)
+    auto load = [&](uint8_t *buf, Source s, const uint32_t (&off)[2], int chunk) {
+#if defined(__HIP_DEVICE_COMPILE__)
+        // 0x00020000: raw 32-bit data.
+        const auto r = __builtin_amdgcn_make_buffer_rsrc((void *)s.base, 0, s.records, 0x00020000);
+        const bool in = chunk < s.limit;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                r, (__attribute__((address_space(3))) void *)(buf + (i * THREADS + wave * kWave) * 16),
+                16, in ? off[i] : 0x80000000u, 0, 0, 0);
+#endif
+    };
+    auto load_a = [&](auto stage, auto half, int kt) {
+        // (past the last K-tile: nothing, which arrives as zeros)
+        Source s = source_a(decltype(half)::value, kt < kt1 ? kt : kt0);
+        if (kt >= kt1) s.records = 0;
+        load(lds_a(stage, half), s, off_a, chunk_a);
+    };
+    auto load_b = [&](auto stage, auto half, int kt) {
+        Source s = source_b(decltype(half)::value, kt < kt1 ? kt : kt0);
+        if (kt >= kt1) s.records = 0;
+        load(lds_b(stage, half), s, off_b, chunk_b);
+    };
+    // Scales of a K-tile: one 4-byte load a thread, [A0 | A1 | B0 | B1][row][block].
+    [[maybe_unused]] const char *scale_base = nullptr;
+    [[maybe_unused]] int scale_records = 0;
+    [[maybe_unused]] uint32_t scale_off = 0;
+    if constexpr (SCALED) {
+        const int quarter = __builtin_amdgcn_readfirstlane(tid / HM), row = tid % HM;
+        const bool b = quarter >= 2;
+        const Matrix &s = b ? p.b_scale[quarter - 2] : p.a_scale;
+        const int64_t first = b ? n0 : m0 + quarter * HM;
+        scale_base = static_cast<const char *>(s.p) + first * s.pitch;
+        scale_records = clamp((b ? p.n : p.m) - first, HM) * (int)s.pitch;
+        scale_off = (uint32_t)((b ? feature_of_row(row) : row) * (int)s.pitch);
+    }
+    auto load_scales = [&](auto stage, int kt) {
+#if defined(__HIP_DEVICE_COMPILE__)
+        if constexpr (SCALED) {
+            const bool in = kt < kt1;
+            const auto r = __builtin_amdgcn_make_buffer_rsrc(
+                (void *)(scale_base + (in ? (int64_t)kt * 4 : 0)), 0, in ? scale_records : 0,
+                0x00020000);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                r, (__attribute__((address_space(3))) void *)(lds_s(stage) + wave * kWave * 4), 4,
+                scale_off, 0, 0, 0);
+        }
+#endif
+    };
+
+    // Fragment addresses.  Rows of 128 bytes: lane (g, r) reads chunk g (then
+    // 4 + g) of row r.  Turned: 8 bytes of row 8 g + r / 4 (then + 4), which
+    // the read hands out as column r of them; a wave's units differ in their
+    // low bits only, so fragment i's unit is the first one's XOR i.
+    auto first_of = [&](bool turned, int row) {
+        if (!turned) return (row + place.r) * kDeep + ((place.g ^ f_of(row + place.r)) * 16);
+        const int t = 8 * place.g + (place.r >> 2);
+        return t * HM * 2 + (((row / 16) ^ turn_of(t)) * 32) + (place.r & 3) * 8;
+    };
+    int at_a = first_of(A_TURNED, place.wm * (HM / S::WM));
+    int at_b = first_of(B_TURNED, place.wn * (HN / S::WN));
+    auto read = [&](auto turned, uint8_t *buf, int at, int i) {
+        Fragment f;
+        if constexpr (decltype(turned)::value != 0) {
+            uint8_t *q = buf + (at ^ (i * 32));
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                union { s4v s[2]; u4v v; } u;
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    u.s[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                        (__attribute__((address_space(3))) s4v *)(q + (32 * kk + 4 * e) * HM * 2));
+                f.v[kk] = u.v;
+            }
+        } else {
+            f.v[0] = *reinterpret_cast<const u4v *>(buf + at + i * 16 * kDeep);
+            f.v[1] = *reinterpret_cast<const u4v *>(buf + (at ^ 64) + i * 16 * kDeep);
+        }
+        return f;
+    };
+    Fragment fa[2][MF], fb[2][NF];
+    int sa[2][MF] = {}, sb[2][NF] = {};
+    auto read_a = [&](auto stage, auto half) {
+        constexpr int h = decltype(half)::value;
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+            fa[h][i] = read(Int<A_TURNED>{}, lds_a(stage, half), at_a, i);
+            if constexpr (SCALED)
+                sa[h][i] = lds_s(stage)[(h * HM + place.wm * (HM / S::WM) + 16 * i + place.r) * 4 + place.g];
+        }
+    };
+    auto read_b = [&](auto stage, auto half, auto slot) {
+        constexpr int h = decltype(half)::value, to = decltype(slot)::value & 1;
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+            fb[to][j] = read(Int<B_TURNED>{}, lds_b(stage, half), at_b, j);
+            if constexpr (SCALED)
+                sb[to][j] = lds_s(stage)[((2 + h) * HM + place.wn * (HN / S::WN) + 16 * j + place.r) * 4 + place.g];
+        }
+    };
+    f4v sum[2][2][MF][NF];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+#pragma unroll
+            for (int j = 0; j < NF; ++j) sum[q >> 1][q & 1][i][j] = (f4v){0.0f, 0.0f, 0.0f, 0.0f};
+    auto multiply = [&](auto qa, auto qb, auto slot) {
+        constexpr int a = decltype(qa)::value, b = decltype(qb)::value, s = decltype(slot)::value & 1;
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+#pragma unroll
+            for (int j = 0; j < NF; ++j)
+                sum[a][b][i][j] = El::run(fb[s][j], fa[a][i], sum[a][b][i][j], sb[s][j], sa[a][i]);
+    };
+
+    // K-tile t of this work-group (counted from kt0) lies in stage t % 2, its
+    // scales in stage t % 4; its B0 fragments in slot t % 2, its B1 fragments
+    // in the other.  Loads are in the order S, A0, B0, B1, A1 of each K-tile, so
+    // "the half has arrived" is a count of those after it.
+    using C0 = Int<0>;
+    using C1 = Int<1>;
+    constexpr int L = S::LOADS, SL = SCALED ? 1 : 0;
+    load_scales(C0{}, kt0);
+    load_a(C0{}, C0{}, kt0);
+    load_b(C0{}, C0{}, kt0);
+    load_b(C0{}, C1{}, kt0);
+    load_a(C0{}, C1{}, kt0);
+    load_scales(C1{}, kt0 + 1);
+    load_a(C1{}, C0{}, kt0 + 1);
+    load_b(C1{}, C0{}, kt0 + 1);
+    load_b(C1{}, C1{}, kt0 + 1);
+    load_a(C1{}, C1{}, kt0 + 1);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(6 * L + SL) : "memory");
+    read_a(C0{}, C0{});
+    read_b(C0{}, C0{}, C0{});
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    load_scales(Int<2>{}, kt0 + 2);
+    load_a(C0{}, C0{}, kt0 + 2);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(6 * L + 2 * SL) : "memory");
+
+    auto phase_end = [&](auto more) {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(6 * L + decltype(more)::value)
+                     : "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto k_tile = [&](auto index, int kt) {
+        constexpr int s = decltype(index)::value;
+        using Now = Int<s & 3>;
+        using Next = Int<(s + 1) & 3>;
+        using After = Int<(s + 2) & 3>;
+        using Third = Int<(s + 3) & 3>;
+        // (A0, B0)
+        load_b(After{}, C0{}, kt + 2);
+        read_b(Now{}, C1{}, Int<s + 1>{});
+        multiply(C0{}, C0{}, Int<s>{});
+        phase_end(Int<2 * SL>{});
+        // (A0, B1)
+        load_b(After{}, C1{}, kt + 2);
+        read_a(Now{}, C1{});
+        multiply(C0{}, C1{}, Int<s + 1>{});
+        phase_end(Int<SL>{});
+        // (A1, B1)
+        load_a(After{}, C1{}, kt + 2);
+        read_a(Next{}, C0{});
+        multiply(C1{}, C1{}, Int<s + 1>{});
+        phase_end(Int<SL>{});
+        // (A1, B0)
+        load_scales(Third{}, kt + 3);
+        load_a(Third{}, C0{}, kt + 3);
+        read_b(Next{}, C0{}, Int<s + 1>{});
+        multiply(C1{}, C0{}, Int<s>{});
+        phase_end(Int<2 * SL>{});
+    };
+    // The tiles read ahead past the last are zeros.
+    for (int kt = kt0;;) {
+        k_tile(C0{}, kt);
+        if (++kt >= kt1) break;
+        k_tile(C1{}, kt);
+        if (++kt >= kt1) break;
+        if constexpr (SCALED) {
+            k_tile(Int<2>{}, kt);
+            if (++kt >= kt1) break;
+            k_tile(Int<3>{}, kt);
+            if (++kt >= kt1) break;
+        }
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+    if (part >= 0) {
+        float *const slab = p.slabs + (int64_t)part * S::SLAB;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+#pragma unroll
+                for (int j = 0; j < NF; ++j)
+                    *reinterpret_cast<f4v *>(slab + (int64_t)((((q >> 1) * MF + i) * 4 + (q & 1) * 2 + j) * THREADS + tid) * 4) =
+                        sum[q >> 1][q & 1][i][j];
+        return;
+    }
+    const Finish<E, K, S> finish{p, place, tile};
+#pragma unroll
+    for (int qa = 0; qa < 2; ++qa)
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+            const f4v v[2][2] = {{sum[qa][0][i][0], sum[qa][0][i][1]}, {sum[qa][1][i][0], sum[qa][1][i][1]}};
+            finish(qa, i, v);
+        }
+}
+
+// Adds the parts of a split tile in order and finishes it: blockIdx.x is the
+// tile after the whole ones, blockIdx.y its row fragment.
+template <typename E, Kind K, typename S>
+__global__ __launch_bounds__(S::THREADS) void join_kernel(Product p, Plan plan) {
+    const Place<S> place(threadIdx.x);
+    const Tile tile = tile_at(plan, plan.whole + blockIdx.x);
+    const float *at = p.slabs + (int64_t)blockIdx.x * plan.parts * S::SLAB +
+                      ((int64_t)blockIdx.y * 4 * S::THREADS + threadIdx.x) * 4;
+    f4v v[2][2] = {};
+    for (int q = 0; q < plan.parts; ++q, at += S::SLAB)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            v[e >> 1][e & 1] += *reinterpret_cast<const f4v *>(at + (int64_t)e * S::THREADS * 4);
+    Finish<E, K, S>{p, place, tile}(blockIdx.y / S::MF, blockIdx.y % S::MF, v);
+}
+
+// ---------------------------------------------------------------- host ----
+
+inline int64_t up(int64_t n, int64_t d) { return (n + d - 1) / d; }
+
+struct Choice {
+    bool large;
+    Plan plan;
+    int64_t split_tiles, slab_floats;
+};
+
+// What a plan's parts cost in microseconds: a work-group's beginning and end,
+// a K-tile while every place of the GPU has one, and a part's sums, written and read.
+struct Cost {
+    int places;            // work-groups that run at once
+    double fixed, step, part;
+};
+constexpr Cost kLargeCost = {256, 6.0, 1.15, 0.11};
+constexpr Cost kSmallCost = {512, 4.0, 0.60, 0.03};
+constexpr double kJoinUs = 5.0;
+
+template <typename S>
+Choice choice_for(Kind kind, const Product &p, int size, const Cost &c, double *us) {
+    Choice r = {};
+    const int64_t kt = kDeep / size;
+    const int64_t depth = up(p.k, kt) * (kind == Kind::kInput ? 2 : 1);
+    const int64_t tm = up(p.m, S::BM) * (kind == Kind::kWeight ? 2 : 1);
+    const int64_t tn = up(p.n, kind == Kind::kForward ? S::HN : S::BN), tiles = tm * tn;
+    const int64_t left = tiles % c.places;
+    auto rounds = [&](int64_t groups, int64_t steps) {
+        return (double)up(groups, c.places) * (c.fixed + (double)steps * c.step);
+    };
+    double best = rounds(tiles, depth);
+    r.plan = {(int32_t)tm, (int32_t)tn, (int32_t)tiles, 1, (int32_t)depth, (int32_t)depth};
+    for (int64_t split : {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
+        if (left == 0 || split * 4 > depth) break;
+        const int64_t share = up(depth, split), parts = up(depth, share);
+        const double t = rounds(tiles - left, depth) + rounds(left * parts, share) +
+                         (double)(left * parts) * c.part + kJoinUs;
+        if (t >= best) continue;
+        best = t;
+        r.plan.whole = (int32_t)(tiles - left);
+        r.plan.parts = (int32_t)parts;
+        r.plan.share = (int32_t)share;
+        r.split_tiles = left;
+        r.slab_floats = left * parts * S::SLAB;
+    }
+    r.large = S::BM == 256;
+    *us = best;
+    return r;
+}
+
+inline Choice choose(Kind kind, const Product &p, int size) {
+    double large_us, small_us;
+    const Choice large = choice_for<Large>(kind, p, size, kLargeCost, &large_us);
+    const Choice small = choice_for<Small>(kind, p, size, kSmallCost, &small_us);
+    return large_us <= small_us ? large : small;
+}
+
+template <typename E, Kind K, typename S>
+taco_status launch_product(const Product &p, const Choice &c, hipStream_t stream) {
+    const int64_t groups = c.plan.whole + c.split_tiles * c.plan.parts;
+    const taco_status st = launch(reinterpret_cast<const void *>(&product_kernel<E, K, S>),
+                                  dim3((unsigned)groups), S::THREADS, stream, p, c.plan);
+    if (st != TACO_OK || c.split_tiles == 0) return st;
+    return launch(reinterpret_cast<const void *>(&join_kernel<E, K, S>),
+                  dim3((unsigned)c.split_tiles, 2 * S::MF), S::THREADS, stream, p, c.plan);
+}
+
+template <typename E, Kind K>
+taco_status run_kind(const Product &p, hipStream_t stream) {
+    const Choice c = choose(K, p, Element<E>::SIZE);
+    return c.large ? launch_product<E, K, Large>(p, c, stream)
+                   : launch_product<E, K, Small>(p, c, stream);
+}
+
+}  // namespace
+
+template <typename E>
+int64_t Products<E>::workspace(Kind kind, const Product &p) {
+    return choose(kind, p, Element<E>::SIZE).slab_floats * (int64_t)sizeof(float);
+}
+
+template <typename E>
+taco_status Products<E>::run(Kind kind, const Product &p, hipStream_t stream) {
+    if constexpr (Element<E>::SCALED) {
+        return run_kind<E, Kind::kForward>(p, stream);
+    } else {
+        switch (kind) {
+            case Kind::kForward: return run_kind<E, Kind::kForward>(p, stream);
+            case Kind::kInput: return run_kind<E, Kind::kInput>(p, stream);
+            default: return run_kind<E, Kind::kWeight>(p, stream);
+        }
+    }
+}
+
+}  // namespace taco_gated

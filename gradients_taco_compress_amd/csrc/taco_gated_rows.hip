@@ -1,0 +1,176 @@
+// The element-wise kernels of libtaco_gated: the gradients of both projections
+// from that of their product, copies of operands to aligned rows, and the
+// block-scaled 8-bit encoding of weights.  All of them stream HBM once.
+#include "taco_gated_internal.hpp"
+#include "taco_gated_device.hpp"
+#include "taco_mx.hpp"
+
+namespace taco_gated {
+namespace {
+
+template <typename T>
+__device__ __forceinline__ void unpack8(u4v raw, float *f) {
+    typedef T t8 __attribute__((ext_vector_type(8)));
+    const t8 v = __builtin_bit_cast(t8, raw);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = (float)v[j];
+}
+template <typename T>
+__device__ __forceinline__ u4v pack8(const float *f) {
+    typedef T t8 __attribute__((ext_vector_type(8)));
+    typedef float f8 __attribute__((ext_vector_type(8)));
+    f8 v;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = f[j];
+    return __builtin_bit_cast(u4v, __builtin_convertvector(v, t8));
+}
+
+// Eight elements of a row, `n` of which exist (the others 0).
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, const T *row, int n, float *f) {
+    unpack8<T>(n >= 8 ? (u4v)*reinterpret_cast<const u4v_any *>(p)
+                      : load_tail<true>(reinterpret_cast<const char *>(p),
+                                        reinterpret_cast<const char *>(row), 2 * n),
+               f);
+}
+
+// A thread to eight neighbours; 2^lanes_log2 threads to a row.
+template <typename T, int ACT>
+__global__ __launch_bounds__(256) void activation_grad_kernel(ActivationGrad a, int lanes_log2) {
+    const int lanes = 1 << lanes_log2, lane = threadIdx.x & (lanes - 1), per = 256 >> lanes_log2;
+    const int chunks = (int)(a.to_pitch / 8);
+    for (int64_t row = (int64_t)blockIdx.x * per + (threadIdx.x >> lanes_log2); row < a.rows;
+         row += (int64_t)gridDim.x * per) {
+        const T *const da = static_cast<const T *>(a.da) + row * a.ldda;
+        const T *const gate = static_cast<const T *>(a.gate) + row * a.ldgu;
+        const T *const up = static_cast<const T *>(a.up) + row * a.ldgu;
+        T *const dgate = static_cast<T *>(a.dgate) + row * a.to_pitch;
+        T *const dup = static_cast<T *>(a.dup) + row * a.to_pitch;
+        for (int c = blockIdx.y * lanes + lane; c < chunks; c += gridDim.y * lanes) {
+            const int n = a.features - 8 * c;
+            float d[8], g[8], u[8], dg[8], du[8];
+            load8<T>(da + 8 * c, da, n, d);
+            load8<T>(gate + 8 * c, gate, n, g);
+            load8<T>(up + 8 * c, up, n, u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float share = gate_share<ACT>(g[j]);
+                dg[j] = d[j] * u[j] * gate_slope<ACT>(g[j], share);
+                du[j] = d[j] * (g[j] * share);
+                if (j >= n) dg[j] = du[j] = 0.0f;
+            }
+            *reinterpret_cast<u4v *>(dgate + 8 * c) = pack8<T>(dg);
+            *reinterpret_cast<u4v *>(dup + 8 * c) = pack8<T>(du);
+        }
+    }
+}
+
+struct Copies {
+    Repack r[3];
+    int32_t lanes_log2[3];
+};
+__global__ __launch_bounds__(256) void repack_kernel(Copies all) {
+    const Repack r = all.r[blockIdx.y];
+    const int log2 = all.lanes_log2[blockIdx.y], lanes = 1 << log2, lane = threadIdx.x & (lanes - 1);
+    const int per = 256 >> log2;
+    for (int64_t row = (int64_t)blockIdx.x * per + (threadIdx.x >> log2); row < r.rows;
+         row += (int64_t)gridDim.x * per) {
+        const char *from = static_cast<const char *>(r.from) + row * r.from_pitch;
+        char *to = static_cast<char *>(r.to) + row * r.to_pitch;
+        for (int64_t at = lane * 16; at < r.to_pitch; at += lanes * 16) {
+            const int64_t n = r.width - at;
+            *reinterpret_cast<u4v *>(to + at) =
+                n > 0 ? load_tail<true>(from + at, from, n < 16 ? (int)n : 16) : (u4v){0u, 0u, 0u, 0u};
+        }
+    }
+}
+
+__global__ __launch_bounds__(256) void zero_kernel(uint16_t *p, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+        p[i] = 0;
+}
+
+template <typename T>
+__device__ __forceinline__ void load8_any(const T *p, float *f) {
+    if constexpr (sizeof(T) == 4) {
+        const u4v a = reinterpret_cast<const u4v_any *>(p)[0], b = reinterpret_cast<const u4v_any *>(p)[1];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[j] = __uint_as_float(a[j]);
+            f[4 + j] = __uint_as_float(b[j]);
+        }
+    } else {
+        unpack8<T>(*reinterpret_cast<const u4v_any *>(p), f);
+    }
+}
+
+// A thread to eight neighbours, four threads to a block.
+template <typename T>
+__global__ __launch_bounds__(256) void encode_kernel(Encode e) {
+    const int64_t per = e.hidden / 8, n = e.rows * per;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / per, c = i - row * per;
+        float y[8];
+        load8_any<T>(static_cast<const T *>(e.x) + row * e.ldx + 8 * c, y);
+        const uint32_t byte = taco_mx::scale_byte(taco_mx::max_of_four(taco_mx::abs_max8(y)));
+        *reinterpret_cast<u2v_any *>(e.codes + 8 * i) = taco_mx::codes8(y, byte);
+        if ((i & 3) == 0) e.scales[i >> 2] = (uint8_t)byte;
+    }
+}
+
+unsigned groups_of(int64_t n, int64_t most) { return (unsigned)(n < most ? n : most); }
+
+}  // namespace
+
+taco_status activation_grad(const ActivationGrad &a, bool f16, hipStream_t stream) {
+    const int64_t chunks = a.to_pitch / 8;
+    int log2 = 0;
+    while (log2 < 8 && (INT64_C(1) << log2) < chunks) ++log2;
+    const int64_t per = 256 >> log2, across = (chunks + 255) / 256;
+    const dim3 grid(groups_of((a.rows + per - 1) / per, 8192), groups_of(across, 64));
+    const void *fn = nullptr;
+    switch (a.activation) {
+        case TACO_GATED_SILU:
+            fn = f16 ? reinterpret_cast<const void *>(&activation_grad_kernel<_Float16, TACO_GATED_SILU>)
+                     : reinterpret_cast<const void *>(&activation_grad_kernel<__bf16, TACO_GATED_SILU>);
+            break;
+        case TACO_GATED_GELU:
+            fn = f16 ? reinterpret_cast<const void *>(&activation_grad_kernel<_Float16, TACO_GATED_GELU>)
+                     : reinterpret_cast<const void *>(&activation_grad_kernel<__bf16, TACO_GATED_GELU>);
+            break;
+        default:
+            fn = f16 ? reinterpret_cast<const void *>(&activation_grad_kernel<_Float16, TACO_GATED_GELU_TANH>)
+                     : reinterpret_cast<const void *>(&activation_grad_kernel<__bf16, TACO_GATED_GELU_TANH>);
+    }
+    return launch(fn, grid, 256, stream, a, log2);
+}
+
+taco_status repack(const Repack *r, int count, hipStream_t stream) {
+    Copies all = {};
+    int64_t groups = 1;
+    for (int i = 0; i < count; ++i) {
+        all.r[i] = r[i];
+        int log2 = 0;
+        while (log2 < 8 && (INT64_C(16) << log2) < r[i].to_pitch) ++log2;
+        all.lanes_log2[i] = log2;
+        const int64_t per = 256 >> log2, g = (r[i].rows + per - 1) / per;
+        groups = g > groups ? g : groups;
+    }
+    return launch(reinterpret_cast<const void *>(&repack_kernel),
+                  dim3(groups_of(groups, 2048), (unsigned)count), 256, stream, all);
+}
+
+taco_status fill_zero(void *p, int64_t n16, hipStream_t stream) {
+    return launch(reinterpret_cast<const void *>(&zero_kernel), dim3(groups_of((n16 + 255) / 256, 4096)),
+                  256, stream, static_cast<uint16_t *>(p), n16);
+}
+
+taco_status encode(const Encode &e, taco_norm_dtype dtype, hipStream_t stream) {
+    const dim3 grid(groups_of((e.rows * (e.hidden / 8) + 255) / 256, 8192));
+    const void *fn = dtype == TACO_NORM_BF16  ? reinterpret_cast<const void *>(&encode_kernel<__bf16>)
+                     : dtype == TACO_NORM_F16 ? reinterpret_cast<const void *>(&encode_kernel<_Float16>)
+                                              : reinterpret_cast<const void *>(&encode_kernel<float>);
+    return launch(fn, grid, 256, stream, e);
+}
+
+}  // namespace taco_gated
