@@ -1,16 +1,18 @@
 """Binding of libtaco_norm (include/taco_norm.h): layer norm for training, with
 an 8-bit checkpoint of the normalised activation that serves both the norm's
-backward pass and the weight gradient of the linear layer behind it.
+backward pass and the weight gradient of the linear layer behind it; and
+root-mean-square norm with the residual's addition, for training and into 8 bits.
 
 Three layers:
 
 * ``taco_norm_*``: the C ABI with the same names and arguments (device
   pointers and stream handles as ints).
 * ``layer_norm``, ``layer_norm_backward``, ``layer_norm_checkpoint``,
-  ``layer_norm_checkpoint_backward``, ``checkpoint_weight_grad``: the same
-  calls on torch tensors, allocating outputs (and workspaces) when none are
-  given and launching on torch's current stream.
-* ``norm`` and ``norm_linear``: autograd functions made of them.
+  ``layer_norm_checkpoint_backward``, ``checkpoint_weight_grad``, ``rms_norm``,
+  ``rms_norm_mx``, ``rms_norm_backward``: the same calls on torch tensors,
+  allocating outputs (and workspaces) when none are given and launching on
+  torch's current stream.
+* ``norm``, ``rms`` and ``norm_linear``: autograd functions made of them.
   ``norm_linear`` is a layer norm and the linear layer behind it; it keeps one
   byte per activation element for its backward pass instead of the norm's
   input and output (four bytes in bf16).
@@ -64,6 +66,13 @@ _SIGNATURES = {
     "taco_norm_weight_grad_workspace": ([_P, _I64, _P, _I64, _I64, _I64], _I64),
     "taco_norm_weight_grad": ([_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _P, _I32, _P, _I32, _I32,
                                _P, _P, _I64, _P], _STATUS),
+    "taco_norm_rms_forward": ([_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I32, _F32, _P, _I64, _P,
+                               _I64, _P, _P], _STATUS),
+    "taco_norm_rms_mx": ([_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I32, _F32, _P, _P, _P, _I64,
+                          _P], _STATUS),
+    "taco_norm_rms_backward_workspace": ([_I64, _I64], _I64),
+    "taco_norm_rms_backward": ([_P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _I64, _I32, _I32, _P,
+                                _I64, _P, _P, _I64, _P], _STATUS),
 }
 #: Symbols the library exports (checked against include/taco_norm.h).
 EXPORTS = tuple(_SIGNATURES)
@@ -380,6 +389,87 @@ def checkpoint_weight_grad(dy, codes, weight=None, bias=None, out=None, dtype=No
     return out, db
 
 
+def _residual(residual, x, rows, hidden):
+    """(device pointer, elements between rows) of a residual like x, or (0, 0)."""
+    if residual is None:
+        return 0, 0
+    ld = _same_rows(residual, "residual", x.dtype, rows, hidden)
+    return residual.data_ptr(), ld
+
+
+def rms_norm(x, weight=None, eps: float = 1e-5, residual=None, out=None, total=None, rstd=None,
+             stream=None):
+    """Root-mean-square norm of x + residual over the last dimension: (y, total,
+    rstd), total = x + residual (None without a residual), rstd float32 [rows], as
+    the backward pass takes them.  out and total may be x or residual (in place)."""
+    rows, hidden, ldx = _pitch(x, "x")
+    w = _param(weight, hidden, x.dtype, "weight")
+    ptype = _param_type(weight, None, x.dtype)
+    r, ldr = _residual(residual, x, rows, hidden)
+    if residual is None and total is not None:
+        raise ValueError("total needs a residual")
+    at = _Launch(stream, (x, weight, residual, out, total, rstd))
+    out = at.empty(x.shape, x.dtype) if out is None else out
+    if residual is not None and total is None:
+        total = at.empty(x.shape, x.dtype)
+    rstd = at.empty(rows, torch.float32) if rstd is None else rstd
+    ldy = _same_rows(out, "out", x.dtype, rows, hidden)
+    ldt = 0 if total is None else _same_rows(total, "total", x.dtype, rows, hidden)
+    at.call(_lib.taco_norm_rms_forward, "taco_norm_rms_forward", x.data_ptr(), ldx, r, ldr, rows,
+            hidden, DTYPES[x.dtype], w, DTYPES[ptype], eps, out.data_ptr(), ldy, _ptr(total), ldt,
+            _vector(rstd, rows, "rstd"))
+    return out, total, rstd
+
+
+def rms_norm_mx(x, weight=None, eps: float = 1e-5, residual=None, total=None, stream=None):
+    """rms_norm into 8 bits: (codes, scales, total), codes uint8 [..., hidden] and
+    scales uint8 [..., hidden / 32], E4M3 codes of each 32 neighbours over their scale
+    2^(byte - 127), as gated.gated_forward_mx takes them.  total may be x or
+    residual (in place)."""
+    rows, hidden, ldx = _pitch(x, "x")
+    if hidden == 0 or hidden % 32:
+        raise ValueError(f"x must hold rows of a multiple of 32, got {list(x.shape)}")
+    w = _param(weight, hidden, x.dtype, "weight")
+    ptype = _param_type(weight, None, x.dtype)
+    r, ldr = _residual(residual, x, rows, hidden)
+    if residual is None and total is not None:
+        raise ValueError("total needs a residual")
+    at = _Launch(stream, (x, weight, residual, total))
+    codes = at.empty(x.shape, torch.uint8)
+    scales = at.empty((*x.shape[:-1], hidden // 32), torch.uint8)
+    if residual is not None and total is None:
+        total = at.empty(x.shape, x.dtype)
+    ldt = 0 if total is None else _same_rows(total, "total", x.dtype, rows, hidden)
+    at.call(_lib.taco_norm_rms_mx, "taco_norm_rms_mx", x.data_ptr(), ldx, r, ldr, rows, hidden,
+            DTYPES[x.dtype], w, DTYPES[ptype], eps, codes.data_ptr(), scales.data_ptr(),
+            _ptr(total), ldt)
+    return codes, scales, total
+
+
+def rms_norm_backward(dy, x, rstd, weight=None, dtotal=None, dx=None, param_grads: bool = True,
+                      param_dtype=None, stream=None):
+    """Gradients of rms_norm: (dx, dweight).  x: its total (x without a residual).
+    dtotal: the gradient that arrives at total.  dx is the gradient of x and of
+    residual alike, and may be dy or dtotal (in place); dweight is of param_dtype
+    (weight's type; float32 without a weight), None without param_grads."""
+    rows, hidden, lddy = _pitch(dy, "dy")
+    ldx = _same_rows(x, "x", dy.dtype, rows, hidden)
+    q = _vector(rstd, rows, "rstd")
+    w, ptype = _backward_param(weight, hidden, dy.dtype, param_dtype)
+    lddt = 0 if dtotal is None else _same_rows(dtotal, "dtotal", dy.dtype, rows, hidden)
+    at = _Launch(stream, (dy, x, rstd, weight, dtotal, dx))
+    dx = at.empty(dy.shape, dy.dtype) if dx is None else dx
+    lddx = _same_rows(dx, "dx", dy.dtype, rows, hidden)
+    dw = at.empty(hidden, ptype) if param_grads else None
+    ws = (at.workspace(_lib.taco_norm_rms_backward_workspace(rows, hidden)) if param_grads
+          else None)
+    at.call(_lib.taco_norm_rms_backward, "taco_norm_rms_backward", dy.data_ptr(), lddy,
+            x.data_ptr(), ldx, q, _ptr(dtotal), lddt, w, rows, hidden, DTYPES[dy.dtype],
+            DTYPES[ptype], dx.data_ptr(), lddx, _ptr(dw), _ptr(ws),
+            0 if ws is None else ws.numel())
+    return dx, dw
+
+
 # --------------------------------------------------------------- autograd --
 
 def _even(t):
@@ -414,6 +504,46 @@ class _Norm(torch.autograd.Function):
             param_dtype=ctx.bias_type if weight is None else None)
         return (dx, dw.view(ctx.shapes[0]) if want_w else None,
                 db.view(ctx.shapes[1]) if want_b else None, None)
+
+
+class _Rms(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, eps):
+        x = _even(x)
+        y, _, rstd = rms_norm(x, weight, eps)
+        ctx.save_for_backward(x, rstd, weight)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, rstd, weight = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx, dw = rms_norm_backward(_even(dy), x, rstd, weight, param_grads=need[1])
+        return dx if need[0] else None, dw.view(weight.shape) if need[1] else None, None
+
+
+class _RmsResidual(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, eps):
+        y, total, rstd = rms_norm(_even(x), weight, eps, residual=_even(residual))
+        ctx.save_for_backward(total, rstd, weight)
+        ctx.set_materialize_grads(False)
+        return y, total
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dtotal):
+        total, rstd, weight = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        if dy is None:                       # y was not used
+            dw = torch.zeros_like(weight) if need[2] else None
+            return dtotal if need[0] else None, dtotal if need[1] else None, dw, None
+        dtotal = None if dtotal is None else _even(dtotal)
+        dx, dw = rms_norm_backward(_even(dy), total, rstd, weight, dtotal=dtotal,
+                                   param_grads=need[2])
+        return (dx if need[0] else None, dx if need[1] else None,
+                dw.view(weight.shape) if need[2] else None, None)
 
 
 class _NormLinear(torch.autograd.Function):
@@ -453,6 +583,14 @@ class _NormLinear(torch.autograd.Function):
 def norm(x, weight=None, bias=None, eps: float = 1e-5):
     """Differentiable layer norm over the last dimension."""
     return _Norm.apply(x, weight, bias, eps)
+
+
+def rms(x, weight=None, eps: float = 1e-5, residual=None):
+    """Differentiable root-mean-square norm over the last dimension: y, or with
+    a residual (y, x + residual)."""
+    if residual is None:
+        return _Rms.apply(x, weight, eps)
+    return _RmsResidual.apply(x, residual, weight, eps)
 
 
 def norm_linear(x, weight, bias, linear_weight, linear_bias=None, eps: float = 1e-5):
