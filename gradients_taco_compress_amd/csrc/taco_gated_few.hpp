@@ -81,8 +81,8 @@ __global__ __launch_bounds__(WAVES * kWave) void few_kernel(Product p) {
     auto multiply = [&](const Turn &in) {
 #pragma unroll
         for (int t = 0; t < TURN; ++t) {
-            gate = El::run(in.v[t][0], in.v[t][2], gate, in.scale[t][0], in.scale[t][2]);
-            up = El::run(in.v[t][1], in.v[t][2], up, in.scale[t][1], in.scale[t][2]);
+            gate = El::template run<0, 0>(in.v[t][0], in.v[t][2], gate, in.scale[t][0], in.scale[t][2]);
+            up = El::template run<0, 0>(in.v[t][1], in.v[t][2], up, in.scale[t][1], in.scale[t][2]);
         }
     };
     const int64_t turns = (bytes + TURN * kDeep - 1) / (TURN * kDeep);

@@ -6,15 +6,21 @@
 //    K-tiles of 128 bytes of summed length (64 elements, or 128 codes).  Both
 //    operands of a K-tile are kept in LDS as two halves each (A0, A1, B0, B1),
 //    two K-tiles at a time, and a K-tile is worked off in four phases, the
-//    quadrants (A0,B0), (A0,B1), (A1,B1), (A1,B0) of the output.
+//    quadrants (A0, F), (A0, S), (A1, S), (A1, F) of the output.  F and S are
+//    B0 and B1, the other way round in every second K-tile: so the half of B
+//    that is done with first is the one that is needed first next.
 //  * The forward pass takes gate features as B0 and the same up features as
 //    B1, so that G and U of an element meet in one lane and A is formed from
 //    the float32 sums: G and U are not written unless training asks for them.
+//  * Registers hold one half of A and both of B.  Where a half of A is used for
+//    the last time, each of its fragments is replaced as its products have
+//    been issued, so the LDS reads run beside the products without a second set
+//    of registers.
 //  * Each phase loads one half of a later K-tile straight to LDS (16 bytes a
-//    lane, no registers), reads the fragments of the next phase, multiplies,
-//    and ends with the one barrier that serves both: the half read next has
-//    arrived, the half overwritten next has been read, by all waves.  Six halves
-//    are on their way at any time.
+//    lane, no registers); three to five halves are on their way at any time.  Two
+//    barriers a K-tile serve all of it: after (A0, F), A1 has arrived and A0 and F have
+//    been read, by all waves; after (A1, S), the next A0, F and S have arrived
+//    and this S and A1 have been read.
 //  * Operands whose summed index is contiguous (X and the weights, forward)
 //    lie in LDS as rows of 128 bytes, 16-byte chunk c of row R at chunk
 //    c ^ f(R); those whose summed index is the slow one lie as they do in memory
@@ -57,6 +63,7 @@ struct Element<BF16> {
     typedef __bf16 type;
     static constexpr int SIZE = 2;
     static constexpr bool SCALED = false;
+    template <int, int>
     static __device__ __forceinline__ f4v run(const Fragment &a, const Fragment &b, f4v c, int, int) {
         typedef __bf16 v8 __attribute__((ext_vector_type(8)));
 #pragma unroll
@@ -71,6 +78,7 @@ struct Element<F16> {
     typedef _Float16 type;
     static constexpr int SIZE = 2;
     static constexpr bool SCALED = false;
+    template <int, int>
     static __device__ __forceinline__ f4v run(const Fragment &a, const Fragment &b, f4v c, int, int) {
         typedef _Float16 v8 __attribute__((ext_vector_type(8)));
 #pragma unroll
@@ -85,11 +93,13 @@ struct Element<Codes> {
     typedef uint8_t type;
     static constexpr int SIZE = 1;
     static constexpr bool SCALED = true;
+    // BA, BB: which byte of the registers holds the scale.
+    template <int BA, int BB>
     static __device__ __forceinline__ f4v run(const Fragment &a, const Fragment &b, f4v c, int sa,
                                               int sb) {
-        // 0, 0: both operands E4M3; 0: the scales' lowest byte.
+        // 0, 0: both operands E4M3.
         return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-            __builtin_bit_cast(i8v, a), __builtin_bit_cast(i8v, b), c, 0, 0, 0, sa, 0, sb);
+            __builtin_bit_cast(i8v, a), __builtin_bit_cast(i8v, b), c, 0, 0, BA, sa, BB, sb);
     }
 };
 
@@ -236,18 +246,17 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
     __shared__ __align__(1024) uint8_t a00[S::A_HALF], a01[S::A_HALF], a10[S::A_HALF],
         a11[S::A_HALF], b00[S::B_HALF], b01[S::B_HALF], b10[S::B_HALF], b11[S::B_HALF];
     constexpr int SCALES = SCALED ? THREADS * 4 : 4;
-    __shared__ __align__(16) uint8_t s0[SCALES], s1[SCALES], s2[SCALES], s3[SCALES];
+    __shared__ __align__(16) uint8_t s0[SCALES], s1[SCALES];
     auto lds_a = [&](auto stage, auto half) -> uint8_t * {
-        constexpr int i = (decltype(stage)::value & 1) * 2 + decltype(half)::value;
+        constexpr int i = decltype(stage)::value * 2 + decltype(half)::value;
         return i == 0 ? a00 : i == 1 ? a01 : i == 2 ? a10 : a11;
     };
     auto lds_b = [&](auto stage, auto half) -> uint8_t * {
-        constexpr int i = (decltype(stage)::value & 1) * 2 + decltype(half)::value;
+        constexpr int i = decltype(stage)::value * 2 + decltype(half)::value;
         return i == 0 ? b00 : i == 1 ? b01 : i == 2 ? b10 : b11;
     };
     [[maybe_unused]] auto lds_s = [&](auto stage) -> uint8_t * {
-        constexpr int i = decltype(stage)::value & 3;
-        return i == 0 ? s0 : i == 1 ? s1 : i == 2 ? s2 : s3;
+        return decltype(stage)::value == 0 ? s0 : s1;
     };
 
     const int tid = threadIdx.x;
@@ -410,24 +419,29 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
         }
         return f;
     };
-    Fragment fa[2][MF], fb[2][NF];
-    int sa[2][MF] = {}, sb[2][NF] = {};
-    auto read_a = [&](auto stage, auto half) {
+    // Scales of two fragments share a register (bytes 0 and 2).
+    Fragment fa[MF], fb[2][NF];
+    int sa[MF / 2] = {}, sb[2][NF / 2] = {};
+    [[maybe_unused]] const int at_sa = (place.wm * (HM / S::WM) + place.r) * 4 + place.g;
+    [[maybe_unused]] const int at_sb = (2 * HM + place.wn * (HN / S::WN) + place.r) * 4 + place.g;
+    [[maybe_unused]] auto two_scales = [&](const uint8_t *q) {
+        typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+        return __builtin_bit_cast(int, (us2){q[0], q[16 * 4]});
+    };
+    auto read_a = [&](auto stage, auto half, auto index) {
+        constexpr int h = decltype(half)::value, i = decltype(index)::value;
+        fa[i] = read(Int<A_TURNED>{}, lds_a(stage, half), at_a, i);
+        // (a pair's scales with its second fragment: the first one's are in use until then)
+        if constexpr (SCALED && i % 2 == 1)
+            sa[i / 2] = two_scales(lds_s(stage) + at_sa + (h * HM + 16 * (i - 1)) * 4);
+    };
+    auto read_b = [&](auto stage, auto half) {
         constexpr int h = decltype(half)::value;
 #pragma unroll
-        for (int i = 0; i < MF; ++i) {
-            fa[h][i] = read(Int<A_TURNED>{}, lds_a(stage, half), at_a, i);
-            if constexpr (SCALED)
-                sa[h][i] = lds_s(stage)[(h * HM + place.wm * (HM / S::WM) + 16 * i + place.r) * 4 + place.g];
-        }
-    };
-    auto read_b = [&](auto stage, auto half, auto slot) {
-        constexpr int h = decltype(half)::value, to = decltype(slot)::value & 1;
-#pragma unroll
         for (int j = 0; j < NF; ++j) {
-            fb[to][j] = read(Int<B_TURNED>{}, lds_b(stage, half), at_b, j);
+            fb[h][j] = read(Int<B_TURNED>{}, lds_b(stage, half), at_b, j);
             if constexpr (SCALED)
-                sb[to][j] = lds_s(stage)[((2 + h) * HM + place.wn * (HN / S::WN) + 16 * j + place.r) * 4 + place.g];
+                if (j % 2 == 0) sb[h][j / 2] = two_scales(lds_s(stage) + at_sb + (h * HM + 16 * j) * 4);
         }
     };
     f4v sum[2][2][MF][NF];
@@ -437,73 +451,73 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
         for (int i = 0; i < MF; ++i)
 #pragma unroll
             for (int j = 0; j < NF; ++j) sum[q >> 1][q & 1][i][j] = (f4v){0.0f, 0.0f, 0.0f, 0.0f};
-    auto multiply = [&](auto qa, auto qb, auto slot) {
-        constexpr int a = decltype(qa)::value, b = decltype(qb)::value, s = decltype(slot)::value & 1;
-#pragma unroll
-        for (int i = 0; i < MF; ++i)
-#pragma unroll
-            for (int j = 0; j < NF; ++j)
-                sum[a][b][i][j] = El::run(fb[s][j], fa[a][i], sum[a][b][i][j], sb[s][j], sa[a][i]);
+    // Products of a row fragment with a half of B.
+    auto multiply = [&](auto qa, auto qb, auto fi) {
+        constexpr int a = decltype(qa)::value, b = decltype(qb)::value, i = decltype(fi)::value;
+        for_each<NF>([&](auto fj) {
+            constexpr int j = decltype(fj)::value;
+            sum[a][b][i][j] = El::template run<(j & 1) * 2, (i & 1) * 2>(
+                fb[b][j], fa[i], sum[a][b][i][j], sb[b][j / 2], sa[i / 2]);
+        });
     };
 
-    // K-tile t of this work-group (counted from kt0) lies in stage t % 2, its
-    // scales in stage t % 4; its B0 fragments in slot t % 2, its B1 fragments
-    // in the other.  Loads are in the order S, A0, B0, B1, A1 of each K-tile, so
-    // "the half has arrived" is a count of those after it.
+    // K-tile t of this work-group (counted from kt0) lies in stage t % 2.  Loads are
+    // in the order A0, F, scales, S, A1 of each K-tile, so "the half has
+    // arrived" is a count of those after it.
     using C0 = Int<0>;
     using C1 = Int<1>;
     constexpr int L = S::LOADS, SL = SCALED ? 1 : 0;
-    load_scales(C0{}, kt0);
     load_a(C0{}, C0{}, kt0);
     load_b(C0{}, C0{}, kt0);
+    load_scales(C0{}, kt0);
     load_b(C0{}, C1{}, kt0);
     load_a(C0{}, C1{}, kt0);
-    load_scales(C1{}, kt0 + 1);
     load_a(C1{}, C0{}, kt0 + 1);
-    load_b(C1{}, C0{}, kt0 + 1);
     load_b(C1{}, C1{}, kt0 + 1);
-    load_a(C1{}, C1{}, kt0 + 1);
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(6 * L + SL) : "memory");
-    read_a(C0{}, C0{});
-    read_b(C0{}, C0{}, C0{});
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    load_scales(Int<2>{}, kt0 + 2);
-    load_a(C0{}, C0{}, kt0 + 2);
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(6 * L + 2 * SL) : "memory");
+    load_scales(C1{}, kt0 + 1);
+    load_b(C1{}, C0{}, kt0 + 1);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(4 * L + SL) : "memory");
+    for_each<MF>([&](auto i) { read_a(C0{}, C0{}, i); });
+    read_b(C0{}, C0{});
 
-    auto phase_end = [&](auto more) {
-        __builtin_amdgcn_sched_barrier(0);
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(6 * L + decltype(more)::value)
-                     : "memory");
-        __builtin_amdgcn_sched_barrier(0);
+    auto pin = [] { __builtin_amdgcn_sched_barrier(0); };
+    auto barrier = [&](auto later) {
+        pin();
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(decltype(later)::value) : "memory");
+        pin();
     };
-    auto k_tile = [&](auto index, int kt) {
-        constexpr int s = decltype(index)::value;
-        using Now = Int<s & 3>;
-        using Next = Int<(s + 1) & 3>;
-        using After = Int<(s + 2) & 3>;
-        using Third = Int<(s + 3) & 3>;
-        // (A0, B0)
-        load_b(After{}, C0{}, kt + 2);
-        read_b(Now{}, C1{}, Int<s + 1>{});
-        multiply(C0{}, C0{}, Int<s>{});
-        phase_end(Int<2 * SL>{});
-        // (A0, B1)
-        load_b(After{}, C1{}, kt + 2);
-        read_a(Now{}, C1{});
-        multiply(C0{}, C1{}, Int<s + 1>{});
-        phase_end(Int<SL>{});
-        // (A1, B1)
-        load_a(After{}, C1{}, kt + 2);
-        read_a(Next{}, C0{});
-        multiply(C1{}, C1{}, Int<s + 1>{});
-        phase_end(Int<SL>{});
-        // (A1, B0)
-        load_scales(Third{}, kt + 3);
-        load_a(Third{}, C0{}, kt + 3);
-        read_b(Next{}, C0{}, Int<s + 1>{});
-        multiply(C1{}, C0{}, Int<s>{});
-        phase_end(Int<2 * SL>{});
+    auto k_tile = [&](auto stage, int kt) {
+        using Now = decltype(stage);
+        using Next = Int<1 - Now::value>;
+        using F = Int<Now::value>;
+        using G = Int<1 - Now::value>;               // S above
+        // (A0, F)
+        load_a(Next{}, C1{}, kt + 1);
+        read_b(Now{}, G{});
+        for_each<MF>([&](auto i) { multiply(C0{}, F{}, i); });
+        barrier(Int<4 * L + SL>{});
+        // (A0, S), A1 into the place of A0
+        load_a(Now{}, C0{}, kt + 2);
+        for_each<MF>([&](auto i) {
+            multiply(C0{}, G{}, i);
+            pin();
+            read_a(Now{}, C1{}, i);
+        });
+        pin();
+        // (A1, S)
+        load_b(Now{}, F{}, kt + 2);
+        for_each<MF>([&](auto i) { multiply(C1{}, G{}, i); });
+        barrier(Int<3 * L>{});
+        // (A1, F), the next A0 into the place of A1, the next F into that of S
+        load_scales(Now{}, kt + 2);
+        load_b(Now{}, G{}, kt + 2);
+        read_b(Next{}, G{});
+        for_each<MF>([&](auto i) {
+            multiply(C1{}, F{}, i);
+            pin();
+            read_a(Next{}, C0{}, i);
+        });
+        pin();
     };
     // The tiles read ahead past the last are zeros.
     for (int kt = kt0;;) {
@@ -511,12 +525,6 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
         if (++kt >= kt1) break;
         k_tile(C1{}, kt);
         if (++kt >= kt1) break;
-        if constexpr (SCALED) {
-            k_tile(Int<2>{}, kt);
-            if (++kt >= kt1) break;
-            k_tile(Int<3>{}, kt);
-            if (++kt >= kt1) break;
-        }
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
