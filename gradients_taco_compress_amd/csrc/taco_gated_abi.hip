@@ -161,18 +161,6 @@ BackwardOperands backward_operands(const void *x, int64_t ldx, const void *gate,
     return o;
 }
 
-// Scale rows of hidden / 32 bytes, which the kernel reads four at a time.
-struct Scales {
-    const uint8_t *p;
-    int64_t rows, width;
-    bool copied;
-    int64_t copy_bytes() const { return copied ? rows * round_up(width, 16) : 0; }
-};
-Scales scales(const uint8_t *p, int64_t rows, int64_t hidden) {
-    const int64_t width = hidden / 32;
-    return {p, rows, width, width % 4 != 0 || !aligned(p, 4)};
-}
-
 bool valid_mx(int64_t rows, int64_t hidden, int64_t features) {
     return valid_sizes(rows, hidden, features) && hidden % 32 == 0;
 }
@@ -329,16 +317,13 @@ taco_status taco_gated_backward(const void *da, int64_t ldda, const void *x, int
     return with_type(dtype, [&](auto k) { return decltype(k)::run(Kind::kWeight, p, stream); });
 }
 
-int64_t taco_gated_forward_mx_workspace(const uint8_t *x_scales, const uint8_t *gate_scales,
-                                        const uint8_t *up_scales, int64_t rows, int64_t hidden,
-                                        int64_t features) {
+int64_t taco_gated_forward_mx_workspace(int64_t rows, int64_t hidden, int64_t features) {
     if (!valid_mx(rows, hidden, features)) return -1;
     if (rows <= kFewRows) return 0;
     Product p = {};
     p.m = rows; p.n = features; p.k = hidden;
-    return Products<Codes>::workspace(Kind::kForward, p) + scales(x_scales, rows, hidden).copy_bytes() +
-           scales(gate_scales, features, hidden).copy_bytes() +
-           scales(up_scales, features, hidden).copy_bytes();
+    return Products<Codes>::workspace(Kind::kForward, p) + scale_tile_bytes(rows, hidden / 32) +
+           2 * scale_tile_bytes(features, hidden / 32);
 }
 
 taco_status taco_gated_forward_mx(const uint8_t *x_codes, const uint8_t *x_scales,
@@ -351,8 +336,7 @@ taco_status taco_gated_forward_mx(const uint8_t *x_codes, const uint8_t *x_scale
     if (!valid_mx(rows, hidden, features) || !valid_rows(rows, features, lda)) return TACO_ERR_SHAPE;
     if (!valid(activation)) return TACO_ERR_PARAM;
     if (rows == 0) return TACO_OK;
-    const int64_t need =
-        taco_gated_forward_mx_workspace(x_scales, gate_scales, up_scales, rows, hidden, features);
+    const int64_t need = taco_gated_forward_mx_workspace(rows, hidden, features);
     if (!x_codes || !x_scales || !gate_codes || !gate_scales || !up_codes || !up_scales || !a ||
         (need && !workspace))
         return TACO_ERR_NULL;
@@ -381,16 +365,15 @@ taco_status taco_gated_forward_mx(const uint8_t *x_codes, const uint8_t *x_scale
     Arena arena = {static_cast<char *>(workspace), {}, 0};
     p.slabs = static_cast<float *>(arena.take(Products<Codes>::workspace(Kind::kForward, p)));
     Matrix *const to[] = {&p.a_scale, &p.b_scale[0], &p.b_scale[1]};
-    const Scales from[] = {scales(x_scales, rows, hidden), scales(gate_scales, features, hidden),
-                           scales(up_scales, features, hidden)};
+    ScaleTiles tiles[3];
     for (int i = 0; i < 3; ++i) {
-        if (!from[i].copied) continue;
-        const int64_t pitch = round_up(blocks, 16);
-        void *const copy = arena.take(from[i].copy_bytes());
-        arena.copies[arena.count++] = {from[i].p, copy, blocks, pitch, from[i].rows, blocks};
-        *to[i] = {copy, pitch};
+        const int64_t n = i == 0 ? rows : features;
+        void *const place = arena.take(scale_tile_bytes(n, blocks));
+        tiles[i] = {static_cast<const uint8_t *>(to[i]->p), static_cast<uint32_t *>(place), n,
+                    (int32_t)blocks, i > 0};
+        *to[i] = {place, scale_tile_pitch(n)};
     }
-    const taco_status st = arena.copy(stream);
+    const taco_status st = tile_scales(tiles, 3, stream);
     return st != TACO_OK ? st : Products<Codes>::run(Kind::kForward, p, stream);
 }
 

@@ -35,7 +35,9 @@ struct Product {
     // kForward: a = X, b = Wg, Wu.  kInput: a = dG, dU, b = Wg, Wu.
     // kWeight: a = dG, dU, b = X (twice).
     Matrix a[2], b[2];
-    Matrix a_scale, b_scale[2];        // kForward of codes: E8M0 bytes
+    // kForward of codes, E8M0 bytes.  few(): rows as they are; run(): by K-tile, as
+    // tile_scales() lays them out (pitch: bytes of a K-tile).
+    Matrix a_scale, b_scale[2];
     void *out[3];                      // kForward: A, G, U (the last two may be null)
     int64_t out_pitch[3];              // in elements
     int64_t m, n, k;                   // rows, columns and summed length of one out
@@ -78,6 +80,29 @@ struct Repack {
     int64_t width;
 };
 taco_status repack(const Repack *r, int count, hipStream_t stream);      // count <= 3
+
+// Feature of LDS row R of a forward B half: of each 32 features, column fragment
+// j takes 8 q + 4 j + (0..3), so that a lane's two fragments are eight
+// neighbours.
+__host__ __device__ constexpr int feature_of_row(int R) {
+    return (R & ~31) | (((R >> 2) & 3) << 3) | (((R >> 4) & 1) << 2) | (R & 3);
+}
+
+// Rows of `width` scale bytes (one a block of 32) to where a K-tile of 128 codes
+// finds its own together, in the order in which lanes take them:
+// [K-tile][64 rows][block g][row r of 16][rows r, 16 + r, 32 + r, 48 + r], zeros
+// where there is no row or block.  features: rows in the order of feature_of_row.
+struct ScaleTiles {
+    const uint8_t *from;
+    uint32_t *to;
+    int64_t rows;
+    int32_t width, features;
+};
+inline int64_t scale_tile_pitch(int64_t rows) { return (rows + 63) / 64 * 256; }
+inline int64_t scale_tile_bytes(int64_t rows, int64_t width) {
+    return (width + 3) / 4 * scale_tile_pitch(rows);
+}
+taco_status tile_scales(const ScaleTiles *s, int count, hipStream_t stream);      // count <= 3
 
 taco_status fill_zero(void *p, int64_t n16, hipStream_t stream);         // n16 16-bit zeros
 

@@ -141,12 +141,6 @@ __device__ __forceinline__ Tile tile_at(const Plan &s, int t) {
     return {strip * kStrip + in % rows, in / rows};
 }
 
-// Feature of LDS row R of a forward B half: of each 32 features, fragment j
-// takes 8 q + 4 j + (0..3), so that a lane's two fragments are eight neighbours.
-__device__ __forceinline__ int feature_of_row(int R) {
-    return (R & ~31) | (((R >> 2) & 3) << 3) | (((R >> 4) & 1) << 2) | (R & 3);
-}
-
 __device__ __forceinline__ int clamp(int64_t v, int most) {
     return v < 0 ? 0 : v < most ? (int)v : most;
 }
@@ -226,13 +220,6 @@ struct Finish {
     }
 };
 
-// What a half's loads read: rows `pitch` apart from `base`, `records` bytes in
-// all, and of each row the first `limit` 16-byte chunks.
-struct Source {
-    const char *base;
-    int records, limit;
-};
-
 template <typename E, Kind K, typename S>
 __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan plan) {
     using El = Element<E>;
@@ -240,23 +227,24 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
     constexpr int SIZE = El::SIZE, KT = kDeep / SIZE;          // summed elements of a K-tile
     constexpr bool A_TURNED = K == Kind::kWeight, B_TURNED = K != Kind::kForward;
     constexpr bool SCALED = El::SCALED;
-    // A variable for each half, not one for all: the compiler then knows that a
-    // load into one does not touch the fragments being read from another, and
-    // does not wait for it.
+    // Several variables, not one for all: the compiler then knows that a load
+    // into one does not touch the fragments being read from another, and does
+    // not wait for it.  It tells few of them apart, so what is never loaded and
+    // read at the same time shares one: F, S and the scales, in the order in
+    // which they are loaded first.
+    constexpr int SCALES = SCALED ? THREADS * 4 : 0;           // [A0 | A1 | B0 | B1], bytes
     __shared__ __align__(1024) uint8_t a00[S::A_HALF], a01[S::A_HALF], a10[S::A_HALF],
-        a11[S::A_HALF], b00[S::B_HALF], b01[S::B_HALF], b10[S::B_HALF], b11[S::B_HALF];
-    constexpr int SCALES = SCALED ? THREADS * 4 : 4;
-    __shared__ __align__(16) uint8_t s0[SCALES], s1[SCALES];
+        a11[S::A_HALF], b0[2 * S::B_HALF + SCALES], b1[2 * S::B_HALF + SCALES];
     auto lds_a = [&](auto stage, auto half) -> uint8_t * {
         constexpr int i = decltype(stage)::value * 2 + decltype(half)::value;
         return i == 0 ? a00 : i == 1 ? a01 : i == 2 ? a10 : a11;
     };
     auto lds_b = [&](auto stage, auto half) -> uint8_t * {
-        constexpr int i = decltype(stage)::value * 2 + decltype(half)::value;
-        return i == 0 ? b00 : i == 1 ? b01 : i == 2 ? b10 : b11;
+        constexpr int s = decltype(stage)::value, h = decltype(half)::value;
+        return (s == 0 ? b0 : b1) + h * S::B_HALF;
     };
-    [[maybe_unused]] auto lds_s = [&](auto stage) -> uint8_t * {
-        return decltype(stage)::value == 0 ? s0 : s1;
+    [[maybe_unused]] auto lds_s = [&](auto stage) -> uint8_t * {      // scales
+        return (decltype(stage)::value == 0 ? b0 : b1) + 2 * S::B_HALF;
     };
 
     const int tid = threadIdx.x;
@@ -309,41 +297,23 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
         off_b[i] = (uint32_t)(row * (int)p.b[0].pitch + chunk_b * 16);
     }
 
-    // Where half h of K-tile kt comes from.
+    // Loads of half h of K-tile kt.  All of it is the same for every lane but
+    // the offset, which is out of bounds for chunks past a row's end, and all
+    // choices are selects: a branch here would part the products from what is
+    // to run beside them.
     const int per_m = (int)((p.m + S::BM - 1) / S::BM);
     const int which = K == Kind::kWeight && tile.m >= per_m;
     const int64_t m0 = (int64_t)(tile.m - which * per_m) * S::BM;
     const int64_t n0 = (int64_t)tile.n * (K == Kind::kForward ? HN : S::BN);
-    auto source_a = [&](int h, int kt) -> Source {
-        const int seg = K == Kind::kInput ? kt >= seg_depth : which;
-        if (K == Kind::kInput && seg) kt -= seg_depth;
-        const char *const base = static_cast<const char *>(p.a[seg].p);
-        const int64_t pitch = p.a[0].pitch, k = (int64_t)kt * KT, m = m0 + h * HM;
-        if constexpr (A_TURNED)
-            return {base + k * pitch + m * SIZE, clamp(p.k - k, KT) * (int)pitch,
-                    clamp((p.m - m + 7) / 8, HM / 8)};
-        return {base + m * pitch + k * SIZE, clamp(p.m - m, HM) * (int)pitch,
-                clamp((p.k - k + 16 / SIZE - 1) / (16 / SIZE), 8)};
-    };
-    auto source_b = [&](int h, int kt) -> Source {
-        const int seg = K == Kind::kInput ? kt >= seg_depth : K == Kind::kForward ? h : 0;
-        if (K == Kind::kInput && seg) kt -= seg_depth;
-        const char *const base = static_cast<const char *>(p.b[seg].p);
-        const int64_t pitch = p.b[0].pitch, k = (int64_t)kt * KT;
-        if constexpr (B_TURNED) {
-            const int64_t n = n0 + h * HN;
-            return {base + k * pitch + n * SIZE, clamp(p.k - k, KT) * (int)pitch,
-                    clamp((p.n - n + 7) / 8, HN / 8)};
-        }
-        return {base + n0 * pitch + k * SIZE, clamp(p.n - n0, HN) * (int)pitch,
-                clamp((p.k - k + 16 / SIZE - 1) / (16 / SIZE), 8)};
-    };
-    // (The host pass does not know the resource type.)
-    auto load = [&](uint8_t *buf, Source s, const uint32_t (&off)[2], int chunk) {
-#if defined(__HIP_DEVICE_COMPILE__)
+    const int pitch_a = (int)p.a[0].pitch, pitch_b = (int)p.b[0].pitch;
+    // Along the summed index: whole K-tiles (of a segment), elements of the one
+    // after them, 16-byte chunks.
+    [[maybe_unused]] const int k_whole = (int)(p.k / KT), k_rest = (int)(p.k % KT);
+    [[maybe_unused]] const int k_chunks = (int)((p.k * SIZE + 15) / 16);
+    auto load = [&](uint8_t *buf, const char *base, int records, const uint32_t (&off)[2], bool in) {
+#if defined(__HIP_DEVICE_COMPILE__)      // the host pass does not know the resource type
         // 0x00020000: raw 32-bit data.
-        const auto r = __builtin_amdgcn_make_buffer_rsrc((void *)s.base, 0, s.records, 0x00020000);
-        const bool in = chunk < s.limit;
+        const auto r = __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, records, 0x00020000);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -351,37 +321,58 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
                 16, in ? off[i] : 0x80000000u, 0, 0, 0);
 #endif
     };
+    // (past the last K-tile: nothing, which arrives as zeros)
+    auto load_half = [&](auto turned, uint8_t *buf, const void *p0, const void *p1, int64_t first,
+                         int64_t count, int pitch, const uint32_t (&off)[2], int chunk, int kt) {
+        const bool seg = K == Kind::kInput && kt >= seg_depth;
+        const int in_seg = seg ? kt - seg_depth : kt;
+        const char *base = static_cast<const char *>(seg ? p1 : p0);
+        const int here = clamp(count - first, HM);             // rows or columns of this half
+        int records;
+        bool in;
+        if constexpr (decltype(turned)::value != 0) {
+            base += (int64_t)in_seg * KT * pitch + first * SIZE;
+            records = (in_seg < k_whole ? KT : in_seg == k_whole ? k_rest : 0) * pitch;
+            in = chunk < (here + 7) / 8;
+        } else {
+            base += first * pitch + (int64_t)in_seg * kDeep;
+            records = here * pitch;
+            in = chunk + in_seg * 8 < k_chunks;
+        }
+        load(buf, base, kt < kt1 ? records : 0, off, in);
+    };
     auto load_a = [&](auto stage, auto half, int kt) {
-        // (past the last K-tile: nothing, which arrives as zeros)
-        Source s = source_a(decltype(half)::value, kt < kt1 ? kt : kt0);
-        if (kt >= kt1) s.records = 0;
-        load(lds_a(stage, half), s, off_a, chunk_a);
+        constexpr int h = decltype(half)::value;
+        const void *const p0 = K == Kind::kWeight ? p.a[which].p : p.a[0].p;
+        load_half(Int<A_TURNED>{}, lds_a(stage, half), p0, p.a[1].p, m0 + h * HM, p.m, pitch_a,
+                  off_a, chunk_a, kt);
     };
     auto load_b = [&](auto stage, auto half, int kt) {
-        Source s = source_b(decltype(half)::value, kt < kt1 ? kt : kt0);
-        if (kt >= kt1) s.records = 0;
-        load(lds_b(stage, half), s, off_b, chunk_b);
+        constexpr int h = decltype(half)::value;
+        // (forward: the same rows of the other weight)
+        const void *const p0 = K == Kind::kForward ? p.b[h].p : p.b[0].p;
+        load_half(Int<B_TURNED>{}, lds_b(stage, half), p0, p.b[1].p,
+                  K == Kind::kForward ? n0 : n0 + h * HN, p.n, pitch_b, off_b, chunk_b, kt);
     };
-    // Scales of a K-tile: one 4-byte load a thread, [A0 | A1 | B0 | B1][row][block].
+    // Scales of a K-tile: one 4-byte load a thread.
     [[maybe_unused]] const char *scale_base = nullptr;
+    [[maybe_unused]] int64_t scale_pitch = 0;
     [[maybe_unused]] int scale_records = 0;
-    [[maybe_unused]] uint32_t scale_off = 0;
     if constexpr (SCALED) {
-        const int quarter = __builtin_amdgcn_readfirstlane(tid / HM), row = tid % HM;
+        const int quarter = __builtin_amdgcn_readfirstlane(tid / HM);
         const bool b = quarter >= 2;
         const Matrix &s = b ? p.b_scale[quarter - 2] : p.a_scale;
         const int64_t first = b ? n0 : m0 + quarter * HM;
-        scale_base = static_cast<const char *>(s.p) + first * s.pitch;
-        scale_records = clamp((b ? p.n : p.m) - first, HM) * (int)s.pitch;
-        scale_off = (uint32_t)((b ? feature_of_row(row) : row) * (int)s.pitch);
+        scale_base = static_cast<const char *>(s.p) + first * 4;
+        scale_pitch = s.pitch;
+        scale_records = clamp(s.pitch / 4 - first, HM) * 4;
     }
+    [[maybe_unused]] const uint32_t scale_off = tid % HM * 4;
     auto load_scales = [&](auto stage, int kt) {
 #if defined(__HIP_DEVICE_COMPILE__)
         if constexpr (SCALED) {
-            const bool in = kt < kt1;
             const auto r = __builtin_amdgcn_make_buffer_rsrc(
-                (void *)(scale_base + (in ? (int64_t)kt * 4 : 0)), 0, in ? scale_records : 0,
-                0x00020000);
+                (void *)(scale_base + kt * scale_pitch), 0, kt < kt1 ? scale_records : 0, 0x00020000);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 r, (__attribute__((address_space(3))) void *)(lds_s(stage) + wave * kWave * 4), 4,
                 scale_off, 0, 0, 0);
@@ -419,30 +410,41 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
         }
         return f;
     };
-    // Scales of two fragments share a register (bytes 0 and 2).
+    // The scales of a wave's fragments of a half share a register, a byte each.
     Fragment fa[MF], fb[2][NF];
-    int sa[MF / 2] = {}, sb[2][NF / 2] = {};
-    [[maybe_unused]] const int at_sa = (place.wm * (HM / S::WM) + place.r) * 4 + place.g;
-    [[maybe_unused]] const int at_sb = (2 * HM + place.wn * (HN / S::WN) + place.r) * 4 + place.g;
-    [[maybe_unused]] auto two_scales = [&](const uint8_t *q) {
-        typedef unsigned short us2 __attribute__((ext_vector_type(2)));
-        return __builtin_bit_cast(int, (us2){q[0], q[16 * 4]});
+    int sa[2] = {}, sb[2] = {};
+    // Where they are among those of a K-tile (see ScaleTiles), from the first
+    // fragment's row on.  (Opaque: a sum taken apart into several additions to the
+    // pointer hides from the compiler which variable is read.)
+    auto scales_at = [&](int row) {
+        int at = 2 * S::B_HALF + (row / 64 * 64 + place.g * 16 + place.r) * 4 + row % 64 / 16;
+        asm volatile("" : "+v"(at));
+        return at;
+    };
+    [[maybe_unused]] int at_sa = 0, at_sb = 0;
+    if constexpr (SCALED) {
+        at_sa = scales_at(place.wm * (HM / S::WM));
+        at_sb = scales_at(2 * HM + place.wn * (HN / S::WN));
+    }
+    auto read_scales = [&](auto stage, int at, auto count) {
+        [[maybe_unused]] const uint8_t *const q = (decltype(stage)::value == 0 ? b0 : b1) + at;
+        if constexpr (decltype(count)::value == 4) return *reinterpret_cast<const int *>(q);
+        else return (int)*reinterpret_cast<const uint16_t *>(q);
+    };
+    auto read_a_scales = [&](auto stage, auto half) {
+        constexpr int h = decltype(half)::value;
+        if constexpr (SCALED) sa[h] = read_scales(stage, at_sa + h * HM * 4, Int<MF>{});
     };
     auto read_a = [&](auto stage, auto half, auto index) {
-        constexpr int h = decltype(half)::value, i = decltype(index)::value;
+        constexpr int i = decltype(index)::value;
         fa[i] = read(Int<A_TURNED>{}, lds_a(stage, half), at_a, i);
-        // (a pair's scales with its second fragment: the first one's are in use until then)
-        if constexpr (SCALED && i % 2 == 1)
-            sa[i / 2] = two_scales(lds_s(stage) + at_sa + (h * HM + 16 * (i - 1)) * 4);
     };
     auto read_b = [&](auto stage, auto half) {
         constexpr int h = decltype(half)::value;
 #pragma unroll
-        for (int j = 0; j < NF; ++j) {
-            fb[h][j] = read(Int<B_TURNED>{}, lds_b(stage, half), at_b, j);
-            if constexpr (SCALED)
-                if (j % 2 == 0) sb[h][j / 2] = two_scales(lds_s(stage) + at_sb + (h * HM + 16 * j) * 4);
-        }
+        for (int j = 0; j < NF; ++j) fb[h][j] = read(Int<B_TURNED>{}, lds_b(stage, half), at_b, j);
+        if constexpr (SCALED)
+            sb[h] = read_scales(stage, at_sb + h * HM * 4, Int<NF>{});
     };
     f4v sum[2][2][MF][NF];
 #pragma unroll
@@ -456,8 +458,8 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
         constexpr int a = decltype(qa)::value, b = decltype(qb)::value, i = decltype(fi)::value;
         for_each<NF>([&](auto fj) {
             constexpr int j = decltype(fj)::value;
-            sum[a][b][i][j] = El::template run<(j & 1) * 2, (i & 1) * 2>(
-                fb[b][j], fa[i], sum[a][b][i][j], sb[b][j / 2], sa[i / 2]);
+            sum[a][b][i][j] =
+                El::template run<j, i>(fb[b][j], fa[i], sum[a][b][i][j], sb[b], sa[a]);
         });
     };
 
@@ -477,6 +479,7 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
     load_scales(C1{}, kt0 + 1);
     load_b(C1{}, C0{}, kt0 + 1);
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(4 * L + SL) : "memory");
+    read_a_scales(C0{}, C0{});
     for_each<MF>([&](auto i) { read_a(C0{}, C0{}, i); });
     read_b(C0{}, C0{});
 
@@ -498,6 +501,7 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
         barrier(Int<4 * L + SL>{});
         // (A0, S), A1 into the place of A0
         load_a(Now{}, C0{}, kt + 2);
+        read_a_scales(Now{}, C1{});
         for_each<MF>([&](auto i) {
             multiply(C0{}, G{}, i);
             pin();
@@ -512,6 +516,7 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
         load_scales(Now{}, kt + 2);
         load_b(Now{}, G{}, kt + 2);
         read_b(Next{}, G{});
+        read_a_scales(Next{}, C0{});
         for_each<MF>([&](auto i) {
             multiply(C1{}, F{}, i);
             pin();
@@ -519,12 +524,11 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
         });
         pin();
     };
-    // The tiles read ahead past the last are zeros.
-    for (int kt = kt0;;) {
+    // K-tiles past the last (the second of an odd number, and what is read ahead) are
+    // zeros.
+    for (int kt = kt0; kt < kt1; kt += 2) {
         k_tile(C0{}, kt);
-        if (++kt >= kt1) break;
-        k_tile(C1{}, kt);
-        if (++kt >= kt1) break;
+        k_tile(C1{}, kt + 1);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 

@@ -85,6 +85,45 @@ __global__ __launch_bounds__(256) void repack_kernel(Copies all) {
     }
 }
 
+// A thread to four rows' bytes (rows r, 16 + r, 32 + r, 48 + r of 64) of four K-tiles.
+struct AllScales {
+    ScaleTiles s[3];
+};
+__global__ __launch_bounds__(256) void tile_scales_kernel(AllScales all) {
+    const ScaleTiles s = all.s[blockIdx.y];
+    const int64_t row_groups = (s.rows + 63) / 64, parts = (s.width + 15) / 16;
+    const int64_t n = row_groups * 16 * parts;
+    const int tiles = (s.width + 3) / 4;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t part = i / (row_groups * 16), at = i - part * row_groups * 16;
+        const int64_t group = at / 16;
+        const int r = (int)(at % 16);
+        u4v v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int in = 16 * q + r;
+            const int64_t row = group * 64 + (s.features ? feature_of_row(in) : in);
+            const char *const from = reinterpret_cast<const char *>(s.from) + row * s.width;
+            const int left = s.width - (int)part * 16;
+            v[q] = row < s.rows ? load_tail<true>(from + part * 16, from, left < 16 ? left : 16)
+                                : (u4v){0u, 0u, 0u, 0u};
+        }
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const int64_t tile = part * 4 + d;
+            if (tile >= tiles) break;
+            uint32_t *const to = s.to + (tile * row_groups + group) * 64 + r;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                uint32_t w = 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) w |= ((v[q][d] >> (8 * g)) & 255u) << (8 * q);
+                to[g * 16] = w;
+            }
+        }
+    }
+}
+
 __global__ __launch_bounds__(256) void zero_kernel(uint16_t *p, int64_t n) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
         p[i] = 0;
@@ -158,6 +197,18 @@ taco_status repack(const Repack *r, int count, hipStream_t stream) {
     }
     return launch(reinterpret_cast<const void *>(&repack_kernel),
                   dim3(groups_of(groups, 2048), (unsigned)count), 256, stream, all);
+}
+
+taco_status tile_scales(const ScaleTiles *s, int count, hipStream_t stream) {
+    AllScales all = {};
+    int64_t most = 1;
+    for (int i = 0; i < count; ++i) {
+        all.s[i] = s[i];
+        const int64_t n = (s[i].rows + 63) / 64 * 16 * ((s[i].width + 15) / 16);
+        most = n > most ? n : most;
+    }
+    return launch(reinterpret_cast<const void *>(&tile_scales_kernel),
+                  dim3(groups_of((most + 255) / 256, 4096), (unsigned)count), 256, stream, all);
 }
 
 taco_status fill_zero(void *p, int64_t n16, hipStream_t stream) {
