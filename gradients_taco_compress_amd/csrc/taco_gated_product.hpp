@@ -115,19 +115,26 @@ struct Shape {
     static_assert(HM == HN, "halves alike: one load count for all");
     static constexpr int LOADS = A_HALF / 16 / THREADS;                // a thread's loads of it
     static_assert(LOADS == 2 && NF == 2, "loads and pairs of column fragments");
+    // Whether a work-group takes several items, one after the other: the loads of
+    // the next begin before the current one's outputs are formed (8192 x 10240x2560
+    // with G and U written 668 us instead of 690).  A small tile's work-groups are
+    // two to a CU, and few; the bookkeeping only costs them (999 x 1030x1111
+    // backward 57 us instead of 51).
+    static constexpr bool WALKS = BM == 256;
     // A split's partial sums.
     static constexpr int64_t SLAB = (int64_t)BM * BN;
 };
 using Large = Shape<256, 256, 2, 4>;
 using Small = Shape<128, 128, 2, 2>;
 
-// Which tile and which K-tiles a work-group takes.  The first `whole`
-// work-groups take a tile each; the remaining tiles are cut into `parts` parts of
-// `share` K-tiles.
+// The items of work: the first `whole` are a tile each; the remaining tiles are cut
+// into `parts` parts of `share` K-tiles.  Work-group b of a grid of g takes items b,
+// b + g, b + 2 g, ... (Shape::WALKS; else there is one for each item).
 struct Plan {
     int32_t tiles_m, tiles_n;
     int32_t whole, parts, share;
     int32_t depth;                 // K-tiles of a tile
+    int32_t items;
 };
 
 struct Tile { int m, n; };
@@ -230,8 +237,7 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
     // Several variables, not one for all: the compiler then knows that a load
     // into one does not touch the fragments being read from another, and does
     // not wait for it.  It tells few of them apart, so what is never loaded and
-    // read at the same time shares one: F, S and the scales, in the order in
-    // which they are loaded first.
+    // read at the same time shares one: the halves of B and the scales.
     constexpr int SCALES = SCALED ? THREADS * 4 : 0;           // [A0 | A1 | B0 | B1], bytes
     __shared__ __align__(1024) uint8_t a00[S::A_HALF], a01[S::A_HALF], a10[S::A_HALF],
         a11[S::A_HALF], b0[2 * S::B_HALF + SCALES], b1[2 * S::B_HALF + SCALES];
@@ -250,22 +256,6 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
     const int tid = threadIdx.x;
     [[maybe_unused]] const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const Place<S> place(tid);
-
-    // Consecutive work-groups go to the 8 XCDs in turn; each XCD gets a
-    // contiguous range of the whole tiles, whose operands meet in its L2.
-    int t_index, part = -1, kt0 = 0, kt1 = plan.depth;
-    if ((int)blockIdx.x < plan.whole) {
-        const int xcd = blockIdx.x % 8, q = plan.whole / 8, rem = plan.whole % 8;
-        t_index = xcd * q + (xcd < rem ? xcd : rem) + blockIdx.x / 8;
-    } else {
-        part = (int)blockIdx.x - plan.whole;
-        const int in = part % plan.parts;
-        t_index = plan.whole + part / plan.parts;
-        kt0 = in * plan.share;
-        if (kt0 + plan.share < kt1) kt1 = kt0 + plan.share;
-    }
-    const Tile tile = tile_at(plan, t_index);
-    const int seg_depth = K == Kind::kInput ? plan.depth / 2 : plan.depth;
 
     // Chunk i of this thread is LDS chunk i * THREADS + tid of a half: its row
     // there, the chunk of the source row it comes from, and its offset there.
@@ -297,19 +287,84 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
         off_b[i] = (uint32_t)(row * (int)p.b[0].pitch + chunk_b * 16);
     }
 
-    // Loads of half h of K-tile kt.  All of it is the same for every lane but
-    // the offset, which is out of bounds for chunks past a row's end, and all
-    // choices are selects: a branch here would part the products from what is
-    // to run beside them.
-    const int per_m = (int)((p.m + S::BM - 1) / S::BM);
-    const int which = K == Kind::kWeight && tile.m >= per_m;
-    const int64_t m0 = (int64_t)(tile.m - which * per_m) * S::BM;
-    const int64_t n0 = (int64_t)tile.n * (K == Kind::kForward ? HN : S::BN);
     const int pitch_a = (int)p.a[0].pitch, pitch_b = (int)p.b[0].pitch;
+    const int per_m = (int)((p.m + S::BM - 1) / S::BM);
     // Along the summed index: whole K-tiles (of a segment), elements of the one
-    // after them, 16-byte chunks.
+    // after them, 16-byte chunks; kInput's second segment (dU, Wu) begins at K-tile
+    // seg_depth.
     [[maybe_unused]] const int k_whole = (int)(p.k / KT), k_rest = (int)(p.k % KT);
     [[maybe_unused]] const int k_chunks = (int)((p.k * SIZE + 15) / 16);
+    [[maybe_unused]] const int seg_depth = plan.depth / 2;
+    // From one K-tile to the next, and from an operand to its second matrix (kInput:
+    // as if it followed the first).
+    const int64_t step_a = A_TURNED ? (int64_t)KT * pitch_a : kDeep;
+    const int64_t step_b = B_TURNED ? (int64_t)KT * pitch_b : kDeep;
+    [[maybe_unused]] const int64_t second_a =
+        static_cast<const char *>(p.a[1].p) - static_cast<const char *>(p.a[0].p) - seg_depth * step_a;
+    [[maybe_unused]] const int64_t second_b =
+        static_cast<const char *>(p.b[1].p) - static_cast<const char *>(p.b[0].p) -
+        (K == Kind::kInput ? seg_depth * step_b : 0);
+
+    // An item: where its K-tiles kt0 .. kt0 + count - 1 begin in both operands, the
+    // rows (or columns) that exist in the halves, and for codes the scales of the
+    // quarter of them that this wave loads.
+    struct Item {
+        const char *a, *b, *scale;
+        int here_a[2], here_b[2], here_scale;
+        int kt0, count, even;              // even: count, rounded up to two
+        int part;                          // of a split tile, else -1
+        Tile tile;
+    };
+    [[maybe_unused]] const int quarter = __builtin_amdgcn_readfirstlane(tid / HM);
+    [[maybe_unused]] const Matrix &scales =
+        quarter >= 2 ? p.b_scale[quarter & 1] : p.a_scale;
+    auto item_at = [&](int j) {
+        Item it;
+        it.part = -1;
+        it.kt0 = 0;
+        it.count = plan.depth;
+        int t;
+        if (j < plan.whole) {
+            // Consecutive work-groups go to the 8 XCDs in turn; each XCD gets a
+            // contiguous range of the whole tiles, whose operands meet in its L2.
+            const int xcd = j % 8, q = plan.whole / 8, rem = plan.whole % 8;
+            t = xcd * q + (xcd < rem ? xcd : rem) + j / 8;
+        } else {
+            it.part = j - plan.whole;
+            const int in = it.part % plan.parts;
+            t = plan.whole + it.part / plan.parts;
+            it.kt0 = in * plan.share;
+            const int left = plan.depth - it.kt0;
+            it.count = left < plan.share ? left : plan.share;
+        }
+        it.even = (it.count + 1) & ~1;
+        it.tile = tile_at(plan, t);
+        const int which = K == Kind::kWeight && it.tile.m >= per_m;
+        const int64_t m0 = (int64_t)(it.tile.m - which * per_m) * S::BM;
+        const int64_t n0 = (int64_t)it.tile.n * (K == Kind::kForward ? HN : S::BN);
+        it.a = static_cast<const char *>(p.a[which].p) + m0 * (A_TURNED ? SIZE : pitch_a) + it.kt0 * step_a;
+        it.b = static_cast<const char *>(p.b[0].p) + n0 * (B_TURNED ? SIZE : pitch_b) + it.kt0 * step_b;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            it.here_a[h] = clamp(p.m - m0 - h * HM, HM);
+            it.here_b[h] = clamp(p.n - n0 - (K == Kind::kForward ? 0 : h * HN), HN);
+        }
+        if constexpr (SCALED) {
+            const int64_t first = quarter >= 2 ? n0 : m0 + quarter * HM;
+            it.scale = static_cast<const char *>(scales.p) + first * 4 + it.kt0 * scales.pitch;
+            it.here_scale = clamp(scales.pitch / 4 - first, HM) * 4;
+        }
+        return it;
+    };
+    int j = blockIdx.x;
+    Item cur = item_at(j), next = cur;
+
+    // Loads.  K-tile kt counts from the current item's first; those past its last
+    // (and past an odd last one) are the next item's, whose loads so begin
+    // before the current one's outputs are formed.  All of this is the same for
+    // every lane but the offset, which is out of bounds for chunks past a row's end,
+    // and all choices are selects: a branch here would part the products from what
+    // is to run beside them.
     auto load = [&](uint8_t *buf, const char *base, int records, const uint32_t (&off)[2], bool in) {
 #if defined(__HIP_DEVICE_COMPILE__)      // the host pass does not know the resource type
         // 0x00020000: raw 32-bit data.
@@ -321,58 +376,59 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
                 16, in ? off[i] : 0x80000000u, 0, 0, 0);
 #endif
     };
-    // (past the last K-tile: nothing, which arrives as zeros)
-    auto load_half = [&](auto turned, uint8_t *buf, const void *p0, const void *p1, int64_t first,
-                         int64_t count, int pitch, const uint32_t (&off)[2], int chunk, int kt) {
-        const bool seg = K == Kind::kInput && kt >= seg_depth;
-        const int in_seg = seg ? kt - seg_depth : kt;
-        const char *base = static_cast<const char *>(seg ? p1 : p0);
-        const int here = clamp(count - first, HM);             // rows or columns of this half
+    // A half of an item's operand at its K-tile `local`, `more` bytes from the
+    // first half.
+    auto load_half = [&](auto turned, uint8_t *buf, const char *base, int64_t step, int64_t second,
+                         int64_t more, int here, int pitch, const uint32_t (&off)[2], int chunk,
+                         int local, int kt, bool exists) {
+        int in_seg = kt;
+        if constexpr (K == Kind::kInput) {
+            const bool seg = kt >= seg_depth;
+            in_seg -= seg ? seg_depth : 0;
+            more += seg ? second : 0;
+        }
+        base += local * step + more;
         int records;
         bool in;
         if constexpr (decltype(turned)::value != 0) {
-            base += (int64_t)in_seg * KT * pitch + first * SIZE;
             records = (in_seg < k_whole ? KT : in_seg == k_whole ? k_rest : 0) * pitch;
             in = chunk < (here + 7) / 8;
         } else {
-            base += first * pitch + (int64_t)in_seg * kDeep;
             records = here * pitch;
             in = chunk + in_seg * 8 < k_chunks;
         }
-        load(buf, base, kt < kt1 ? records : 0, off, in);
+        load(buf, base, exists ? records : 0, off, in);
     };
     auto load_a = [&](auto stage, auto half, int kt) {
         constexpr int h = decltype(half)::value;
-        const void *const p0 = K == Kind::kWeight ? p.a[which].p : p.a[0].p;
-        load_half(Int<A_TURNED>{}, lds_a(stage, half), p0, p.a[1].p, m0 + h * HM, p.m, pitch_a,
-                  off_a, chunk_a, kt);
+        const bool on = S::WALKS && kt >= cur.even;
+        const int local = on ? kt - cur.even : kt;
+        load_half(Int<A_TURNED>{}, lds_a(stage, half), on ? next.a : cur.a, step_a, second_a,
+                  (int64_t)(h * HM) * (A_TURNED ? SIZE : pitch_a), on ? next.here_a[h] : cur.here_a[h],
+                  pitch_a, off_a, chunk_a, local, local + (on ? next.kt0 : cur.kt0),
+                  local < (on ? next.count : cur.count));
     };
     auto load_b = [&](auto stage, auto half, int kt) {
         constexpr int h = decltype(half)::value;
-        // (forward: the same rows of the other weight)
-        const void *const p0 = K == Kind::kForward ? p.b[h].p : p.b[0].p;
-        load_half(Int<B_TURNED>{}, lds_b(stage, half), p0, p.b[1].p,
-                  K == Kind::kForward ? n0 : n0 + h * HN, p.n, pitch_b, off_b, chunk_b, kt);
+        const bool on = S::WALKS && kt >= cur.even;
+        const int local = on ? kt - cur.even : kt;
+        // (forward: the second half is the same rows of the other weight)
+        load_half(Int<B_TURNED>{}, lds_b(stage, half), on ? next.b : cur.b, step_b, second_b,
+                  h == 0 ? 0 : K == Kind::kForward ? second_b : (int64_t)HN * SIZE,
+                  on ? next.here_b[h] : cur.here_b[h], pitch_b, off_b, chunk_b, local,
+                  local + (on ? next.kt0 : cur.kt0), local < (on ? next.count : cur.count));
     };
     // Scales of a K-tile: one 4-byte load a thread.
-    [[maybe_unused]] const char *scale_base = nullptr;
-    [[maybe_unused]] int64_t scale_pitch = 0;
-    [[maybe_unused]] int scale_records = 0;
-    if constexpr (SCALED) {
-        const int quarter = __builtin_amdgcn_readfirstlane(tid / HM);
-        const bool b = quarter >= 2;
-        const Matrix &s = b ? p.b_scale[quarter - 2] : p.a_scale;
-        const int64_t first = b ? n0 : m0 + quarter * HM;
-        scale_base = static_cast<const char *>(s.p) + first * 4;
-        scale_pitch = s.pitch;
-        scale_records = clamp(s.pitch / 4 - first, HM) * 4;
-    }
     [[maybe_unused]] const uint32_t scale_off = tid % HM * 4;
     auto load_scales = [&](auto stage, int kt) {
 #if defined(__HIP_DEVICE_COMPILE__)
         if constexpr (SCALED) {
+            const bool on = S::WALKS && kt >= cur.even;
+            const int local = on ? kt - cur.even : kt;
+            const int records = local < (on ? next.count : cur.count)
+                                    ? on ? next.here_scale : cur.here_scale : 0;
             const auto r = __builtin_amdgcn_make_buffer_rsrc(
-                (void *)(scale_base + kt * scale_pitch), 0, kt < kt1 ? scale_records : 0, 0x00020000);
+                (void *)((on ? next.scale : cur.scale) + local * scales.pitch), 0, records, 0x00020000);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 r, (__attribute__((address_space(3))) void *)(lds_s(stage) + wave * kWave * 4), 4,
                 scale_off, 0, 0, 0);
@@ -447,12 +503,6 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
             sb[h] = read_scales(stage, at_sb + h * HM * 4, Int<NF>{});
     };
     f4v sum[2][2][MF][NF];
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int i = 0; i < MF; ++i)
-#pragma unroll
-            for (int j = 0; j < NF; ++j) sum[q >> 1][q & 1][i][j] = (f4v){0.0f, 0.0f, 0.0f, 0.0f};
     // Products of a row fragment with a half of B.
     auto multiply = [&](auto qa, auto qb, auto fi) {
         constexpr int a = decltype(qa)::value, b = decltype(qb)::value, i = decltype(fi)::value;
@@ -463,21 +513,21 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
         });
     };
 
-    // K-tile t of this work-group (counted from kt0) lies in stage t % 2.  Loads are
-    // in the order A0, F, scales, S, A1 of each K-tile, so "the half has
+    // K-tile t of an item lies in stage t % 2 (items take an even number of them).
+    // Loads are in the order A0, F, scales, S, A1 of each K-tile, so "the half has
     // arrived" is a count of those after it.
     using C0 = Int<0>;
     using C1 = Int<1>;
     constexpr int L = S::LOADS, SL = SCALED ? 1 : 0;
-    load_a(C0{}, C0{}, kt0);
-    load_b(C0{}, C0{}, kt0);
-    load_scales(C0{}, kt0);
-    load_b(C0{}, C1{}, kt0);
-    load_a(C0{}, C1{}, kt0);
-    load_a(C1{}, C0{}, kt0 + 1);
-    load_b(C1{}, C1{}, kt0 + 1);
-    load_scales(C1{}, kt0 + 1);
-    load_b(C1{}, C0{}, kt0 + 1);
+    load_a(C0{}, C0{}, 0);
+    load_b(C0{}, C0{}, 0);
+    load_scales(C0{}, 0);
+    load_b(C0{}, C1{}, 0);
+    load_a(C0{}, C1{}, 0);
+    load_a(C1{}, C0{}, 1);
+    load_b(C1{}, C1{}, 1);
+    load_scales(C1{}, 1);
+    load_b(C1{}, C0{}, 1);
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(4 * L + SL) : "memory");
     read_a_scales(C0{}, C0{});
     for_each<MF>([&](auto i) { read_a(C0{}, C0{}, i); });
@@ -524,34 +574,52 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
         });
         pin();
     };
-    // K-tiles past the last (the second of an odd number, and what is read ahead) are
-    // zeros.
-    for (int kt = kt0; kt < kt1; kt += 2) {
-        k_tile(C0{}, kt);
-        k_tile(C1{}, kt + 1);
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-
-    if (part >= 0) {
-        float *const slab = p.slabs + (int64_t)part * S::SLAB;
+    for (;;) {
+        if constexpr (S::WALKS) {
+            // (after the last item there is none: nothing exists of its K-tiles)
+            j += gridDim.x;
+            next = j < plan.items ? item_at(j) : cur;
+            if (j >= plan.items) next.count = 0;
+        }
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
             for (int i = 0; i < MF; ++i)
 #pragma unroll
-                for (int j = 0; j < NF; ++j)
-                    *reinterpret_cast<f4v *>(slab + (int64_t)((((q >> 1) * MF + i) * 4 + (q & 1) * 2 + j) * THREADS + tid) * 4) =
-                        sum[q >> 1][q & 1][i][j];
-        return;
-    }
-    const Finish<E, K, S> finish{p, place, tile};
-#pragma unroll
-    for (int qa = 0; qa < 2; ++qa)
-#pragma unroll
-        for (int i = 0; i < MF; ++i) {
-            const f4v v[2][2] = {{sum[qa][0][i][0], sum[qa][0][i][1]}, {sum[qa][1][i][0], sum[qa][1][i][1]}};
-            finish(qa, i, v);
+                for (int e = 0; e < NF; ++e)
+                    sum[q >> 1][q & 1][i][e] = (f4v){0.0f, 0.0f, 0.0f, 0.0f};
+        for (int kt = 0; kt < cur.even; kt += 2) {
+            k_tile(C0{}, kt);
+            k_tile(C1{}, kt + 1);
         }
+        if (cur.part >= 0) {
+            float *const slab = p.slabs + (int64_t)cur.part * S::SLAB;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int i = 0; i < MF; ++i)
+#pragma unroll
+                    for (int e = 0; e < NF; ++e) {
+                        const int at = ((q >> 1) * MF + i) * 4 + (q & 1) * 2 + e;
+                        *reinterpret_cast<f4v *>(slab + (int64_t)(at * THREADS + tid) * 4) =
+                            sum[q >> 1][q & 1][i][e];
+                    }
+        } else {
+            const Finish<E, K, S> finish{p, place, cur.tile};
+#pragma unroll
+            for (int qa = 0; qa < 2; ++qa)
+#pragma unroll
+                for (int i = 0; i < MF; ++i) {
+                    const f4v v[2][2] = {{sum[qa][0][i][0], sum[qa][0][i][1]},
+                                         {sum[qa][1][i][0], sum[qa][1][i][1]}};
+                    finish(qa, i, v);
+                }
+        }
+        if (!S::WALKS || j >= plan.items) break;
+        cur = next;
+    }
+    // (loads of nothing may still be on their way to LDS)
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
 // Adds the parts of a split tile in order and finishes it: blockIdx.x is the
@@ -602,7 +670,7 @@ Choice choice_for(Kind kind, const Product &p, int size, const Cost &c, double *
         return (double)up(groups, c.places) * (c.fixed + (double)steps * c.step);
     };
     double best = rounds(tiles, depth);
-    r.plan = {(int32_t)tm, (int32_t)tn, (int32_t)tiles, 1, (int32_t)depth, (int32_t)depth};
+    r.plan = {(int32_t)tm, (int32_t)tn, (int32_t)tiles, 1, (int32_t)depth, (int32_t)depth, (int32_t)tiles};
     for (int64_t split : {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
         if (left == 0 || split * 4 > depth) break;
         const int64_t share = up(depth, split), parts = up(depth, share);
@@ -613,6 +681,7 @@ Choice choice_for(Kind kind, const Product &p, int size, const Cost &c, double *
         r.plan.whole = (int32_t)(tiles - left);
         r.plan.parts = (int32_t)parts;
         r.plan.share = (int32_t)share;
+        r.plan.items = (int32_t)(tiles - left + left * parts);
         r.split_tiles = left;
         r.slab_floats = left * parts * S::SLAB;
     }
@@ -630,7 +699,7 @@ inline Choice choose(Kind kind, const Product &p, int size) {
 
 template <typename E, Kind K, typename S>
 taco_status launch_product(const Product &p, const Choice &c, hipStream_t stream) {
-    const int64_t groups = c.plan.whole + c.split_tiles * c.plan.parts;
+    const int32_t groups = S::WALKS && c.plan.items > kLargeCost.places ? kLargeCost.places : c.plan.items;
     const taco_status st = launch(reinterpret_cast<const void *>(&product_kernel<E, K, S>),
                                   dim3((unsigned)groups), S::THREADS, stream, p, c.plan);
     if (st != TACO_OK || c.split_tiles == 0) return st;

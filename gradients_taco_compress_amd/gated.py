@@ -49,7 +49,7 @@ _SIGNATURES = {
                                       _I64),
     "taco_gated_backward": ([_P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _P, _I64, _I64, _I64,
                              _I64, _I32, _I32, _P, _I64, _P, _P, _P, _I64, _P], _STATUS),
-    "taco_gated_forward_mx_workspace": ([_P, _P, _P, _I64, _I64, _I64], _I64),
+    "taco_gated_forward_mx_workspace": ([_I64, _I64, _I64], _I64),
     "taco_gated_forward_mx": ([_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _P, _I64, _P,
                                _I64, _P], _STATUS),
     "taco_gated_mx_encode": ([_P, _I64, _I64, _I64, _I32, _P, _P, _P], _STATUS),
@@ -204,8 +204,7 @@ def gated_forward_mx(x, gate_weight, up_weight, activation: str = "silu", dtype=
     if out.shape != shape:
         raise ValueError(f"out must be {list(shape)}, got {list(out.shape)}")
     lda = _same_rows(out, "out", dtype, rows, features)
-    ws = at.workspace(_lib.taco_gated_forward_mx_workspace(
-        xs.data_ptr(), gs.data_ptr(), us.data_ptr(), rows, hidden, features))
+    ws = at.workspace(_lib.taco_gated_forward_mx_workspace(rows, hidden, features))
     at.call(_lib.taco_gated_forward_mx, "taco_gated_forward_mx", xc.data_ptr(), xs.data_ptr(),
             gc.data_ptr(), gs.data_ptr(), uc.data_ptr(), us.data_ptr(), rows, hidden, features,
             DTYPES[dtype], act, out.data_ptr(), lda, _ptr(ws), _size(ws))

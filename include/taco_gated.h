@@ -112,9 +112,7 @@ taco_status taco_gated_backward(const void *da, int64_t ldda, const void *x, int
                                 void *workspace, int64_t workspace_bytes, hipStream_t stream);
 
 /* Bytes of workspace of taco_gated_forward_mx (-1 for a bad shape). */
-int64_t taco_gated_forward_mx_workspace(const uint8_t *x_scales, const uint8_t *gate_scales,
-                                        const uint8_t *up_scales, int64_t rows, int64_t hidden,
-                                        int64_t features);
+int64_t taco_gated_forward_mx_workspace(int64_t rows, int64_t hidden, int64_t features);
 
 /* Forward on codes [.., hidden] and scales [.., hidden / 32] of x and of both
  * weights; hidden is a multiple of 32.  a is of dtype.  Products of codes and
