@@ -50,6 +50,8 @@ GATED_SOURCES = [os.path.join(CSRC, f) for f in
                  ("taco_gated_abi.hip", "taco_gated_bf16.hip", "taco_gated_f16.hip",
                   "taco_gated_mx.hip", "taco_gated_rows.hip")]
 GATED_LIB = os.path.join(PKG, "libtaco_gated.so")
+GATED_TORCH_SOURCE = os.path.join(CSRC, "taco_gated_torch.cpp")
+GATED_TORCH = os.path.join(PKG, "_gated_torch.so")
 CXX = os.environ.get("CXX", "g++")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -122,9 +124,9 @@ def build(verbose: bool = False, out: str | None = None) -> str:
     return lib
 
 
-def _norm_torch_command(out: str) -> list:
-    """Compile command of the torch module: torch's headers and libraries, and
-    NORM_LIB from the folder the module lies in."""
+def _torch_command(source: str, library: str, out: str) -> list:
+    """Compile command of a torch module: torch's headers and libraries, and the
+    library that it calls, from the folder the module lies in."""
     import sysconfig
     from torch.utils.cpp_extension import include_paths, library_paths
     cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
@@ -132,16 +134,16 @@ def _norm_torch_command(out: str) -> list:
     for path in [sysconfig.get_paths()["include"], *include_paths(),
                  os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include")]:
         cmd += ["-isystem", path]
-    cmd += [NORM_TORCH_SOURCE, "-o", out]
+    cmd += [source, "-o", out]
     for path in library_paths():
         cmd += ["-L", path]
-    return cmd + ["-L", PKG, "-l:libtaco_norm.so", "-Wl,-rpath,$ORIGIN", "-ltorch_python",
+    return cmd + ["-L", PKG, f"-l:{library}", "-Wl,-rpath,$ORIGIN", "-ltorch_python",
                   "-ltorch_hip", "-ltorch_cpu", "-lc10_hip", "-lc10"]
 
 
 def build_gated(verbose: bool = False) -> str:
-    """Compile GATED_SOURCES (in parallel) and link GATED_LIB; always recompiles.
-    Returns GATED_LIB."""
+    """Compile GATED_SOURCES (in parallel), link GATED_LIB and GATED_TORCH;
+    always recompiles.  Returns GATED_LIB."""
     from concurrent.futures import ThreadPoolExecutor
     tag = f".tmp{os.getpid()}"
     objs = [src + tag + ".o" for src in GATED_SOURCES]
@@ -155,8 +157,10 @@ def build_gated(verbose: bool = False) -> str:
         _run([HIPCC, "--offload-arch=gfx950", "-shared", "-Wl,-soname,libtaco_gated.so", *objs,
               "-o", GATED_LIB + tag], verbose)
         os.replace(GATED_LIB + tag, GATED_LIB)
+        _run(_torch_command(GATED_TORCH_SOURCE, "libtaco_gated.so", GATED_TORCH + tag), verbose)
+        os.replace(GATED_TORCH + tag, GATED_TORCH)
     finally:
-        for path in objs + [GATED_LIB + tag]:
+        for path in objs + [GATED_LIB + tag, GATED_TORCH + tag]:
             if os.path.exists(path):
                 os.remove(path)
     return GATED_LIB
@@ -178,7 +182,7 @@ def build_norm(verbose: bool = False) -> str:
         _run([HIPCC, "--offload-arch=gfx950", "-shared", "-Wl,-soname,libtaco_norm.so", *objs,
               "-o", NORM_LIB + tag], verbose)
         os.replace(NORM_LIB + tag, NORM_LIB)
-        _run(_norm_torch_command(NORM_TORCH + tag), verbose)
+        _run(_torch_command(NORM_TORCH_SOURCE, "libtaco_norm.so", NORM_TORCH + tag), verbose)
         os.replace(NORM_TORCH + tag, NORM_TORCH)
     finally:
         for path in objs + [NORM_LIB + tag, NORM_TORCH + tag]:

@@ -5,67 +5,9 @@
 // given outputs, a bad argument) before it launches anything; norm.py then
 // takes its general path, which also words the errors.  Measured on a [1, 2560] layer norm: 16 us per call
 // in Python, 6 us here.
-#include <Python.h>
-
-#include <array>
-#include <cstdint>
-#include <vector>
-
-#include <ATen/ATen.h>
-#include <ATen/hip/EmptyTensor.h>
-#include <c10/hip/HIPFunctions.h>
-#include <c10/hip/HIPStream.h>
-#include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/python_variable.h>
-
-#include "taco_norm.h"
+#include "taco_torch.hpp"
 
 namespace {
-
-using at::ScalarType;
-
-struct Type {
-    taco_norm_dtype id;
-    bool ok;
-};
-Type type_of(ScalarType t) {
-    switch (t) {
-        case at::kBFloat16: return {TACO_NORM_BF16, true};
-        case at::kHalf: return {TACO_NORM_F16, true};
-        case at::kFloat: return {TACO_NORM_F32, true};
-        default: return {TACO_NORM_F32, false};
-    }
-}
-
-// The tensor of an argument, or nullptr (None, or no tensor at all).
-const at::Tensor *tensor(PyObject *o) {
-    return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr;
-}
-
-// Rows of a tensor [..., n]: contiguous, or two-dimensional with a pitch.
-struct RowsOf {
-    int64_t rows = 0, n = 0, ld = 0;
-    bool ok = false;
-};
-RowsOf rows_of(const at::Tensor &t) {
-    RowsOf r;
-    const int64_t d = t.dim();
-    if (d == 0 || t.numel() == 0) return r;
-    r.n = t.size(d - 1);
-    r.rows = t.numel() / r.n;
-    if (t.is_contiguous()) {
-        r.ld = r.n;
-        r.ok = true;
-    } else if (d == 2 && t.stride(1) == 1 && t.stride(0) >= r.n) {
-        r.ld = t.stride(0);
-        r.ok = true;
-    }
-    return r;
-}
-
-bool on_device(const at::Tensor *t, c10::Device dev) {
-    return t && t->defined() && t->device() == dev && t->layout() == at::kStrided;
-}
 
 // A norm parameter: None, or hidden contiguous elements of the activations'
 // type or float32, and of one type with the other parameter.
@@ -83,18 +25,10 @@ bool parameter(PyObject *o, c10::Device dev, int64_t hidden, ScalarType dtype, c
     return true;
 }
 
-bool vector(const at::Tensor *t, c10::Device dev, int64_t n, ScalarType dtype) {
-    return on_device(t, dev) && t->scalar_type() == dtype && t->numel() == n && t->is_contiguous();
-}
-
 // A checkpoint [..., hidden] of `rows` rows.
 bool codes_of(const at::Tensor *t, c10::Device dev, int64_t rows, int64_t hidden) {
     return vector(t, dev, rows * hidden, at::kByte) && t->dim() > 0 &&
            t->size(t->dim() - 1) == hidden;
-}
-
-at::Tensor make(at::IntArrayRef sizes, ScalarType dtype, c10::Device dev) {
-    return at::Tensor(at::detail::empty_cuda(sizes, dtype, dev, std::nullopt));
 }
 
 // n elements of a contiguous tensor's storage from `offset` on, as a tensor
@@ -105,74 +39,6 @@ at::Tensor slice(const at::Tensor &t, int64_t offset, int64_t n) {
     impl->set_storage_offset(offset);
     impl->set_sizes_contiguous({n});
     return at::Tensor(std::move(impl));
-}
-
-// The activations' common ground: device, type, rows.
-struct Input {
-    const at::Tensor *t = nullptr;
-    c10::Device dev = c10::Device(c10::DeviceType::CPU);
-    RowsOf r;
-    Type type = {TACO_NORM_F32, false};
-    hipStream_t stream = nullptr;
-};
-bool input(PyObject *o, Input *in) {
-    in->t = tensor(o);
-    if (!in->t || !in->t->defined() || !in->t->is_cuda() || in->t->layout() != at::kStrided)
-        return false;
-    in->dev = in->t->device();
-    in->type = type_of(in->t->scalar_type());
-    in->r = rows_of(*in->t);
-    if (!in->type.ok || !in->r.ok) return false;
-    if (c10::hip::current_device() != in->dev.index()) return false;
-    in->stream = c10::hip::getCurrentHIPStream(in->dev.index()).stream();
-    return true;
-}
-
-bool same_rows(const at::Tensor *t, const Input &in, RowsOf *r) {
-    if (!on_device(t, in.dev) || t->scalar_type() != in.t->scalar_type()) return false;
-    *r = rows_of(*t);
-    return r->ok && r->rows == in.r.rows && r->n == in.r.n;
-}
-
-PyObject *none() { Py_RETURN_NONE; }
-
-PyObject *wrap(const at::Tensor &t) { return THPVariable_Wrap(t); }
-template <size_t N>
-PyObject *pack(std::array<PyObject *, N> v) {
-    PyObject *out = PyTuple_New(N);
-    for (size_t i = 0; i < N; ++i) {
-        if (!out || !v[i]) {
-            for (size_t j = i; j < N; ++j) Py_XDECREF(v[j]);
-            Py_XDECREF(out);
-            return nullptr;
-        }
-        PyTuple_SET_ITEM(out, i, v[i]);
-    }
-    return out;
-}
-
-// Runs f, turning a C++ exception into the Python one that torch's own calls
-// raise for it (torch.OutOfMemoryError where there is no memory).
-template <typename F>
-PyObject *guarded(F &&f) {
-    HANDLE_TH_ERRORS
-    return f();
-    END_HANDLE_TH_ERRORS
-}
-
-// What a call returns that the C ABI did not make: None after a check, before
-// which nothing is launched (norm.py words the error), and TacoError for a
-// launch that failed, which may follow one of the same call that did not.
-PyObject *refused(taco_status st, const char *what) {
-    if (st != TACO_ERR_HIP) return none();
-    PyObject *const package = PyImport_ImportModule("gradients_taco_compress_amd");
-    PyObject *const type = package ? PyObject_GetAttrString(package, "TacoError") : nullptr;
-    PyObject *const error = type ? PyObject_CallFunction(type, "is", (int)st, what) : nullptr;
-    if (error) PyErr_SetObject(type, error);
-    Py_XDECREF(error);
-    Py_XDECREF(type);
-    Py_XDECREF(package);
-    return nullptr;
 }
 
 // (x, weight, bias, eps)
@@ -312,10 +178,97 @@ PyObject *checkpoint_weight_grad(PyObject *, PyObject *const *args, Py_ssize_t n
     });
 }
 
-template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)>
-PyMethodDef method(const char *name) {
-    return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(F)), METH_FASTCALL,
-            nullptr};
+// A residual or the gradient that arrives at the sum: None, or rows like x's.
+bool like_rows(PyObject *o, const Input &in, const void **p, int64_t *ld) {
+    *p = nullptr;
+    *ld = 0;
+    if (o == Py_None) return true;
+    const at::Tensor *t = tensor(o);
+    RowsOf r;
+    if (!same_rows(t, in, &r)) return false;
+    *p = t->data_ptr();
+    *ld = r.ld;
+    return true;
+}
+
+PyObject *wrap_or_none(const at::Tensor &t) { return t.defined() ? wrap(t) : none(); }
+
+// (x, weight, eps, residual): (y, total or None, rstd), or with mx (codes, scales,
+// total or None)
+PyObject *rms_forward(PyObject *const *args, Py_ssize_t n, bool mx) {
+    return guarded([&]() -> PyObject * {
+        Input in;
+        if (n != 4 || !input(args[0], &in)) return none();
+        const ScalarType dtype = in.t->scalar_type();
+        ScalarType ptype = dtype;
+        bool typed = false;
+        const void *w, *residual;
+        int64_t ldr;
+        if (!parameter(args[1], in.dev, in.r.n, dtype, &w, &ptype, &typed) ||
+            !PyFloat_Check(args[2]) || !like_rows(args[3], in, &residual, &ldr) ||
+            (mx && in.r.n % 32 != 0))
+            return none();
+        const float eps = (float)PyFloat_AS_DOUBLE(args[2]);
+        at::Tensor total;
+        if (residual) total = make(in.t->sizes(), dtype, in.dev);
+        void *const total_p = residual ? total.data_ptr() : nullptr;
+        const taco_norm_dtype pt = type_of(ptype).id;
+        if (mx) {
+            std::vector<int64_t> sizes = in.t->sizes().vec();
+            const at::Tensor codes = make(sizes, at::kByte, in.dev);
+            sizes.back() /= 32;
+            const at::Tensor scales = make(sizes, at::kByte, in.dev);
+            const taco_status st = taco_norm_rms_mx(
+                in.t->data_ptr(), in.r.ld, residual, ldr, in.r.rows, in.r.n, in.type.id, w, pt, eps,
+                static_cast<uint8_t *>(codes.data_ptr()), static_cast<uint8_t *>(scales.data_ptr()),
+                total_p, in.r.n, in.stream);
+            if (st != TACO_OK) return refused(st, "taco_norm_rms_mx");
+            return pack<3>({wrap(codes), wrap(scales), wrap_or_none(total)});
+        }
+        const at::Tensor y = make(in.t->sizes(), dtype, in.dev);
+        const at::Tensor rstd = make({in.r.rows}, at::kFloat, in.dev);
+        const taco_status st = taco_norm_rms_forward(
+            in.t->data_ptr(), in.r.ld, residual, ldr, in.r.rows, in.r.n, in.type.id, w, pt, eps,
+            y.data_ptr(), in.r.n, total_p, in.r.n, static_cast<float *>(rstd.data_ptr()), in.stream);
+        if (st != TACO_OK) return refused(st, "taco_norm_rms_forward");
+        return pack<3>({wrap(y), wrap_or_none(total), wrap(rstd)});
+    });
+}
+PyObject *rms_norm(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    return rms_forward(args, n, false);
+}
+PyObject *rms_norm_mx(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    return rms_forward(args, n, true);
+}
+
+// (dy, x, rstd, weight, dtotal): (dx, dweight), the weight's gradient of its type
+// (float32 without one).
+PyObject *rms_norm_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        Input in;
+        if (n != 5 || !input(args[0], &in)) return none();
+        const ScalarType dtype = in.t->scalar_type();
+        const at::Tensor *x = tensor(args[1]), *rstd = tensor(args[2]);
+        RowsOf rx;
+        ScalarType ptype = at::kFloat;
+        bool typed = false;
+        const void *w, *dtotal;
+        int64_t lddt;
+        if (!same_rows(x, in, &rx) || !vector(rstd, in.dev, in.r.rows, at::kFloat) ||
+            !parameter(args[3], in.dev, in.r.n, dtype, &w, &ptype, &typed) ||
+            !like_rows(args[4], in, &dtotal, &lddt))
+            return none();
+        const int64_t bytes = taco_norm_rms_backward_workspace(in.r.rows, in.r.n);
+        if (bytes < 0) return none();
+        const at::Tensor dx = make(in.t->sizes(), dtype, in.dev);
+        const at::Tensor dw = make({in.r.n}, ptype, in.dev), ws = make({bytes}, at::kByte, in.dev);
+        const taco_status st = taco_norm_rms_backward(
+            in.t->data_ptr(), in.r.ld, x->data_ptr(), rx.ld, static_cast<const float *>(rstd->data_ptr()),
+            dtotal, lddt, w, in.r.rows, in.r.n, in.type.id, type_of(ptype).id, dx.data_ptr(), in.r.n,
+            dw.data_ptr(), ws.data_ptr(), bytes, in.stream);
+        if (st != TACO_OK) return refused(st, "taco_norm_rms_backward");
+        return pack<2>({wrap(dx), wrap(dw)});
+    });
 }
 
 PyMethodDef methods[] = {
@@ -324,6 +277,9 @@ PyMethodDef methods[] = {
     method<layer_norm_backward>("layer_norm_backward"),
     method<layer_norm_checkpoint_backward>("layer_norm_checkpoint_backward"),
     method<checkpoint_weight_grad>("checkpoint_weight_grad"),
+    method<rms_norm>("rms_norm"),
+    method<rms_norm_mx>("rms_norm_mx"),
+    method<rms_norm_backward>("rms_norm_backward"),
     {nullptr, nullptr, 0, nullptr},
 };
 

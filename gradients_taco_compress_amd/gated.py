@@ -39,6 +39,15 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
+# The usual calls, without the interpreter between them and the C ABI: each
+# function returns None for what is not usual (the code below then takes over, and
+# words the errors).
+try:
+    from . import _gated_torch as _fast
+except ImportError as e:
+    raise ImportError(f"the torch module of libtaco_gated is not built ({e}); run "
+                      "`python gradients_taco_compress_amd/build.py`") from e
+
 _P, _I64, _I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
 _STATUS = ctypes.c_int
 _SIGNATURES = {
@@ -70,7 +79,7 @@ MX_BLOCK = 32
 # ------------------------------------------------------------- arguments --
 
 def _activation(name):
-    if name not in ACTIVATIONS:
+    if not isinstance(name, str) or name not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {name!r}")
     return ACTIVATIONS[name]
 
@@ -124,6 +133,10 @@ def gated_forward(x, gate_weight, up_weight, activation: str = "silu", save: boo
                   out=None, stream=None):
     """act(x gate_weight^T) * (x up_weight^T): [..., features].  With ``save``:
     (a, gate, up), gate and up the two projections as gated_backward takes them."""
+    if out is None and stream is None:
+        done = _fast.gated_forward(x, gate_weight, up_weight, ACTIVATIONS.get(activation), bool(save))
+        if done is not None:
+            return done
     dtype, act = _type(x, "x"), _activation(activation)
     rows, hidden, ldx = _pitch(x, "x")
     features, ldg = _weight(gate_weight, "gate_weight", dtype, hidden)
@@ -147,6 +160,11 @@ def gated_backward(da, x, gate, up, gate_weight, up_weight, activation: str = "s
                    input_grad: bool = True, weight_grads: bool = True, stream=None):
     """Gradients of gated_forward from its saved projections: (dx,
     dgate_weight, dup_weight), None for those that are not asked for."""
+    if input_grad and weight_grads and stream is None:
+        done = _fast.gated_backward(da, x, gate, up, gate_weight, up_weight,
+                                    ACTIVATIONS.get(activation))
+        if done is not None:
+            return done
     dtype, act = _type(da, "da"), _activation(activation)
     rows, features, ldda = _pitch(da, "da")
     ldgu = _same_rows(gate, "gate", dtype, rows, features)
@@ -188,6 +206,11 @@ def gated_forward_mx(x, gate_weight, up_weight, activation: str = "silu", dtype=
     """gated_forward on 8-bit operands: x, gate_weight and up_weight are pairs
     (codes, scales) as norm.rms_norm_mx and mx_encode return them.  The result is
     of ``dtype`` (bf16 or fp16)."""
+    if out is None and stream is None and dtype in (torch.bfloat16, torch.float16):
+        done = _fast.gated_forward_mx(x, gate_weight, up_weight, ACTIVATIONS.get(activation),
+                                      dtype is torch.float16)
+        if done is not None:
+            return done
     act = _activation(activation)
     if dtype not in (torch.bfloat16, torch.float16):
         raise TypeError(f"dtype must be torch.bfloat16 or torch.float16, got {dtype}")

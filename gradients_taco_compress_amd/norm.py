@@ -402,6 +402,10 @@ def rms_norm(x, weight=None, eps: float = 1e-5, residual=None, out=None, total=N
     """Root-mean-square norm of x + residual over the last dimension: (y, total,
     rstd), total = x + residual (None without a residual), rstd float32 [rows], as
     the backward pass takes them.  out and total may be x or residual (in place)."""
+    if out is None and total is None and rstd is None and stream is None:
+        done = _fast.rms_norm(x, weight, eps, residual)
+        if done is not None:
+            return done
     rows, hidden, ldx = _pitch(x, "x")
     w = _param(weight, hidden, x.dtype, "weight")
     ptype = _param_type(weight, None, x.dtype)
@@ -426,6 +430,10 @@ def rms_norm_mx(x, weight=None, eps: float = 1e-5, residual=None, total=None, st
     scales uint8 [..., hidden / 32], E4M3 codes of each 32 neighbours over their scale
     2^(byte - 127), as gated.gated_forward_mx takes them.  total may be x or
     residual (in place)."""
+    if total is None and stream is None:
+        done = _fast.rms_norm_mx(x, weight, eps, residual)
+        if done is not None:
+            return done
     rows, hidden, ldx = _pitch(x, "x")
     if hidden == 0 or hidden % 32:
         raise ValueError(f"x must hold rows of a multiple of 32, got {list(x.shape)}")
@@ -452,6 +460,10 @@ def rms_norm_backward(dy, x, rstd, weight=None, dtotal=None, dx=None, param_grad
     dtotal: the gradient that arrives at total.  dx is the gradient of x and of
     residual alike, and may be dy or dtotal (in place); dweight is of param_dtype
     (weight's type; float32 without a weight), None without param_grads."""
+    if dx is None and param_grads and param_dtype is None and stream is None:
+        done = _fast.rms_norm_backward(dy, x, rstd, weight, dtotal)
+        if done is not None:
+            return done
     rows, hidden, lddy = _pitch(dy, "dy")
     ldx = _same_rows(x, "x", dy.dtype, rows, hidden)
     q = _vector(rstd, rows, "rstd")
