@@ -648,15 +648,31 @@ struct Choice {
     int64_t split_tiles, slab_floats;
 };
 
-// What a plan's parts cost in microseconds: a work-group's beginning and end,
-// a K-tile while every place of the GPU has one, and a part's sums, written and read.
+// What a plan's parts cost in microseconds, as measured on an MI355X: a round of
+// tiles' beginning and end, a K-tile while every place of the GPU has a tile and
+// while half of them or fewer have one (between, the share that is taken counts),
+// and a part's sums, written and read.  Measured forward without G and U, at
+// 16, 32 and 64 K-tiles in us:
+//     large, 256 / 512 / 768 tiles    33, 57, 104 / 63, 113, 205 / 91, 165, 307
+//     large, 32 / 128 tiles           25, 42, 76 / 28, 45, 78
+//     small, 512 / 1024 / 2048 tiles  25, 37, 69 / 39, 71, 133 / 74, 137, 259
+//     small, 128 / 256 tiles          15, 23, 39 / 15, 24, 41
+// A K-tile of codes takes the same time as one of 16-bit elements.
 struct Cost {
     int places;            // work-groups that run at once
-    double fixed, step, part;
+    double fixed, step, alone, part;
 };
-constexpr Cost kLargeCost = {256, 6.0, 1.15, 0.11};
-constexpr Cost kSmallCost = {512, 4.0, 0.60, 0.03};
+constexpr Cost kLargeCost = {256, 8.0, 1.48, 1.06, 0.11};
+constexpr Cost kSmallCost = {512, 6.0, 0.95, 0.53, 0.03};
 constexpr double kJoinUs = 5.0;
+
+inline double groups_us(const Cost &c, int64_t groups, int64_t steps) {
+    const int64_t left = groups % c.places;
+    const double more = 2.0 * (double)left / c.places - 1.0;
+    const double step = c.alone + (c.step - c.alone) * (more > 0.0 ? more : 0.0);
+    return (double)(groups / c.places) * (c.fixed + (double)steps * c.step) +
+           (left == 0 ? 0.0 : c.fixed + (double)steps * step);
+}
 
 template <typename S>
 Choice choice_for(Kind kind, const Product &p, int size, const Cost &c, double *us) {
@@ -666,15 +682,12 @@ Choice choice_for(Kind kind, const Product &p, int size, const Cost &c, double *
     const int64_t tm = up(p.m, S::BM) * (kind == Kind::kWeight ? 2 : 1);
     const int64_t tn = up(p.n, kind == Kind::kForward ? S::HN : S::BN), tiles = tm * tn;
     const int64_t left = tiles % c.places;
-    auto rounds = [&](int64_t groups, int64_t steps) {
-        return (double)up(groups, c.places) * (c.fixed + (double)steps * c.step);
-    };
-    double best = rounds(tiles, depth);
+    double best = groups_us(c, tiles, depth);
     r.plan = {(int32_t)tm, (int32_t)tn, (int32_t)tiles, 1, (int32_t)depth, (int32_t)depth, (int32_t)tiles};
     for (int64_t split : {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
         if (left == 0 || split * 4 > depth) break;
         const int64_t share = up(depth, split), parts = up(depth, share);
-        const double t = rounds(tiles - left, depth) + rounds(left * parts, share) +
+        const double t = groups_us(c, tiles - left, depth) + groups_us(c, left * parts, share) +
                          (double)(left * parts) * c.part + kJoinUs;
         if (t >= best) continue;
         best = t;
