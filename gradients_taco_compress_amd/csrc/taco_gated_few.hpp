@@ -7,8 +7,13 @@
 //    (g, r) reads chunks of feature r (and of row r of X, which stays in
 //    cache); the waves of a work-group share the summed length and add their
 //    sums in LDS, in order.
-//  * A wave's turn takes 256 bytes of each feature, all its loads issued before the
-//    products of the turn before.
+//  * A wave's turn takes 128 bytes of each feature.  All its loads are issued before
+//    they are waited for; where turns are held ahead, the next round's go out
+//    between the products of this one.
+//
+// Bound by HBM: 1 x 10240x2560 bf16 22.0 us (4.8 TB/s), 4 x 14336x3584 codes
+// 22.5 us (4.7).  Few features fill few CUs, each of which takes about 40 GB/ms
+// (1 x 256x8192: 18.7 us).
 #pragma once
 
 #include <type_traits>
@@ -18,10 +23,10 @@
 namespace taco_gated {
 namespace {
 
-template <typename E, int WAVES>
+template <typename E, int WAVES, int AHEAD>
 __global__ __launch_bounds__(WAVES * kWave) void few_kernel(Product p) {
     using El = Element<E>;
-    constexpr int SIZE = El::SIZE, TURN = 2;                     // K-tiles in a turn
+    constexpr int SIZE = El::SIZE;
     constexpr bool SCALED = El::SCALED;
     __shared__ f4v sums[WAVES > 1 ? WAVES - 1 : 1][2][kWave];
     const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, r = lane & 15;
@@ -39,63 +44,70 @@ __global__ __launch_bounds__(WAVES * kWave) void few_kernel(Product p) {
         scales[2] = static_cast<const uint8_t *>(p.a_scale.p) + m * p.a_scale.pitch;
     }
     const int64_t bytes = p.k * SIZE;
+    // A K-tile of 128 bytes of each row.
     struct Turn {
-        Fragment v[TURN][3];
-        int scale[TURN][3];
+        Fragment v[3];
+        int scale[3];
     };
-    Turn held[2];
+    Turn held[AHEAD];
     auto load = [&](int64_t turn, Turn &to) {
-        const int64_t at = turn * TURN * kDeep;
-        if (at + TURN * kDeep <= bytes) {
+        const int64_t at = turn * kDeep;
 #pragma unroll
-            for (int t = 0; t < TURN; ++t)
+        for (int s = 0; s < 3; ++s) {
 #pragma unroll
-                for (int s = 0; s < 3; ++s) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        to.v[t][s].v[h] = *reinterpret_cast<const u4v_any *>(
-                            rows[s] + at + t * kDeep + h * 64 + g * 16);
-                    if constexpr (SCALED) to.scale[t][s] = scales[s][(at + t * kDeep) / 32 + g];
-                }
-            return;
+            for (int h = 0; h < 2; ++h)
+                to.v[s].v[h] = *reinterpret_cast<const u4v_any *>(rows[s] + at + h * 64 + g * 16);
+            if constexpr (SCALED) to.scale[s] = scales[s][at / 32 + g];
         }
-        // The last turn: what is past the row's end is zero.
+    };
+    // What is left of each row: past its end is zero.
+    auto load_rest = [&](int64_t turn, Turn &to) {
+        const int64_t at = turn * kDeep;
 #pragma unroll
-        for (int t = 0; t < TURN; ++t)
+        for (int s = 0; s < 3; ++s) {
 #pragma unroll
-            for (int s = 0; s < 3; ++s) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int64_t c = at + t * kDeep + h * 64 + g * 16, left = bytes - c;
-                    to.v[t][s].v[h] = (u4v){0u, 0u, 0u, 0u};
-                    if (left > 0)
-                        to.v[t][s].v[h] = load_tail<true>(rows[s] + c, rows[s], left < 16 ? (int)left : 16);
-                }
-                if constexpr (SCALED) {
-                    const int64_t block = (at + t * kDeep) / 32 + g;
-                    to.scale[t][s] = block < p.k / 32 ? scales[s][block] : 0;
-                }
+            for (int h = 0; h < 2; ++h) {
+                const int64_t c = at + h * 64 + g * 16, left = bytes - c;
+                to.v[s].v[h] = (u4v){0u, 0u, 0u, 0u};
+                if (left > 0)
+                    to.v[s].v[h] = load_tail<true>(rows[s] + c, rows[s], left < 16 ? (int)left : 16);
             }
+            if constexpr (SCALED) {
+                const int64_t block = at / 32 + g;
+                to.scale[s] = block < p.k / 32 ? scales[s][block] : 0;
+            }
+        }
     };
     f4v gate = {0.0f, 0.0f, 0.0f, 0.0f}, up = gate;
     auto multiply = [&](const Turn &in) {
-#pragma unroll
-        for (int t = 0; t < TURN; ++t) {
-            gate = El::template run<0, 0>(in.v[t][0], in.v[t][2], gate, in.scale[t][0], in.scale[t][2]);
-            up = El::template run<0, 0>(in.v[t][1], in.v[t][2], up, in.scale[t][1], in.scale[t][2]);
-        }
+        gate = El::template run<0, 0>(in.v[0], in.v[2], gate, in.scale[0], in.scale[2]);
+        up = El::template run<0, 0>(in.v[1], in.v[2], up, in.scale[1], in.scale[2]);
     };
-    const int64_t turns = (bytes + TURN * kDeep - 1) / (TURN * kDeep);
+    const int64_t turns = bytes / kDeep;
     int64_t turn = wave;
-    if (turn < turns) load(turn, held[0]);
-    while (turn < turns) {
-        if (turn + WAVES < turns) load(turn + WAVES, held[1]);
+    // Whole rounds of AHEAD turns, the next round's loads between the products.
+    if (turn + (AHEAD - 1) * WAVES < turns) {
+        for_each<AHEAD>([&](auto i) { load(turn + decltype(i)::value * WAVES, held[decltype(i)::value]); });
+        for (turn += AHEAD * WAVES; turn + (AHEAD - 1) * WAVES < turns; turn += AHEAD * WAVES)
+            for_each<AHEAD>([&](auto i) {
+                constexpr int n = decltype(i)::value;
+                multiply(held[n]);
+                load(turn + n * WAVES, held[n]);
+            });
+        for_each<AHEAD>([&](auto i) { multiply(held[decltype(i)::value]); });
+    }
+    // Fewer than AHEAD turns, together.
+    for_each<AHEAD - 1>([&](auto i) {
+        constexpr int n = decltype(i)::value;
+        if (turn + n * WAVES < turns) load(turn + n * WAVES, held[n]);
+    });
+    for_each<AHEAD - 1>([&](auto i) {
+        constexpr int n = decltype(i)::value;
+        if (turn + n * WAVES < turns) multiply(held[n]);
+    });
+    if (turns * kDeep < bytes && turns % WAVES == wave) {
+        load_rest(turns, held[0]);
         multiply(held[0]);
-        turn += WAVES;
-        if (turn >= turns) break;
-        if (turn + WAVES < turns) load(turn + WAVES, held[0]);
-        multiply(held[1]);
-        turn += WAVES;
     }
     if constexpr (WAVES > 1) {
         if (wave > 0) {
@@ -144,7 +156,12 @@ __global__ __launch_bounds__(WAVES * kWave) void few_kernel(Product p) {
 template <typename E>
 taco_status Products<E>::few(const Product &p, hipStream_t stream) {
     const dim3 grid((unsigned)up(p.n, 16));
-    return launch(reinterpret_cast<const void *>(&few_kernel<E, 4>), grid, 4 * kWave, stream, p);
+    // Turns held at once: 1, 3 and 4 of 16-bit elements take 22.9, 22.4 and 22.0 us at
+    // 1 x 10240x2560, and of codes, whose turn is twice as long in summed elements,
+    // 13.5, 16.5 and 16.5 us.  (Four waves 22.2 and 14.1 at their best, sixteen 24.0
+    // and 15.5.)
+    constexpr int kAhead = Element<E>::SCALED ? 1 : 4;
+    return launch(reinterpret_cast<const void *>(&few_kernel<E, 8, kAhead>), grid, 8 * kWave, stream, p);
 }
 
 }  // namespace taco_gated
