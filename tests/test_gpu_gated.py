@@ -1,0 +1,532 @@
+"""The gated feed-forward block on the GPU against its formulas in 64 bits.
+
+Bounds are derived in gated_reference.py.  Where inputs are small whole numbers,
+every sum is exact in float32 and results have to be equal.  Every case
+prints its name before it touches the GPU.
+"""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from gated_reference import (ACTIVATIONS, BF, F16, F32, Backward64, Forward64, mx_decode, mx_dot_error,
+                             mx_encode)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gated():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import gradients_taco_compress_amd.gated as gated
+    return gated
+
+
+def announce(msg):
+    print(f"[case] {msg}", flush=True)
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def rows_of(rows, width, dtype, seed, scale=1.0, pitch=0, offset=0):
+    n = rows * (width + pitch) + offset
+    flat = torch.empty(n, device="cuda").normal_(0.0, scale, generator=gen(seed)).to(dtype)
+    return flat[offset:].as_strided((rows, width), (width + pitch, 1))
+
+
+def whole(rows, width, dtype, seed, most=2):
+    """Small whole numbers."""
+    return torch.randint(-most, most + 1, (rows, width), generator=gen(seed),
+                         device="cuda").to(dtype)
+
+
+def operands(rows, hidden, features, dtype, seed, pitch=0, offset=0):
+    return (rows_of(rows, hidden, dtype, seed, 1.0, pitch, offset),
+            rows_of(features, hidden, dtype, seed + 1, hidden ** -0.5, pitch, offset),
+            rows_of(features, hidden, dtype, seed + 2, hidden ** -0.5, pitch, offset))
+
+
+def check_forward(gated, x, wg, wu, kind, save=True):
+    ref = Forward64(x.double(), wg.double(), wu.double(), kind)
+    ref.check(*gated.gated_forward(x, wg, wu, kind, save=True))
+    a = gated.gated_forward(x, wg, wu, kind)
+    ref.check(a)
+    return a
+
+
+SIZES = [(1, 32, 16), (1, 2560, 640), (2, 8, 1), (3, 7, 5), (5, 1, 3), (15, 1111, 37), (16, 256, 300),
+         (17, 8, 8), (17, 40, 33), (31, 64, 64), (33, 65, 63), (64, 200, 129), (127, 128, 128),
+         (128, 136, 65), (129, 72, 130), (200, 1111, 96), (255, 63, 257), (256, 512, 256),
+         (300, 200, 136), (513, 320, 96)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("rows,hidden,features", SIZES)
+def test_forward(gated, rows, hidden, features, dtype):
+    kind = ACTIVATIONS[(rows + hidden + features) % 3]
+    announce(f"forward {rows} x {features}x{hidden} {dtype} {kind}")
+    check_forward(gated, *operands(rows, hidden, features, dtype, rows + hidden), kind)
+
+
+@pytest.mark.parametrize("kind", ACTIVATIONS)
+@pytest.mark.parametrize("rows", [4, 100])
+def test_forward_activations(gated, kind, rows):
+    announce(f"forward {kind} {rows}")
+    x, wg, wu = operands(rows, 64, 96, F16, 5)
+    check_forward(gated, x * 4, wg * 3, wu, kind)            # gates up to about 50
+
+
+@pytest.mark.parametrize("pitch,offset", [(8, 0), (24, 8), (5, 0), (0, 1), (3, 3), (4, 4)])
+@pytest.mark.parametrize("rows", [3, 70])
+def test_strides(gated, rows, pitch, offset):
+    for hidden in (64, 72, 45):
+        announce(f"forward strides {rows} {hidden} pitch {pitch} offset {offset}")
+        x, wg, wu = operands(rows, hidden, 40, BF, 9, pitch, offset)
+        check_forward(gated, x, wg, wu, "silu")
+        g, u = rows_of(rows, 40, BF, 4), rows_of(rows, 40, BF, 5)
+        da = rows_of(rows, 40, BF, 6, 0.1, pitch, offset)
+        Backward64(*(t.double() for t in (da, x, g, u, wg, wu)), "silu", BF).check(
+            *gated.gated_backward(da, x, g, u, wg, wu, "silu"))
+
+
+@pytest.mark.parametrize("rows", [2, 50])
+def test_weights_of_different_pitch_and_halves_of_one(gated, rows):
+    announce("weights of different pitch")
+    x = rows_of(rows, 64, BF, 1)
+    wg, wu = rows_of(48, 64, BF, 2, 0.1, 8), rows_of(48, 64, BF, 3, 0.1, 16)
+    check_forward(gated, x, wg, wu, "gelu")
+    both = rows_of(96, 64, BF, 7, 0.1)
+    one = gated.gated_forward(x, both[:48], both[48:])
+    assert torch.equal(one, gated.gated_forward(x, both[:48].clone(), both[48:].clone()))
+
+
+def test_leading_dimensions(gated):
+    announce("leading dimensions")
+    x, wg, wu = operands(60, 64, 40, BF, 3)
+    flat = gated.gated_forward(x, wg, wu)
+    assert torch.equal(gated.gated_forward(x.view(3, 4, 5, 64), wg, wu), flat.view(3, 4, 5, 40))
+    assert torch.equal(gated.gated_forward(x[0], wg, wu), gated.gated_forward(x[:1], wg, wu)[0])
+
+
+# Large tiles, several items a work-group, split tiles; every edge ragged.
+@pytest.mark.parametrize("rows,hidden,features", [(2053, 72, 8203), (1000, 8, 33000), (33000, 40, 130),
+                                                  (18, 16384, 24), (260, 9000, 200), (300, 24576, 520)])
+def test_exact_sums_forward(gated, rows, hidden, features):
+    announce(f"exact forward {rows} x {features}x{hidden}")
+    x, wg, wu = (whole(n, hidden, BF, i) for i, n in enumerate((rows, features, features)))
+    _, gate, up = gated.gated_forward(x, wg, wu, save=True)
+    assert torch.equal(gate, (x.float() @ wg.float().t()).to(BF))
+    assert torch.equal(up, (x.float() @ wu.float().t()).to(BF))
+
+
+@pytest.mark.parametrize("rows,hidden,features", [(64, 64, 64), (129, 136, 65), (2053, 200, 1030),
+                                                  (8200, 72, 40), (300, 264, 9000), (700, 4200, 130),
+                                                  (20000, 520, 264), (1, 8, 3), (5000, 2600, 1100)])
+def test_exact_sums_backward(gated, rows, hidden, features):
+    """silu(64) = 64 and its slope is 1 in float32: dG = dA U and dU = 64 dA are
+    whole numbers, and so are all sums."""
+    announce(f"exact backward {rows} x {features}x{hidden}")
+    da, up = whole(rows, features, BF, 1, 1), whole(rows, features, BF, 2)
+    gate = torch.full_like(up, 64.0)
+    x, wg, wu = (whole(n, hidden, BF, 3 + i) for i, n in enumerate((rows, features, features)))
+    wu = wu.clamp(-1, 1)
+    dx, dg, du = gated.gated_backward(da, x, gate, up, wg, wu)
+    f = [t.float() for t in (da, up, x, wg, wu)]
+    dgate, dup = f[0] * f[1], f[0] * 64
+    assert torch.equal(dx, (dgate @ f[3] + dup @ f[4]).to(BF))
+    assert torch.equal(dg, (dgate.t().contiguous() @ f[2]).to(BF))
+    assert torch.equal(du, (dup.t().contiguous() @ f[2]).to(BF))
+    only, none, also = gated.gated_backward(da, x, gate, up, wg, wu, weight_grads=False)
+    assert torch.equal(only, dx) and none is None and also is None
+    none, dg2, du2 = gated.gated_backward(da, x, gate, up, wg, wu, input_grad=False)
+    assert none is None and torch.equal(dg2, dg) and torch.equal(du2, du)
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("rows,hidden,features", [(1, 8, 8), (3, 7, 5), (17, 40, 33), (64, 64, 64),
+                                                  (129, 72, 130), (200, 111, 96), (300, 200, 136),
+                                                  (1000, 333, 257)])
+def test_backward(gated, rows, hidden, features, dtype):
+    kind = ACTIVATIONS[(rows + features) % 3]
+    announce(f"backward {rows} x {features}x{hidden} {dtype} {kind}")
+    x, wg, wu = operands(rows, hidden, features, dtype, rows)
+    g, u = rows_of(rows, features, dtype, 21, 3.0), rows_of(rows, features, dtype, 22)
+    da = rows_of(rows, features, dtype, 23, 0.1)
+    Backward64(*(t.double() for t in (da, x, g, u, wg, wu)), kind, dtype).check(
+        *gated.gated_backward(da, x, g, u, wg, wu, kind))
+
+
+def test_backward_with_projections_of_different_pitch(gated):
+    announce("backward, gate and up of different pitch")
+    x, wg, wu = operands(20, 24, 16, BF, 1)
+    g, u, da = rows_of(20, 16, BF, 2, 1.0, 8), rows_of(20, 16, BF, 3), rows_of(20, 16, BF, 4)
+    Backward64(*(t.double() for t in (da, x, g, u, wg, wu)), "silu", BF).check(
+        *gated.gated_backward(da, x, g, u, wg, wu))
+
+
+@pytest.mark.parametrize("kind", ACTIVATIONS)
+def test_activation_slopes_far_out(gated, kind):
+    """Gates from float16's smallest to its largest: slopes 0 and 1, no NaN."""
+    announce(f"slopes {kind}")
+    g = torch.tensor([0.0, 6e-8, 1e-3, 0.5, 1.0, 3.0, 8.0, 11.0, 20.0, 300.0, 65504.0], device="cuda")
+    g = torch.cat([g, -g]).to(F16)[None].contiguous()
+    n = g.shape[1]
+    eye = torch.eye(n, device="cuda", dtype=F16)
+    one = torch.ones_like(g)
+    x = torch.zeros(1, n, device="cuda", dtype=F16)
+    dx, _, _ = gated.gated_backward(one, x, g, one, eye, torch.zeros_like(eye), kind)
+    ref = Backward64(*(t.double() for t in (one, x, g, one, eye, torch.zeros_like(eye))), kind, F16)
+    ref.check(dx, None, None)
+    assert float(dx[0, 10]) == 1.0 and float(dx[0, -1]) == 0.0
+    # forward: A = act(G) for U = 1
+    xs = torch.cat([g.view(-1, 1), torch.ones(n, 1, device="cuda", dtype=F16)], 1).contiguous()
+    a = gated.gated_forward(xs, torch.tensor([[1.0, 0.0]], device="cuda", dtype=F16),
+                            torch.tensor([[0.0, 1.0]], device="cuda", dtype=F16), kind)
+    Forward64(xs.double(), torch.tensor([[1.0, 0.0]], device="cuda", dtype=torch.float64),
+              torch.tensor([[0.0, 1.0]], device="cuda", dtype=torch.float64), kind).check(a)
+
+
+@pytest.mark.parametrize("rows", [5, 150])
+def test_nan_and_infinities_stay_in_their_rows_and_columns(gated, rows):
+    announce(f"nan {rows}")
+    x, wg, wu = operands(rows, 72, 70, BF, 1)
+    clean = gated.gated_forward(x, wg, wu)
+    x2, wg2 = x.clone(), wg.clone()
+    x2[3, 70], wg2[69, 1] = float("nan"), float("inf")
+    a = gated.gated_forward(x2, wg2, wu)
+    assert bool(a[3].isnan().all()) and bool((~a[:, 69].isfinite()).all())
+    keep = torch.ones_like(a, dtype=torch.bool)
+    keep[3], keep[:, 69] = False, False
+    assert torch.equal(a[keep], clean[keep])
+
+
+@pytest.mark.parametrize("rows", [9, 140])
+def test_neighbours_are_left_alone(gated, rows):
+    """Outputs in wider buffers, NaN around every operand."""
+    announce(f"neighbours {rows}")
+
+    def surrounded(r, w, seed, scale=1.0):
+        full = torch.full((r + 4, w + 16), float("nan"), device="cuda", dtype=BF)
+        full[2:-2, 8:-8] = rows_of(r, w, BF, seed, scale)
+        return full[2:-2, 8:-8]
+    for hidden, features in ((72, 40), (67, 37)):
+        x, wg, wu = (surrounded(n, hidden, i, 0.2) for i, n in enumerate((rows, features, features)))
+        out = torch.full((rows + 2, features + 6), 7.0, device="cuda", dtype=BF)
+        view = out[1:-1, 3:3 + features]
+        gated.gated_forward(x, wg, wu, out=view)
+        assert torch.equal(view, gated.gated_forward(x.contiguous(), wg.contiguous(), wu.contiguous()))
+        view.fill_(7.0)
+        assert bool((out == 7.0).all())
+        g, u, da = (surrounded(rows, features, 5 + i) for i in range(3))
+        got = gated.gated_backward(da, x, g, u, wg, wu)
+        want = gated.gated_backward(*(t.contiguous() for t in (da, x, g, u, wg, wu)))
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+def test_no_rows(gated):
+    announce("no rows")
+    x, wg, wu = operands(4, 64, 40, BF, 1)
+    a, gate, up = gated.gated_forward(x[:0], wg, wu, save=True)
+    assert a.shape == gate.shape == up.shape == (0, 40)
+    dx, dg, du = gated.gated_backward(a, x[:0], gate, up, wg, wu)
+    assert dx.shape == (0, 64) and float(dg.abs().sum()) == float(du.abs().sum()) == 0.0
+    assert dg.shape == du.shape == (40, 64)
+    xm, gm, um = gated.mx_encode(x[:0]), gated.mx_encode(wg), gated.mx_encode(wu)
+    assert gated.gated_forward_mx(xm, gm, um).shape == (0, 40)
+
+
+def test_offsets_past_32_bits(gated):
+    """Rows of x and of the output beyond 4 GiB from the first."""
+    announce("offsets past 32 bits")
+    rows, pitch = 300, 1 << 23
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GiB")
+    full = torch.empty(rows * pitch, device="cuda", dtype=BF)
+    x = full.as_strided((rows, 64), (pitch, 1))
+    out = full[4096:].as_strided((rows, 40), (pitch, 1))
+    small, wg, wu = operands(rows, 64, 40, BF, 3)
+    x.copy_(small)
+    want = gated.gated_forward(small, wg, wu)
+    gated.gated_forward(x, wg, wu, out=out)              # the pitch is past what is read in place
+    assert torch.equal(out, want)
+    assert torch.equal(gated.gated_forward(x[:10], wg, wu), gated.gated_forward(small[:10], wg, wu))
+
+
+def test_results_repeat(gated):
+    announce("repeat")
+    x, wg, wu = operands(500, 2000, 300, BF, 1)
+    g, u, da = (rows_of(500, 300, BF, 5 + i) for i in range(3))
+    one = (gated.gated_forward(x, wg, wu), *gated.gated_backward(da, x, g, u, wg, wu))
+    for _ in range(3):
+        two = (gated.gated_forward(x, wg, wu), *gated.gated_backward(da, x, g, u, wg, wu))
+        assert all(torch.equal(p, q) for p, q in zip(one, two))
+
+
+def test_another_stream(gated):
+    announce("another stream")
+    s = torch.cuda.Stream()
+    x, wg, wu = operands(200, 320, 96, BF, 1)
+    g, u, da = (rows_of(200, 96, BF, 5 + i) for i in range(3))
+    want = (gated.gated_forward(x, wg, wu), *gated.gated_backward(da, x, g, u, wg, wu))
+    xm, gm, um = (gated.mx_encode(t) for t in (x, wg, wu))
+    want_mx = gated.gated_forward_mx(xm, gm, um)
+    torch.cuda.synchronize()
+    got = (gated.gated_forward(x, wg, wu, stream=s),
+           *gated.gated_backward(da, x, g, u, wg, wu, stream=s))
+    got_mx = gated.gated_forward_mx(xm, gm, um, stream=s)
+    codes, scales = gated.mx_encode(x, stream=s)
+    with torch.cuda.stream(s):
+        inside = gated.gated_forward(x, wg, wu)
+    s.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got, want)) and torch.equal(inside, want[0])
+    assert torch.equal(got_mx, want_mx) and torch.equal(codes, xm[0]) and torch.equal(scales, xm[1])
+
+
+def test_graph_replays(gated):
+    """Forward, backward and the 8-bit pass in one graph, with split tiles and copies
+    of ragged operands; eager calls between the replays."""
+    announce("graph")
+    x, wg, wu = operands(130, 1111, 60, BF, 1)
+    da = rows_of(130, 60, BF, 9)
+    xm, gm, um = (gated.mx_encode(t[:, :1088].contiguous()) for t in (x, wg, wu))
+
+    def step():
+        a, gate, up = gated.gated_forward(x, wg, wu, save=True)
+        return (a, *gated.gated_backward(da, x, gate, up, wg, wu), gated.gated_forward_mx(xm, gm, um),
+                gated.gated_forward(x[:3], wg, wu))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for turn in range(4):
+        x.copy_(rows_of(130, 1111, BF, 30 + turn))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in outs]
+        assert all(torch.equal(p, q) for p, q in zip(got, step())), turn
+
+
+# ------------------------------------------------------------------ 8 bits --
+
+@pytest.mark.parametrize("dtype", [BF, F16, F32])
+def test_encode(gated, dtype):
+    announce(f"encode {dtype}")
+    x = rows_of(70, 96, F32, 1, 1.0)
+    x[0], x[1, 32:64] = 0.0, 0.0
+    x[2] *= 1e-30 if dtype != F16 else 1e-6
+    x[3, :32] = 448.0
+    x[4, :32], x[4, 32] = 1e-3, 449.0
+    x[5] = torch.linspace(-448, 448, 96, device="cuda")
+    if dtype != F16:
+        x[6] *= 1e30
+        x[7] *= 2.0 ** -128
+        x[8, 5] = 3e38
+    x = x.to(dtype)
+    codes, scales = gated.mx_encode(x)
+    want_codes, want_scales = mx_encode(x.float())
+    assert torch.equal(scales, want_scales) and torch.equal(codes, want_codes)
+    wide = torch.zeros(70, 101, device="cuda", dtype=dtype)
+    wide[:, 3:99] = x
+    again = gated.mx_encode(wide[:, 3:99])
+    assert torch.equal(again[0], codes) and torch.equal(again[1], scales)
+
+
+def test_encode_of_values_that_are_not_finite(gated):
+    announce("encode nan")
+    x = rows_of(4, 96, BF, 1)
+    x[1, 40], x[2, 3], x[3, 95] = float("nan"), float("inf"), -float("inf")
+    codes, scales = gated.mx_encode(x)
+    want_codes, want_scales = mx_encode(x.float())
+    assert torch.equal(scales, want_scales) and torch.equal(codes, want_codes)
+    assert scales.flatten().tolist().count(255) == 3
+
+
+def test_every_code_and_scale_is_encoded_as_itself(gated):
+    announce("encode itself")
+    codes = torch.arange(127, device="cuda", dtype=torch.uint8)
+    v = codes.view(torch.float8_e4m3fn).float()
+    x = torch.zeros(127, 32, device="cuda")
+    x[:, 0], x[:, 1] = v, 448.0
+    got, scales = gated.mx_encode(x)
+    assert torch.equal(got[:, 0], codes) and bool((scales == 127).all())
+    powers = torch.exp2(torch.arange(-110, 119, device="cuda", dtype=torch.float64)).float()
+    got, scales = gated.mx_encode((powers[:, None] * 448).expand(-1, 32).contiguous())
+    assert bool((got == 126).all())
+    assert scales.flatten().tolist() == list(range(17, 246))
+
+
+MX_SIZES = [(1, 32, 16), (3, 64, 5), (4, 1120, 40), (16, 96, 300), (17, 32, 8), (31, 128, 64),
+            (64, 160, 129), (130, 512, 65), (200, 1184, 96), (256, 256, 256), (300, 224, 136)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("rows,hidden,features", MX_SIZES)
+def test_forward_mx(gated, rows, hidden, features, dtype):
+    kind = ACTIVATIONS[rows % 3]
+    announce(f"mx {rows} x {features}x{hidden} {dtype} {kind}")
+    # blocks of very different size
+    size = torch.exp2(torch.randint(-6, 7, (1, hidden // 32), generator=gen(5), device="cuda").float())
+    size = size.repeat_interleave(32, 1)
+    x, wg, wu = operands(rows, hidden, features, F32, rows)
+    x, wg, wu = x * size, wg / size, wu / size
+    pairs = [gated.mx_encode(t) for t in (x, wg, wu)]
+    d = [mx_decode(*p) for p in pairs]
+    ref = Forward64(*d, kind, (mx_dot_error(d[0], d[1]), mx_dot_error(d[0], d[2])))
+    a = gated.gated_forward_mx(*pairs, kind, dtype=dtype)
+    assert a.dtype == dtype
+    ref.check(a)
+
+
+# Large tiles, split tiles, several items; sums of powers of two are exact.
+@pytest.mark.parametrize("rows,hidden,features", [(2053, 96, 8203), (18, 16384, 24), (300, 24576, 520),
+                                                  (1000, 32, 33000)])
+def test_exact_sums_mx(gated, rows, hidden, features):
+    announce(f"exact mx {rows} x {features}x{hidden}")
+    x, wg, wu = (whole(n, hidden, F32, i, 1) for i, n in enumerate((rows, features, features)))
+    # U = 64 in every row, by a column of its own: A = 64 silu(G)
+    x[:, 0], wg[:, 0], wu[:, :] = 8.0, 0.0, 0.0
+    wu[:, 0] = 8.0
+    pairs = [gated.mx_encode(t) for t in (x, wg, wu)]
+    a = gated.gated_forward_mx(*pairs)
+    g = x @ wg.t()
+    want = torch.nn.functional.silu(g.double()) * 64
+    # silu of a whole number, a few float32 roundings and one to bf16
+    assert bool(((a.double() - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -16) + 1e-30).all())
+
+
+@pytest.mark.parametrize("rows", [5, 150])
+def test_nan_blocks_in_the_8_bit_pass(gated, rows):
+    announce(f"mx nan {rows}")
+    x, wg, wu = operands(rows, 160, 70, BF, 1)
+    clean = gated.gated_forward_mx(*(gated.mx_encode(t) for t in (x, wg, wu)))
+    x[3, 140], wg[69, 1] = float("nan"), float("inf")
+    a = gated.gated_forward_mx(*(gated.mx_encode(t) for t in (x, wg, wu)))
+    assert bool(a[3].isnan().all()) and bool(a[:, 69].isnan().all())
+    keep = torch.ones_like(a, dtype=torch.bool)
+    keep[3], keep[:, 69] = False, False
+    assert torch.equal(a[keep], clean[keep])
+
+
+# ---------------------------------------------------------------- autograd --
+
+@pytest.mark.parametrize("kind", ACTIVATIONS)
+def test_autograd_against_64_bits(gated, kind):
+    announce(f"autograd {kind}")
+    x, wg, wu = (t.requires_grad_() for t in operands(6, 40, 24, BF, 2))
+    a = gated.gated(x.view(2, 3, 40), wg, wu, kind)
+    dy = rows_of(6, 24, BF, 8)
+    a.backward(dy.view(2, 3, 24))
+    assert x.grad.shape == x.shape
+    f = Forward64(x.detach().double(), wg.detach().double(), wu.detach().double(), kind)
+    f.check(a.detach().view(6, 24))
+    xd, wgd, wud = (t.detach().double().requires_grad_() for t in (x, wg, wu))
+    g, u = xd @ wgd.t(), xd @ wud.t()
+    act = {"silu": torch.nn.functional.silu, "gelu": torch.nn.functional.gelu,
+           "gelu_tanh": lambda v: torch.nn.functional.gelu(v, approximate="tanh")}[kind]
+    (act(g) * u).backward(dy.double())
+    for got, want in ((x.grad, xd.grad), (wg.grad, wgd.grad), (wu.grad, wud.grad)):
+        # G, U, dG, dU and the result are rounded to bf16: four half steps of terms that
+        # the sums weigh alike
+        assert float((got.double() - want).norm() / want.norm()) < 4 * 2.0 ** -8
+
+
+def test_gradients_are_differences(gated):
+    """The gradient along a direction against differences of the forward pass in
+    float16, whose steps are small enough for a difference of 1 % of the size."""
+    announce("differences")
+    x, wg, wu = operands(4, 64, 32, F16, 3)
+    dy = rows_of(4, 32, F16, 8)
+
+    def loss(*t):
+        return float((gated.gated_forward(*t).double() * dy.double()).sum())
+    leaves = [t.clone().requires_grad_() for t in (x, wg, wu)]
+    gated.gated(*leaves).backward(dy)
+    for i, t in enumerate((x, wg, wu)):
+        # along the gradient itself, by h of its norm's inverse: the change is 2 h |grad|
+        g = leaves[i].grad.double()
+        h = 0.02 * float(t.double().norm() / g.norm())
+        args = [x, wg, wu]
+        args[i] = (t.double() + h * g).to(F16)
+        up = loss(*args)
+        step_up = args[i].double() - t.double()
+        args[i] = (t.double() - h * g).to(F16)
+        down = loss(*args)
+        step_down = args[i].double() - t.double()
+        want = float((g * (step_up - step_down)).sum())
+        # third-order terms (0.02^2 of the size, times a few) and A's roundings,
+        # 128 values of half a step each at random
+        assert abs((up - down) - want) < 0.02 * abs(want)
+
+
+def test_autograd_asks_for_what_is_needed(gated):
+    announce("autograd needs")
+    x, wg, wu = operands(20, 40, 24, BF, 2)
+    full = [t.clone().requires_grad_() for t in (x, wg, wu)]
+    gated.gated(*full).sum().backward()
+    for need in ((1, 0, 0), (0, 1, 0), (0, 0, 1), (0, 1, 1)):
+        leaves = [t.clone().requires_grad_(bool(n)) for t, n in zip((x, wg, wu), need)]
+        gated.gated(*leaves).sum().backward()
+        for leaf, f, n in zip(leaves, full, need):
+            assert (leaf.grad is None) if not n else torch.equal(leaf.grad, f.grad)
+    with torch.no_grad():
+        assert torch.equal(gated.gated(x, wg, wu), gated.gated_forward(x, wg, wu))
+    # a transposed x, and a gradient that is an expanded one
+    xt = x.t().contiguous().t().requires_grad_()
+    gated.gated(xt, wg, wu).sum().backward()
+    assert torch.equal(xt.grad, full[0].grad)
+
+
+# ---------------------------------------------------------------- refusals --
+
+def test_refusals(gated):
+    announce("refusals")
+    x, wg, wu = operands(4, 64, 32, BF, 1)
+    g, u, da = (rows_of(4, 32, BF, 5 + i) for i in range(3))
+    with pytest.raises(ValueError, match="activation"):
+        gated.gated_forward(x, wg, wu, "relu")
+    with pytest.raises(ValueError, match="activation"):
+        gated.gated_backward(da, x, g, u, wg, wu, None)
+    for bad in (x.float(), x.double()):
+        with pytest.raises(TypeError, match="bfloat16 or float16"):
+            gated.gated_forward(bad, wg, wu)
+    with pytest.raises(TypeError, match="gate_weight must be"):
+        gated.gated_forward(x, wg.half(), wu)
+    with pytest.raises(TypeError, match="CUDA/HIP"):
+        gated.gated_forward(x, wg.cpu(), wu)
+    for bad in (wu[:31], wu[:, :63], wu.view(-1), wu.t()):
+        with pytest.raises(ValueError):
+            gated.gated_forward(x, wg, bad)
+    with pytest.raises(ValueError, match="rows must be contiguous"):
+        gated.gated_forward(x.t().contiguous().t(), wg, wu)
+    with pytest.raises(ValueError, match="out must be"):
+        gated.gated_forward(x, wg, wu, out=torch.empty(32, 4, device="cuda", dtype=BF))
+    with pytest.raises(TypeError, match="out must be"):
+        gated.gated_forward(x, wg, wu, out=torch.empty(4, 32, device="cuda"))
+    square = torch.zeros(64, 64, device="cuda", dtype=BF)
+    with pytest.raises(gated.TacoError, match="ALIAS"):
+        gated.gated_forward(square, square, square.clone(), out=square)
+    for args in ((da[:3], x, g, u), (da, x[:3], g, u), (da, x, g[:, :31], u), (da, x, g, u.float())):
+        with pytest.raises((ValueError, TypeError)):
+            gated.gated_backward(*args, wg, wu)
+    xm, gm, um = (gated.mx_encode(t) for t in (x, wg, wu))
+    for args in ((xm[0], gm, um), ((xm[0], xm[1][:2]), gm, um), ((xm[0], xm[1].float()), gm, um),
+                 (xm, (gm[0][:31], gm[1][:31]), um), (xm, gm, (um[0].t(), um[1])),
+                 ((xm[0][:, :32].contiguous(), xm[1][:, :1].contiguous()), gm, um)):
+        with pytest.raises((ValueError, TypeError)):
+            gated.gated_forward_mx(*args)
+    with pytest.raises(TypeError, match="dtype"):
+        gated.gated_forward_mx(xm, gm, um, dtype=F32)
+    with pytest.raises(ValueError, match="multiple of 32"):
+        gated.mx_encode(x[:, :40])
+    # codes off 16 bytes
+    shifted = torch.zeros(4 * 64 + 8, device="cuda", dtype=torch.uint8)[8:].view(4, 64)
+    with pytest.raises(gated.TacoError, match="ALIGN"):
+        gated.gated_forward_mx((shifted, xm[1]), gm, um)
