@@ -105,9 +105,11 @@ struct Element<Codes> {
 
 // Shape of a work-group: BM x BN outputs by WM x WN waves.  (Forward: BN / 2
 // features.)
-template <int BM_, int BN_, int WM_, int WN_>
+template <int BM_, int BN_, int WM_, int WN_, int RING_>
 struct Shape {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+    static constexpr int RING = RING_;                                 // K-tiles in LDS
+    static_assert(RING == 2 || RING == 4, "F and S change places with every K-tile");
     static constexpr int THREADS = WM * WN * kWave;
     static constexpr int HM = BM / 2, HN = BN / 2;                     // a half's rows
     static constexpr int MF = HM / WM / 16, NF = HN / WN / 16;         // a wave's fragments of it
@@ -121,11 +123,16 @@ struct Shape {
     // two to a CU, and few; the bookkeeping only costs them (999 x 1030x1111
     // backward 57 us instead of 51).
     static constexpr bool WALKS = BM == 256;
+    // Register sets for the halves of A: large tiles have none to spare, the others
+    // read a half in one go (1 to 2 % less time).
+    static constexpr int SETS = BM == 256 ? 1 : 2;
     // A split's partial sums.
     static constexpr int64_t SLAB = (int64_t)BM * BN;
 };
-using Large = Shape<256, 256, 2, 4>;
-using Small = Shape<128, 128, 2, 2>;
+using Large = Shape<256, 256, 2, 4, 2>;
+using Small = Shape<128, 128, 2, 2, 2>;
+// One to a CU, for few tiles: its loads are asked for three K-tiles ahead.
+using Deep = Shape<128, 128, 2, 2, 4>;
 
 // The items of work: the first `whole` are a tile each; the remaining tiles are cut
 // into `parts` parts of `share` K-tiles.  Work-group b of a grid of g takes items b,
@@ -239,19 +246,24 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
     // not wait for it.  It tells few of them apart, so what is never loaded and
     // read at the same time shares one: the halves of B and the scales.
     constexpr int SCALES = SCALED ? THREADS * 4 : 0;           // [A0 | A1 | B0 | B1], bytes
-    __shared__ __align__(1024) uint8_t a00[S::A_HALF], a01[S::A_HALF], a10[S::A_HALF],
-        a11[S::A_HALF], b0[2 * S::B_HALF + SCALES], b1[2 * S::B_HALF + SCALES];
+    constexpr bool APART = S::RING == 2;                       // halves of A have their own
+    constexpr int B_AT = APART ? 0 : 2 * S::A_HALF, S_AT = B_AT + 2 * S::B_HALF;
+    constexpr int HALF = APART ? S::A_HALF : 1, REST = S_AT + SCALES;
+    __shared__ __align__(1024) uint8_t a00[HALF], a01[HALF], a10[HALF], a11[HALF], b0[REST], b1[REST],
+        b2[APART ? 1 : REST], b3[APART ? 1 : REST];
+    auto lds = [&](auto stage) -> uint8_t * {
+        constexpr int s = decltype(stage)::value % S::RING;
+        return s == 0 ? b0 : s == 1 ? b1 : s == 2 ? b2 : b3;
+    };
     auto lds_a = [&](auto stage, auto half) -> uint8_t * {
-        constexpr int i = decltype(stage)::value * 2 + decltype(half)::value;
-        return i == 0 ? a00 : i == 1 ? a01 : i == 2 ? a10 : a11;
+        constexpr int s = decltype(stage)::value % S::RING, h = decltype(half)::value;
+        if constexpr (!APART) return lds(stage) + h * S::A_HALF;
+        else return s == 0 ? (h == 0 ? a00 : a01) : (h == 0 ? a10 : a11);
     };
     auto lds_b = [&](auto stage, auto half) -> uint8_t * {
-        constexpr int s = decltype(stage)::value, h = decltype(half)::value;
-        return (s == 0 ? b0 : b1) + h * S::B_HALF;
+        return lds(stage) + B_AT + decltype(half)::value * S::B_HALF;
     };
-    [[maybe_unused]] auto lds_s = [&](auto stage) -> uint8_t * {      // scales
-        return (decltype(stage)::value == 0 ? b0 : b1) + 2 * S::B_HALF;
-    };
+    [[maybe_unused]] auto lds_s = [&](auto stage) -> uint8_t * { return lds(stage) + S_AT; };   // scales
 
     const int tid = threadIdx.x;
     [[maybe_unused]] const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -311,7 +323,7 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
     struct Item {
         const char *a, *b, *scale;
         int here_a[2], here_b[2], here_scale;
-        int kt0, count, even;              // even: count, rounded up to two
+        int kt0, count, end;               // end: count, rounded up to a whole ring
         int part;                          // of a split tile, else -1
         Tile tile;
     };
@@ -337,7 +349,7 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
             const int left = plan.depth - it.kt0;
             it.count = left < plan.share ? left : plan.share;
         }
-        it.even = (it.count + 1) & ~1;
+        it.end = (it.count + S::RING - 1) / S::RING * S::RING;
         it.tile = tile_at(plan, t);
         const int which = K == Kind::kWeight && it.tile.m >= per_m;
         const int64_t m0 = (int64_t)(it.tile.m - which * per_m) * S::BM;
@@ -360,7 +372,7 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
     Item cur = item_at(j), next = cur;
 
     // Loads.  K-tile kt counts from the current item's first; those past its last
-    // (and past an odd last one) are the next item's, whose loads so begin
+    // (and past a whole ring of them) are the next item's, whose loads so begin
     // before the current one's outputs are formed.  All of this is the same for
     // every lane but the offset, which is out of bounds for chunks past a row's end,
     // and all choices are selects: a branch here would part the products from what
@@ -401,8 +413,8 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
     };
     auto load_a = [&](auto stage, auto half, int kt) {
         constexpr int h = decltype(half)::value;
-        const bool on = S::WALKS && kt >= cur.even;
-        const int local = on ? kt - cur.even : kt;
+        const bool on = S::WALKS && kt >= cur.end;
+        const int local = on ? kt - cur.end : kt;
         load_half(Int<A_TURNED>{}, lds_a(stage, half), on ? next.a : cur.a, step_a, second_a,
                   (int64_t)(h * HM) * (A_TURNED ? SIZE : pitch_a), on ? next.here_a[h] : cur.here_a[h],
                   pitch_a, off_a, chunk_a, local, local + (on ? next.kt0 : cur.kt0),
@@ -410,8 +422,8 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
     };
     auto load_b = [&](auto stage, auto half, int kt) {
         constexpr int h = decltype(half)::value;
-        const bool on = S::WALKS && kt >= cur.even;
-        const int local = on ? kt - cur.even : kt;
+        const bool on = S::WALKS && kt >= cur.end;
+        const int local = on ? kt - cur.end : kt;
         // (forward: the second half is the same rows of the other weight)
         load_half(Int<B_TURNED>{}, lds_b(stage, half), on ? next.b : cur.b, step_b, second_b,
                   h == 0 ? 0 : K == Kind::kForward ? second_b : (int64_t)HN * SIZE,
@@ -423,8 +435,8 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
     auto load_scales = [&](auto stage, int kt) {
 #if defined(__HIP_DEVICE_COMPILE__)
         if constexpr (SCALED) {
-            const bool on = S::WALKS && kt >= cur.even;
-            const int local = on ? kt - cur.even : kt;
+            const bool on = S::WALKS && kt >= cur.end;
+            const int local = on ? kt - cur.end : kt;
             const int records = local < (on ? next.count : cur.count)
                                     ? on ? next.here_scale : cur.here_scale : 0;
             const auto r = __builtin_amdgcn_make_buffer_rsrc(
@@ -467,13 +479,13 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
         return f;
     };
     // The scales of a wave's fragments of a half share a register, a byte each.
-    Fragment fa[MF], fb[2][NF];
+    Fragment fa[S::SETS][MF], fb[2][NF];
     int sa[2] = {}, sb[2] = {};
     // Where they are among those of a K-tile (see ScaleTiles), from the first
     // fragment's row on.  (Opaque: a sum taken apart into several additions to the
     // pointer hides from the compiler which variable is read.)
     auto scales_at = [&](int row) {
-        int at = 2 * S::B_HALF + (row / 64 * 64 + place.g * 16 + place.r) * 4 + row % 64 / 16;
+        int at = S_AT + (row / 64 * 64 + place.g * 16 + place.r) * 4 + row % 64 / 16;
         asm volatile("" : "+v"(at));
         return at;
     };
@@ -483,7 +495,7 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
         at_sb = scales_at(2 * HM + place.wn * (HN / S::WN));
     }
     auto read_scales = [&](auto stage, int at, auto count) {
-        [[maybe_unused]] const uint8_t *const q = (decltype(stage)::value == 0 ? b0 : b1) + at;
+        [[maybe_unused]] const uint8_t *const q = lds(stage) + at;
         if constexpr (decltype(count)::value == 4) return *reinterpret_cast<const int *>(q);
         else return (int)*reinterpret_cast<const uint16_t *>(q);
     };
@@ -493,7 +505,7 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
     };
     auto read_a = [&](auto stage, auto half, auto index) {
         constexpr int i = decltype(index)::value;
-        fa[i] = read(Int<A_TURNED>{}, lds_a(stage, half), at_a, i);
+        fa[decltype(half)::value % S::SETS][i] = read(Int<A_TURNED>{}, lds_a(stage, half), at_a, i);
     };
     auto read_b = [&](auto stage, auto half) {
         constexpr int h = decltype(half)::value;
@@ -509,26 +521,26 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
         for_each<NF>([&](auto fj) {
             constexpr int j = decltype(fj)::value;
             sum[a][b][i][j] =
-                El::template run<j, i>(fb[b][j], fa[i], sum[a][b][i][j], sb[b], sa[a]);
+                El::template run<j, i>(fb[b][j], fa[a % S::SETS][i], sum[a][b][i][j], sb[b], sa[a]);
         });
     };
 
-    // K-tile t of an item lies in stage t % 2 (items take an even number of them).
+    // K-tile t of an item lies in stage t % RING (items take whole rings of them: an
+    // exit in between would make the compiler wait for all loads at its target).
     // Loads are in the order A0, F, scales, S, A1 of each K-tile, so "the half has
     // arrived" is a count of those after it.
     using C0 = Int<0>;
     using C1 = Int<1>;
-    constexpr int L = S::LOADS, SL = SCALED ? 1 : 0;
-    load_a(C0{}, C0{}, 0);
-    load_b(C0{}, C0{}, 0);
-    load_scales(C0{}, 0);
-    load_b(C0{}, C1{}, 0);
-    load_a(C0{}, C1{}, 0);
-    load_a(C1{}, C0{}, 1);
-    load_b(C1{}, C1{}, 1);
-    load_scales(C1{}, 1);
-    load_b(C1{}, C0{}, 1);
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(4 * L + SL) : "memory");
+    constexpr int L = S::LOADS, SL = SCALED ? 1 : 0, RING = S::RING;
+    for_each<RING>([&](auto stage) {
+        constexpr int t = decltype(stage)::value;
+        load_a(stage, C0{}, t);
+        load_b(stage, Int<t & 1>{}, t);
+        load_scales(stage, t);
+        load_b(stage, Int<1 - (t & 1)>{}, t);
+        if constexpr (t + 1 < RING) load_a(stage, C1{}, t);
+    });
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((RING - 1) * (4 * L + SL)) : "memory");
     read_a_scales(C0{}, C0{});
     for_each<MF>([&](auto i) { read_a(C0{}, C0{}, i); });
     read_b(C0{}, C0{});
@@ -539,40 +551,45 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
         asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(decltype(later)::value) : "memory");
         pin();
     };
+    // The products of a half of A that is used for the last time with half b of B, and
+    // the reads of the half that follows it.
+    auto last_use = [&](auto qa, auto qb, auto stage, auto half) {
+        read_a_scales(stage, half);
+        if constexpr (S::SETS == 2) for_each<MF>([&](auto i) { read_a(stage, half, i); });
+        for_each<MF>([&](auto i) {
+            multiply(qa, qb, i);
+            if constexpr (S::SETS == 1) {
+                pin();
+                read_a(stage, half, i);
+            }
+        });
+        pin();
+    };
     auto k_tile = [&](auto stage, int kt) {
         using Now = decltype(stage);
-        using Next = Int<1 - Now::value>;
-        using F = Int<Now::value>;
-        using G = Int<1 - Now::value>;               // S above
+        using Next = Int<(Now::value + 1) % RING>;
+        using Before = Int<(Now::value + RING - 1) % RING>;
+        using F = Int<Now::value & 1>;
+        using G = Int<1 - F::value>;                 // S above
         // (A0, F)
-        load_a(Next{}, C1{}, kt + 1);
+        if constexpr (APART) load_a(Before{}, C1{}, kt + RING - 1);
         read_b(Now{}, G{});
+        if constexpr (!APART) load_a(Before{}, C1{}, kt + RING - 1);
         for_each<MF>([&](auto i) { multiply(C0{}, F{}, i); });
-        barrier(Int<4 * L + SL>{});
-        // (A0, S), A1 into the place of A0
-        load_a(Now{}, C0{}, kt + 2);
-        read_a_scales(Now{}, C1{});
-        for_each<MF>([&](auto i) {
-            multiply(C0{}, G{}, i);
-            pin();
-            read_a(Now{}, C1{}, i);
-        });
-        pin();
+        barrier(Int<(RING - 1) * (4 * L + SL)>{});
+        // (A0, S), A1 read.  (A load into the variable that is read follows the reads.)
+        if constexpr (APART) load_a(Now{}, C0{}, kt + RING);
+        last_use(C0{}, G{}, Now{}, C1{});
+        if constexpr (!APART) load_a(Now{}, C0{}, kt + RING);
         // (A1, S)
-        load_b(Now{}, F{}, kt + 2);
+        load_b(Now{}, F{}, kt + RING);
         for_each<MF>([&](auto i) { multiply(C1{}, G{}, i); });
-        barrier(Int<3 * L>{});
-        // (A1, F), the next A0 into the place of A1, the next F into that of S
-        load_scales(Now{}, kt + 2);
-        load_b(Now{}, G{}, kt + 2);
+        barrier(Int<3 * L + (RING - 2) * (4 * L + SL)>{});
+        // (A1, F), the next A0 and F read
+        load_scales(Now{}, kt + RING);
+        load_b(Now{}, G{}, kt + RING);
         read_b(Next{}, G{});
-        read_a_scales(Next{}, C0{});
-        for_each<MF>([&](auto i) {
-            multiply(C1{}, F{}, i);
-            pin();
-            read_a(Next{}, C0{}, i);
-        });
-        pin();
+        last_use(C1{}, F{}, Next{}, C0{});
     };
     for (;;) {
         if constexpr (S::WALKS) {
@@ -588,9 +605,13 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
 #pragma unroll
                 for (int e = 0; e < NF; ++e)
                     sum[q >> 1][q & 1][i][e] = (f4v){0.0f, 0.0f, 0.0f, 0.0f};
-        for (int kt = 0; kt < cur.even; kt += 2) {
+        for (int kt = 0; kt < cur.end; kt += RING) {
             k_tile(C0{}, kt);
             k_tile(C1{}, kt + 1);
+            if constexpr (RING == 4) {
+                k_tile(Int<2>{}, kt + 2);
+                k_tile(Int<3>{}, kt + 3);
+            }
         }
         if (cur.part >= 0) {
             float *const slab = p.slabs + (int64_t)cur.part * S::SLAB;
@@ -642,8 +663,9 @@ __global__ __launch_bounds__(S::THREADS) void join_kernel(Product p, Plan plan) 
 
 inline int64_t up(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
+enum class Size { kLarge, kSmall, kDeep };
 struct Choice {
-    bool large;
+    Size size;
     Plan plan;
     int64_t split_tiles, slab_floats;
 };
@@ -656,14 +678,19 @@ struct Choice {
 //     large, 256 / 512 / 768 tiles    33, 57, 104 / 63, 113, 205 / 91, 165, 307
 //     large, 32 / 128 tiles           25, 42, 76 / 28, 45, 78
 //     small, 512 / 1024 / 2048 tiles  25, 37, 69 / 39, 71, 133 / 74, 137, 259
-//     small, 128 / 256 tiles          15, 23, 39 / 15, 24, 41
-// A K-tile of codes takes the same time as one of 16-bit elements.
+//     small, 128 / 256 tiles          15, 23, 38 / 15, 23, 41
+//     deep, 128 / 256 / 512 tiles     15, 21, 34 / 15, 21, 38 / 24, 40, 74
+// (64x64 outputs a wave read twice as much LDS for a product as 128x64: small tiles
+// are bound by that, at 0.35 us a K-tile.)  The backward products take the same or
+// up to a fifth more: turned fragments are twice as many reads.  A K-tile of codes
+// takes the same time as one of 16-bit elements.
 struct Cost {
     int places;            // work-groups that run at once
     double fixed, step, alone, part;
 };
-constexpr Cost kLargeCost = {256, 8.0, 1.48, 1.06, 0.11};
-constexpr Cost kSmallCost = {512, 6.0, 0.95, 0.53, 0.03};
+constexpr Cost kLargeCost = {256, 8.0, 1.48, 1.06, 0.08};
+constexpr Cost kSmallCost = {512, 6.5, 0.95, 0.55, 0.015};
+constexpr Cost kDeepCost = {256, 8.0, 0.50, 0.45, 0.015};
 constexpr double kJoinUs = 5.0;
 
 inline double groups_us(const Cost &c, int64_t groups, int64_t steps) {
@@ -682,12 +709,15 @@ Choice choice_for(Kind kind, const Product &p, int size, const Cost &c, double *
     const int64_t tm = up(p.m, S::BM) * (kind == Kind::kWeight ? 2 : 1);
     const int64_t tn = up(p.n, kind == Kind::kForward ? S::HN : S::BN), tiles = tm * tn;
     const int64_t left = tiles % c.places;
-    double best = groups_us(c, tiles, depth);
+    auto rounds_us = [&](int64_t groups, int64_t steps) {
+        return groups_us(c, groups, up(steps, S::RING) * S::RING);
+    };
+    double best = rounds_us(tiles, depth);
     r.plan = {(int32_t)tm, (int32_t)tn, (int32_t)tiles, 1, (int32_t)depth, (int32_t)depth, (int32_t)tiles};
     for (int64_t split : {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
         if (left == 0 || split * 4 > depth) break;
         const int64_t share = up(depth, split), parts = up(depth, share);
-        const double t = groups_us(c, tiles - left, depth) + groups_us(c, left * parts, share) +
+        const double t = rounds_us(tiles - left, depth) + rounds_us(left * parts, share) +
                          (double)(left * parts) * c.part + kJoinUs;
         if (t >= best) continue;
         best = t;
@@ -698,15 +728,17 @@ Choice choice_for(Kind kind, const Product &p, int size, const Cost &c, double *
         r.split_tiles = left;
         r.slab_floats = left * parts * S::SLAB;
     }
-    r.large = S::BM == 256;
+    r.size = S::BM == 256 ? Size::kLarge : S::RING == 2 ? Size::kSmall : Size::kDeep;
     *us = best;
     return r;
 }
 
 inline Choice choose(Kind kind, const Product &p, int size) {
-    double large_us, small_us;
+    double large_us, small_us, deep_us;
     const Choice large = choice_for<Large>(kind, p, size, kLargeCost, &large_us);
     const Choice small = choice_for<Small>(kind, p, size, kSmallCost, &small_us);
+    const Choice deep = choice_for<Deep>(kind, p, size, kDeepCost, &deep_us);
+    if (deep_us <= small_us && deep_us <= large_us) return deep;
     return large_us <= small_us ? large : small;
 }
 
@@ -723,8 +755,11 @@ taco_status launch_product(const Product &p, const Choice &c, hipStream_t stream
 template <typename E, Kind K>
 taco_status run_kind(const Product &p, hipStream_t stream) {
     const Choice c = choose(K, p, Element<E>::SIZE);
-    return c.large ? launch_product<E, K, Large>(p, c, stream)
-                   : launch_product<E, K, Small>(p, c, stream);
+    switch (c.size) {
+        case Size::kLarge: return launch_product<E, K, Large>(p, c, stream);
+        case Size::kSmall: return launch_product<E, K, Small>(p, c, stream);
+        default: return launch_product<E, K, Deep>(p, c, stream);
+    }
 }
 
 }  // namespace
