@@ -114,10 +114,10 @@ taco_status with_type(taco_norm_dtype dtype, F &&f) {
 }
 
 // (A plan depends on the sizes only, not on which 16-bit type it is.)
-int64_t slabs(Kind kind, int64_t m, int64_t n, int64_t k) {
+Product sizes(int64_t m, int64_t n, int64_t k) {
     Product p = {};
     p.m = m; p.n = n; p.k = k;
-    return Products<BF16>::workspace(kind, p);
+    return p;
 }
 
 struct ForwardOperands {
@@ -131,7 +131,7 @@ ForwardOperands forward_operands(const void *x, int64_t ldx, const void *gate, i
                          operand(up, ldu, features, hidden), 0, 0};
     if (rows <= kFewRows) return o;
     alike(&o.gate, &o.up);
-    o.slab_bytes = slabs(Kind::kForward, rows, features, hidden);
+    o.slab_bytes = Products<BF16>::workspace(Kind::kForward, sizes(rows, features, hidden));
     o.bytes = o.slab_bytes + o.x.copy_bytes() + o.gate.copy_bytes() + o.up.copy_bytes();
     return o;
 }
@@ -147,16 +147,12 @@ BackwardOperands backward_operands(const void *x, int64_t ldx, const void *gate,
                           operand(up, ldu, features, hidden), 0, 0, 0};
     alike(&o.gate, &o.up);
     o.d_pitch = round_up(features, 8);
-    if (want_dx) {
-        o.slab_bytes = slabs(Kind::kInput, rows, hidden, features);
-        o.bytes += o.gate.copy_bytes() + o.up.copy_bytes();
-    }
-    if (want_dw) {
-        // The two products follow one another and share their partial sums' place.
-        const int64_t more = slabs(Kind::kWeight, features, hidden, rows);
-        o.slab_bytes = more > o.slab_bytes ? more : o.slab_bytes;
-        o.bytes += o.x.copy_bytes();
-    }
+    const Product input = sizes(rows, hidden, features), weight = sizes(features, hidden, rows);
+    if (want_dx) o.bytes += o.gate.copy_bytes() + o.up.copy_bytes();
+    if (want_dw) o.bytes += o.x.copy_bytes();
+    o.slab_bytes = want_dx && want_dw ? Products<BF16>::pair_workspace(input, weight)
+                   : want_dx          ? Products<BF16>::workspace(Kind::kInput, input)
+                                      : Products<BF16>::workspace(Kind::kWeight, weight);
     o.bytes += o.slab_bytes + 2 * rows * o.d_pitch * kSize;
     return o;
 }
@@ -207,8 +203,7 @@ taco_status taco_gated_forward(const void *x, int64_t ldx, const void *gate_weig
                         rows_span(up_weight, features, hidden, ldu)};
     if (any_overlap(outs, ins)) return TACO_ERR_ALIAS;
     if (workspace_bytes < o.bytes) return TACO_ERR_PARAM;
-    Product p = {};
-    p.m = rows; p.n = features; p.k = hidden;
+    Product p = sizes(rows, features, hidden);
     p.activation = activation;
     p.out[0] = a; p.out[1] = gate; p.out[2] = up;
     p.out_pitch[0] = lda; p.out_pitch[1] = p.out_pitch[2] = ldgu;
@@ -290,38 +285,33 @@ taco_status taco_gated_backward(const void *da, int64_t ldda, const void *x, int
     const Matrix mx = want_dw ? arena.place(o.x) : Matrix{};
     const Matrix mg = want_dx ? arena.place(o.gate) : Matrix{};
     const Matrix mu = want_dx ? arena.place(o.up) : Matrix{};
-    taco_status st = arena.copy(stream);
-    if (st != TACO_OK) return st;
     ActivationGrad act = {};
     act.da = da; act.gate = gate; act.up = up; act.dgate = dgate; act.dup = dup;
     act.ldda = ldda; act.ldgu = ldgu; act.to_pitch = o.d_pitch; act.rows = rows;
     act.features = (int32_t)features; act.activation = activation;
-    st = activation_grad(act, dtype == TACO_NORM_F16, stream);
+    const taco_status st =
+        activation_grad(act, dtype == TACO_NORM_F16, arena.copies, arena.count, stream);
     if (st != TACO_OK) return st;
-    Product p = {};
-    p.a[0] = {dgate, o.d_pitch * kSize};
-    p.a[1] = {dup, o.d_pitch * kSize};
-    p.slabs = slab;
-    if (want_dx) {
-        p.b[0] = mg; p.b[1] = mu;
-        p.out[0] = dx; p.out_pitch[0] = lddx;
-        p.m = rows; p.n = hidden; p.k = features;
-        st = with_type(dtype, [&](auto k) { return decltype(k)::run(Kind::kInput, p, stream); });
-        if (st != TACO_OK) return st;
-    }
-    if (!want_dw) return TACO_OK;
-    p.b[0] = p.b[1] = mx;
-    p.out[0] = dgate_weight; p.out[1] = dup_weight;
-    p.out_pitch[0] = p.out_pitch[1] = hidden;
-    p.m = features; p.n = hidden; p.k = rows;
-    return with_type(dtype, [&](auto k) { return decltype(k)::run(Kind::kWeight, p, stream); });
+    Product input = sizes(rows, hidden, features), weight = sizes(features, hidden, rows);
+    input.a[0] = weight.a[0] = {dgate, o.d_pitch * kSize};
+    input.a[1] = weight.a[1] = {dup, o.d_pitch * kSize};
+    input.slabs = weight.slabs = slab;
+    input.b[0] = mg; input.b[1] = mu;
+    input.out[0] = dx; input.out_pitch[0] = lddx;
+    weight.b[0] = weight.b[1] = mx;
+    weight.out[0] = dgate_weight; weight.out[1] = dup_weight;
+    weight.out_pitch[0] = weight.out_pitch[1] = hidden;
+    return with_type(dtype, [&](auto k) {
+        using P = decltype(k);
+        if (want_dx && want_dw) return P::run_pair(input, weight, stream);
+        return want_dx ? P::run(Kind::kInput, input, stream) : P::run(Kind::kWeight, weight, stream);
+    });
 }
 
 int64_t taco_gated_forward_mx_workspace(int64_t rows, int64_t hidden, int64_t features) {
     if (!valid_mx(rows, hidden, features)) return -1;
     if (rows <= kFewRows) return 0;
-    Product p = {};
-    p.m = rows; p.n = features; p.k = hidden;
+    Product p = sizes(rows, features, hidden);
     return Products<Codes>::workspace(Kind::kForward, p) + scale_tile_bytes(rows, hidden / 32) +
            2 * scale_tile_bytes(features, hidden / 32);
 }
@@ -350,8 +340,7 @@ taco_status taco_gated_forward_mx(const uint8_t *x_codes, const uint8_t *x_scale
                         {up_codes, features * hidden}, {up_scales, features * blocks}};
     if (any_overlap(outs, ins)) return TACO_ERR_ALIAS;
     if (workspace_bytes < need) return TACO_ERR_PARAM;
-    Product p = {};
-    p.m = rows; p.n = features; p.k = hidden;
+    Product p = sizes(rows, features, hidden);
     p.activation = activation;
     p.out_f16 = dtype == TACO_NORM_F16;
     p.out[0] = a; p.out_pitch[0] = lda;

@@ -50,6 +50,9 @@ struct Product {
 template <typename E> struct Products {
     static int64_t workspace(Kind kind, const Product &p);
     static taco_status run(Kind kind, const Product &p, hipStream_t stream);
+    // kInput and kWeight of one backward pass; slabs are input's.
+    static int64_t pair_workspace(const Product &input, const Product &weight);
+    static taco_status run_pair(const Product &input, Product weight, hipStream_t stream);
     // kForward of at most kFewRows rows; operands at any 2-byte (codes:
     // 16-byte) boundary.
     static taco_status few(const Product &p, hipStream_t stream);
@@ -69,8 +72,6 @@ struct ActivationGrad {
     int64_t ldda, ldgu, to_pitch, rows;
     int32_t features, activation;
 };
-taco_status activation_grad(const ActivationGrad &a, bool f16, hipStream_t stream);
-
 // Rows of `width` bytes to rows `to_pitch` bytes apart (a multiple of 16) on
 // 16-byte boundaries, with zeros behind them.
 struct Repack {
@@ -80,6 +81,9 @@ struct Repack {
     int64_t width;
 };
 taco_status repack(const Repack *r, int count, hipStream_t stream);      // count <= 3
+// (with the copies in the same launch)
+taco_status activation_grad(const ActivationGrad &a, bool f16, const Repack *r, int count,
+                            hipStream_t stream);
 
 // Feature of LDS row R of a forward B half: of each 32 features, column fragment
 // j takes 8 q + 4 j + (0..3), so that a lane's two fragments are eight

@@ -234,31 +234,37 @@ struct Finish {
     }
 };
 
+// A work-group's LDS.  Several variables, not one for all: the compiler then knows
+// that a load into one does not touch the fragments being read from another, and
+// does not wait for it.  It tells few of them apart, so what is never loaded and
+// read at the same time shares one: the halves of B and the scales, and in a ring
+// of four K-tiles (whose loads into a variable follow the reads from it) all of a
+// K-tile.
+template <typename E, typename S>
+struct Lds {
+    static constexpr bool APART = S::RING == 2;                // halves of A have their own
+    static constexpr int SCALES = Element<E>::SCALED ? S::THREADS * 4 : 0;     // [A0 | A1 | B0 | B1]
+    static constexpr int B_AT = APART ? 0 : 2 * S::A_HALF, S_AT = B_AT + 2 * S::B_HALF;
+    static constexpr int HALF = APART ? S::A_HALF : 1, REST = S_AT + SCALES;
+    static constexpr int MORE = APART ? 1 : REST;
+    uint8_t *a[4], *rest[4];
+};
+
+// The items first, first + stride, ... of a product.
 template <typename E, Kind K, typename S>
-__global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan plan) {
+__device__ __forceinline__ void multiply_items(const Product &p, const Plan &plan, int first, int stride,
+                                               const Lds<E, S> &mem) {
     using El = Element<E>;
     constexpr int HM = S::HM, HN = S::HN, MF = S::MF, NF = S::NF, THREADS = S::THREADS;
     constexpr int SIZE = El::SIZE, KT = kDeep / SIZE;          // summed elements of a K-tile
     constexpr bool A_TURNED = K == Kind::kWeight, B_TURNED = K != Kind::kForward;
-    constexpr bool SCALED = El::SCALED;
-    // Several variables, not one for all: the compiler then knows that a load
-    // into one does not touch the fragments being read from another, and does
-    // not wait for it.  It tells few of them apart, so what is never loaded and
-    // read at the same time shares one: the halves of B and the scales.
-    constexpr int SCALES = SCALED ? THREADS * 4 : 0;           // [A0 | A1 | B0 | B1], bytes
-    constexpr bool APART = S::RING == 2;                       // halves of A have their own
-    constexpr int B_AT = APART ? 0 : 2 * S::A_HALF, S_AT = B_AT + 2 * S::B_HALF;
-    constexpr int HALF = APART ? S::A_HALF : 1, REST = S_AT + SCALES;
-    __shared__ __align__(1024) uint8_t a00[HALF], a01[HALF], a10[HALF], a11[HALF], b0[REST], b1[REST],
-        b2[APART ? 1 : REST], b3[APART ? 1 : REST];
-    auto lds = [&](auto stage) -> uint8_t * {
-        constexpr int s = decltype(stage)::value % S::RING;
-        return s == 0 ? b0 : s == 1 ? b1 : s == 2 ? b2 : b3;
-    };
+    constexpr bool SCALED = El::SCALED, APART = Lds<E, S>::APART;
+    constexpr int B_AT = Lds<E, S>::B_AT, S_AT = Lds<E, S>::S_AT;
+    auto lds = [&](auto stage) -> uint8_t * { return mem.rest[decltype(stage)::value % S::RING]; };
     auto lds_a = [&](auto stage, auto half) -> uint8_t * {
         constexpr int s = decltype(stage)::value % S::RING, h = decltype(half)::value;
         if constexpr (!APART) return lds(stage) + h * S::A_HALF;
-        else return s == 0 ? (h == 0 ? a00 : a01) : (h == 0 ? a10 : a11);
+        else return mem.a[2 * s + h];
     };
     auto lds_b = [&](auto stage, auto half) -> uint8_t * {
         return lds(stage) + B_AT + decltype(half)::value * S::B_HALF;
@@ -368,7 +374,7 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
         }
         return it;
     };
-    int j = blockIdx.x;
+    int j = first;
     Item cur = item_at(j), next = cur;
 
     // Loads.  K-tile kt counts from the current item's first; those past its last
@@ -594,7 +600,7 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
     for (;;) {
         if constexpr (S::WALKS) {
             // (after the last item there is none: nothing exists of its K-tiles)
-            j += gridDim.x;
+            j += stride;
             next = j < plan.items ? item_at(j) : cur;
             if (j >= plan.items) next.count = 0;
         }
@@ -643,20 +649,54 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
-// Adds the parts of a split tile in order and finishes it: blockIdx.x is the
-// tile after the whole ones, blockIdx.y its row fragment.
 template <typename E, Kind K, typename S>
-__global__ __launch_bounds__(S::THREADS) void join_kernel(Product p, Plan plan) {
+__global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan plan) {
+    using M = Lds<E, S>;
+    __shared__ __align__(1024) uint8_t a00[M::HALF], a01[M::HALF], a10[M::HALF], a11[M::HALF],
+        b0[M::REST], b1[M::REST], b2[M::MORE], b3[M::MORE];
+    multiply_items<E, K, S>(p, plan, blockIdx.x, gridDim.x, M{{a00, a01, a10, a11}, {b0, b1, b2, b3}});
+}
+
+// Both products of a small backward pass in one launch: neither fills the GPU.
+template <typename E, typename S>
+__global__ __launch_bounds__(S::THREADS) void both_kernel(Product input, Plan input_plan, Product weight,
+                                                          Plan weight_plan) {
+    using M = Lds<E, S>;
+    __shared__ __align__(1024) uint8_t a00[M::HALF], a01[M::HALF], a10[M::HALF], a11[M::HALF],
+        b0[M::REST], b1[M::REST], b2[M::MORE], b3[M::MORE];
+    const M mem = {{a00, a01, a10, a11}, {b0, b1, b2, b3}};
+    static_assert(!S::WALKS, "an item a work-group");
+    const int j = (int)blockIdx.x;
+    if (j < input_plan.items)
+        multiply_items<E, Kind::kInput, S>(input, input_plan, j, 0, mem);
+    else
+        multiply_items<E, Kind::kWeight, S>(weight, weight_plan, j - input_plan.items, 0, mem);
+}
+
+// Adds the parts of split tile `split` in order and finishes row fragment `part` of it.
+template <typename E, Kind K, typename S>
+__device__ __forceinline__ void join_parts(const Product &p, const Plan &plan, int split, int part) {
     const Place<S> place(threadIdx.x);
-    const Tile tile = tile_at(plan, plan.whole + blockIdx.x);
-    const float *at = p.slabs + (int64_t)blockIdx.x * plan.parts * S::SLAB +
-                      ((int64_t)blockIdx.y * 4 * S::THREADS + threadIdx.x) * 4;
+    const Tile tile = tile_at(plan, plan.whole + split);
+    const float *at = p.slabs + (int64_t)split * plan.parts * S::SLAB +
+                      ((int64_t)part * 4 * S::THREADS + threadIdx.x) * 4;
     f4v v[2][2] = {};
     for (int q = 0; q < plan.parts; ++q, at += S::SLAB)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             v[e >> 1][e & 1] += *reinterpret_cast<const f4v *>(at + (int64_t)e * S::THREADS * 4);
-    Finish<E, K, S>{p, place, tile}(blockIdx.y / S::MF, blockIdx.y % S::MF, v);
+    Finish<E, K, S>{p, place, tile}(part / S::MF, part % S::MF, v);
+}
+template <typename E, Kind K, typename S>
+__global__ __launch_bounds__(S::THREADS) void join_kernel(Product p, Plan plan) {
+    join_parts<E, K, S>(p, plan, blockIdx.x, blockIdx.y);
+}
+template <typename E, typename S>
+__global__ __launch_bounds__(S::THREADS) void join_both_kernel(Product input, Plan input_plan, int splits,
+                                                               Product weight, Plan weight_plan) {
+    const int j = (int)blockIdx.x;
+    if (j < splits) join_parts<E, Kind::kInput, S>(input, input_plan, j, blockIdx.y);
+    else join_parts<E, Kind::kWeight, S>(weight, weight_plan, j - splits, blockIdx.y);
 }
 
 // ---------------------------------------------------------------- host ----
@@ -762,6 +802,26 @@ taco_status run_kind(const Product &p, hipStream_t stream) {
     }
 }
 
+// A backward pass that wants both products.  Where neither takes large tiles they are
+// one launch of small ones, each with half of the places (999 x 1030x1111: 24 us,
+// one after the other 14 and 18, and one join).
+struct Pair {
+    bool together;
+    Choice input, weight;
+};
+inline Pair pair_of(const Product &input, const Product &weight, int size) {
+    Pair r = {};
+    r.together = choose(Kind::kInput, input, size).size != Size::kLarge &&
+                 choose(Kind::kWeight, weight, size).size != Size::kLarge;
+    if (!r.together) return r;
+    Cost half = kSmallCost;
+    half.places /= 2;
+    double us;
+    r.input = choice_for<Small>(Kind::kInput, input, size, half, &us);
+    r.weight = choice_for<Small>(Kind::kWeight, weight, size, half, &us);
+    return r;
+}
+
 }  // namespace
 
 template <typename E>
@@ -779,6 +839,38 @@ taco_status Products<E>::run(Kind kind, const Product &p, hipStream_t stream) {
             case Kind::kInput: return run_kind<E, Kind::kInput>(p, stream);
             default: return run_kind<E, Kind::kWeight>(p, stream);
         }
+    }
+}
+
+template <typename E>
+int64_t Products<E>::pair_workspace(const Product &input, const Product &weight) {
+    const Pair c = pair_of(input, weight, Element<E>::SIZE);
+    if (c.together) return (c.input.slab_floats + c.weight.slab_floats) * (int64_t)sizeof(float);
+    // One after the other, in the same place.
+    const int64_t i = workspace(Kind::kInput, input), w = workspace(Kind::kWeight, weight);
+    return i > w ? i : w;
+}
+
+template <typename E>
+taco_status Products<E>::run_pair(const Product &input, Product weight, hipStream_t stream) {
+    if constexpr (Element<E>::SCALED) {
+        return TACO_ERR_FORMAT;            // codes have no backward pass
+    } else {
+        const Pair c = pair_of(input, weight, Element<E>::SIZE);
+        if (!c.together) {
+            const taco_status st = run(Kind::kInput, input, stream);
+            return st != TACO_OK ? st : run(Kind::kWeight, weight, stream);
+        }
+        weight.slabs += c.input.slab_floats;
+        const taco_status st =
+            launch(reinterpret_cast<const void *>(&both_kernel<E, Small>),
+                   dim3((unsigned)(c.input.plan.items + c.weight.plan.items)), Small::THREADS, stream,
+                   input, c.input.plan, weight, c.weight.plan);
+        const int64_t splits = c.input.split_tiles + c.weight.split_tiles;
+        if (st != TACO_OK || splits == 0) return st;
+        return launch(reinterpret_cast<const void *>(&join_both_kernel<E, Small>),
+                      dim3((unsigned)splits, 2 * Small::MF), Small::THREADS, stream, input,
+                      c.input.plan, (int)c.input.split_tiles, weight, c.weight.plan);
     }
 }
 

@@ -34,19 +34,26 @@ __device__ __forceinline__ void load8(const T *p, const T *row, int n, float *f)
                f);
 }
 
-// A thread to eight neighbours; 2^lanes_log2 threads to a row.
+// Work-groups of a kernel that share rows: this one is `at` of `of` along the rows,
+// and `col` of `cols` along the columns; 2^lanes_log2 threads to a row.
+struct Part {
+    int64_t at, of;
+    int col, cols, lanes_log2;
+};
+
+// A thread to eight neighbours.
 template <typename T, int ACT>
-__global__ __launch_bounds__(256) void activation_grad_kernel(ActivationGrad a, int lanes_log2) {
-    const int lanes = 1 << lanes_log2, lane = threadIdx.x & (lanes - 1), per = 256 >> lanes_log2;
+__device__ __forceinline__ void activation_grad_rows(const ActivationGrad &a, const Part &part) {
+    const int lanes = 1 << part.lanes_log2, lane = threadIdx.x & (lanes - 1), per = 256 >> part.lanes_log2;
     const int chunks = (int)(a.to_pitch / 8);
-    for (int64_t row = (int64_t)blockIdx.x * per + (threadIdx.x >> lanes_log2); row < a.rows;
-         row += (int64_t)gridDim.x * per) {
+    for (int64_t row = part.at * per + (threadIdx.x >> part.lanes_log2); row < a.rows;
+         row += part.of * per) {
         const T *const da = static_cast<const T *>(a.da) + row * a.ldda;
         const T *const gate = static_cast<const T *>(a.gate) + row * a.ldgu;
         const T *const up = static_cast<const T *>(a.up) + row * a.ldgu;
         T *const dgate = static_cast<T *>(a.dgate) + row * a.to_pitch;
         T *const dup = static_cast<T *>(a.dup) + row * a.to_pitch;
-        for (int c = blockIdx.y * lanes + lane; c < chunks; c += gridDim.y * lanes) {
+        for (int c = part.col * lanes + lane; c < chunks; c += part.cols * lanes) {
             const int n = a.features - 8 * c;
             float d[8], g[8], u[8], dg[8], du[8];
             load8<T>(da + 8 * c, da, n, d);
@@ -65,16 +72,10 @@ __global__ __launch_bounds__(256) void activation_grad_kernel(ActivationGrad a, 
     }
 }
 
-struct Copies {
-    Repack r[3];
-    int32_t lanes_log2[3];
-};
-__global__ __launch_bounds__(256) void repack_kernel(Copies all) {
-    const Repack r = all.r[blockIdx.y];
-    const int log2 = all.lanes_log2[blockIdx.y], lanes = 1 << log2, lane = threadIdx.x & (lanes - 1);
-    const int per = 256 >> log2;
-    for (int64_t row = (int64_t)blockIdx.x * per + (threadIdx.x >> log2); row < r.rows;
-         row += (int64_t)gridDim.x * per) {
+__device__ __forceinline__ void repack_rows(const Repack &r, const Part &part) {
+    const int lanes = 1 << part.lanes_log2, lane = threadIdx.x & (lanes - 1), per = 256 >> part.lanes_log2;
+    for (int64_t row = part.at * per + (threadIdx.x >> part.lanes_log2); row < r.rows;
+         row += part.of * per) {
         const char *from = static_cast<const char *>(r.from) + row * r.from_pitch;
         char *to = static_cast<char *>(r.to) + row * r.to_pitch;
         for (int64_t at = lane * 16; at < r.to_pitch; at += lanes * 16) {
@@ -82,6 +83,38 @@ __global__ __launch_bounds__(256) void repack_kernel(Copies all) {
             *reinterpret_cast<u4v *>(to + at) =
                 n > 0 ? load_tail<true>(from + at, from, n < 16 ? (int)n : 16) : (u4v){0u, 0u, 0u, 0u};
         }
+    }
+}
+
+struct Copies {
+    Repack r[3];
+    int32_t lanes_log2[3], groups[3];
+};
+// Work-group b of those that all copies take, one after the other.
+__device__ __forceinline__ Part part_of_copies(const Copies &all, int b, int *which) {
+    const int second = all.groups[0], third = second + all.groups[1];
+    *which = (b >= second) + (b >= third);
+    return {b - (b >= third ? third : b >= second ? second : 0), all.groups[*which], 0, 1,
+            all.lanes_log2[*which]};
+}
+__global__ __launch_bounds__(256) void repack_kernel(Copies all) {
+    int which;
+    const Part part = part_of_copies(all, blockIdx.x, &which);
+    repack_rows(all.r[which], part);
+}
+
+// The gradients of the activations, and the copies that the products after them need,
+// in one launch.
+template <typename T, int ACT>
+__global__ __launch_bounds__(256) void activation_grad_kernel(ActivationGrad a, int groups, int cols,
+                                                              int lanes_log2, Copies copies) {
+    const int b = (int)blockIdx.x;
+    if (b < groups * cols) {
+        activation_grad_rows<T, ACT>(a, {b % groups, groups, b / groups, cols, lanes_log2});
+    } else {
+        int which;
+        const Part part = part_of_copies(copies, b - groups * cols, &which);
+        repack_rows(copies.r[which], part);
     }
 }
 
@@ -161,12 +194,33 @@ unsigned groups_of(int64_t n, int64_t most) { return (unsigned)(n < most ? n : m
 
 }  // namespace
 
-taco_status activation_grad(const ActivationGrad &a, bool f16, hipStream_t stream) {
+namespace {
+Copies copies_of(const Repack *r, int count, int64_t *groups) {
+    Copies all = {};
+    *groups = 0;
+    for (int i = 0; i < count; ++i) {
+        all.r[i] = r[i];
+        int log2 = 0;
+        while (log2 < 8 && (INT64_C(16) << log2) < r[i].to_pitch) ++log2;
+        all.lanes_log2[i] = log2;
+        const int64_t per = 256 >> log2;
+        all.groups[i] = (int32_t)groups_of((r[i].rows + per - 1) / per, 2048);
+        *groups += all.groups[i];
+    }
+    return all;
+}
+}  // namespace
+
+taco_status activation_grad(const ActivationGrad &a, bool f16, const Repack *r, int count,
+                            hipStream_t stream) {
     const int64_t chunks = a.to_pitch / 8;
     int log2 = 0;
     while (log2 < 8 && (INT64_C(1) << log2) < chunks) ++log2;
-    const int64_t per = 256 >> log2, across = (chunks + 255) / 256;
-    const dim3 grid(groups_of((a.rows + per - 1) / per, 8192), groups_of(across, 64));
+    const int64_t per = 256 >> log2;
+    const int groups = (int)groups_of((a.rows + per - 1) / per, 8192);
+    const int cols = (int)groups_of((chunks + 255) / 256, 64);
+    int64_t more;
+    const Copies copies = copies_of(r, count, &more);
     const void *fn = nullptr;
     switch (a.activation) {
         case TACO_GATED_SILU:
@@ -181,22 +235,14 @@ taco_status activation_grad(const ActivationGrad &a, bool f16, hipStream_t strea
             fn = f16 ? reinterpret_cast<const void *>(&activation_grad_kernel<_Float16, TACO_GATED_GELU_TANH>)
                      : reinterpret_cast<const void *>(&activation_grad_kernel<__bf16, TACO_GATED_GELU_TANH>);
     }
-    return launch(fn, grid, 256, stream, a, log2);
+    return launch(fn, dim3((unsigned)((int64_t)groups * cols + more)), 256, stream, a, groups, cols, log2,
+                  copies);
 }
 
 taco_status repack(const Repack *r, int count, hipStream_t stream) {
-    Copies all = {};
-    int64_t groups = 1;
-    for (int i = 0; i < count; ++i) {
-        all.r[i] = r[i];
-        int log2 = 0;
-        while (log2 < 8 && (INT64_C(16) << log2) < r[i].to_pitch) ++log2;
-        all.lanes_log2[i] = log2;
-        const int64_t per = 256 >> log2, g = (r[i].rows + per - 1) / per;
-        groups = g > groups ? g : groups;
-    }
-    return launch(reinterpret_cast<const void *>(&repack_kernel),
-                  dim3(groups_of(groups, 2048), (unsigned)count), 256, stream, all);
+    int64_t groups;
+    const Copies all = copies_of(r, count, &groups);
+    return launch(reinterpret_cast<const void *>(&repack_kernel), dim3((unsigned)groups), 256, stream, all);
 }
 
 taco_status tile_scales(const ScaleTiles *s, int count, hipStream_t stream) {
