@@ -117,12 +117,6 @@ struct Shape {
     static_assert(HM == HN, "halves alike: one load count for all");
     static constexpr int LOADS = A_HALF / 16 / THREADS;                // a thread's loads of it
     static_assert(LOADS == 2 && NF == 2, "loads and pairs of column fragments");
-    // Whether a work-group takes several items, one after the other: the loads of
-    // the next begin before the current one's outputs are formed (8192 x 10240x2560
-    // with G and U written 668 us instead of 690).  A small tile's work-groups are
-    // two to a CU, and few; the bookkeeping only costs them (999 x 1030x1111
-    // backward 57 us instead of 51).
-    static constexpr bool WALKS = BM == 256;
     // Register sets for the halves of A: large tiles have none to spare, the others
     // read a half in one go (1 to 2 % less time).
     static constexpr int SETS = BM == 256 ? 1 : 2;
@@ -134,9 +128,12 @@ using Small = Shape<128, 128, 2, 2, 2>;
 // One to a CU, for few tiles: its loads are asked for three K-tiles ahead.
 using Deep = Shape<128, 128, 2, 2, 4>;
 
-// The items of work: the first `whole` are a tile each; the remaining tiles are cut
-// into `parts` parts of `share` K-tiles.  Work-group b of a grid of g takes items b,
-// b + g, b + 2 g, ... (Shape::WALKS; else there is one for each item).
+// The items of work, one to a work-group: the first `whole` are a tile each; the
+// remaining tiles are cut into `parts` parts of `share` K-tiles.  (Work-groups that
+// stay and walk over items, the next one's loads going out before the current
+// one's outputs are formed, took as long forward and 5 % longer backward, 8192 x
+// 10240x2560 1577 instead of 1507 us: items handed out one by one even out what CUs
+// take.)
 struct Plan {
     int32_t tiles_m, tiles_n;
     int32_t whole, parts, share;
@@ -250,10 +247,10 @@ struct Lds {
     uint8_t *a[4], *rest[4];
 };
 
-// The items first, first + stride, ... of a product.
+// Item j of a product.
 template <typename E, Kind K, typename S>
-__device__ __forceinline__ void multiply_items(const Product &p, const Plan &plan, int first, int stride,
-                                               const Lds<E, S> &mem) {
+__device__ __forceinline__ void multiply_item(const Product &p, const Plan &plan, int j,
+                                              const Lds<E, S> &mem) {
     using El = Element<E>;
     constexpr int HM = S::HM, HN = S::HN, MF = S::MF, NF = S::NF, THREADS = S::THREADS;
     constexpr int SIZE = El::SIZE, KT = kDeep / SIZE;          // summed elements of a K-tile
@@ -323,66 +320,53 @@ __device__ __forceinline__ void multiply_items(const Product &p, const Plan &pla
         static_cast<const char *>(p.b[1].p) - static_cast<const char *>(p.b[0].p) -
         (K == Kind::kInput ? seg_depth * step_b : 0);
 
-    // An item: where its K-tiles kt0 .. kt0 + count - 1 begin in both operands, the
-    // rows (or columns) that exist in the halves, and for codes the scales of the
-    // quarter of them that this wave loads.
-    struct Item {
-        const char *a, *b, *scale;
-        int here_a[2], here_b[2], here_scale;
-        int kt0, count, end;               // end: count, rounded up to a whole ring
-        int part;                          // of a split tile, else -1
-        Tile tile;
-    };
-    [[maybe_unused]] const int quarter = __builtin_amdgcn_readfirstlane(tid / HM);
-    [[maybe_unused]] const Matrix &scales =
-        quarter >= 2 ? p.b_scale[quarter & 1] : p.a_scale;
-    auto item_at = [&](int j) {
-        Item it;
-        it.part = -1;
-        it.kt0 = 0;
-        it.count = plan.depth;
-        int t;
-        if (j < plan.whole) {
-            // Consecutive work-groups go to the 8 XCDs in turn; each XCD gets a
-            // contiguous range of the whole tiles, whose operands meet in its L2.
-            const int xcd = j % 8, q = plan.whole / 8, rem = plan.whole % 8;
-            t = xcd * q + (xcd < rem ? xcd : rem) + j / 8;
-        } else {
-            it.part = j - plan.whole;
-            const int in = it.part % plan.parts;
-            t = plan.whole + it.part / plan.parts;
-            it.kt0 = in * plan.share;
-            const int left = plan.depth - it.kt0;
-            it.count = left < plan.share ? left : plan.share;
-        }
-        it.end = (it.count + S::RING - 1) / S::RING * S::RING;
-        it.tile = tile_at(plan, t);
-        const int which = K == Kind::kWeight && it.tile.m >= per_m;
-        const int64_t m0 = (int64_t)(it.tile.m - which * per_m) * S::BM;
-        const int64_t n0 = (int64_t)it.tile.n * (K == Kind::kForward ? HN : S::BN);
-        it.a = static_cast<const char *>(p.a[which].p) + m0 * (A_TURNED ? SIZE : pitch_a) + it.kt0 * step_a;
-        it.b = static_cast<const char *>(p.b[0].p) + n0 * (B_TURNED ? SIZE : pitch_b) + it.kt0 * step_b;
+    // The item: its K-tiles kt0 .. kt0 + count - 1, where they begin in both operands,
+    // the rows (or columns) that exist in the halves, and for codes the scales of
+    // the quarter of them that this wave loads.
+    int part = -1, kt0 = 0, count = plan.depth, t;             // part: of a split tile, else -1
+    if (j < plan.whole) {
+        // Consecutive work-groups go to the 8 XCDs in turn; each XCD gets a
+        // contiguous range of the whole tiles, whose operands meet in its L2.
+        const int xcd = j % 8, q = plan.whole / 8, rem = plan.whole % 8;
+        t = xcd * q + (xcd < rem ? xcd : rem) + j / 8;
+    } else {
+        part = j - plan.whole;
+        const int in = part % plan.parts;
+        t = plan.whole + part / plan.parts;
+        kt0 = in * plan.share;
+        const int left = plan.depth - kt0;
+        count = left < plan.share ? left : plan.share;
+    }
+    const Tile tile = tile_at(plan, t);
+    const int which = K == Kind::kWeight && tile.m >= per_m;
+    const int64_t m0 = (int64_t)(tile.m - which * per_m) * S::BM;
+    const int64_t n0 = (int64_t)tile.n * (K == Kind::kForward ? HN : S::BN);
+    const char *const item_a =
+        static_cast<const char *>(p.a[which].p) + m0 * (A_TURNED ? SIZE : pitch_a) + kt0 * step_a;
+    const char *const item_b =
+        static_cast<const char *>(p.b[0].p) + n0 * (B_TURNED ? SIZE : pitch_b) + kt0 * step_b;
+    int here_a[2], here_b[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            it.here_a[h] = clamp(p.m - m0 - h * HM, HM);
-            it.here_b[h] = clamp(p.n - n0 - (K == Kind::kForward ? 0 : h * HN), HN);
-        }
-        if constexpr (SCALED) {
-            const int64_t first = quarter >= 2 ? n0 : m0 + quarter * HM;
-            it.scale = static_cast<const char *>(scales.p) + first * 4 + it.kt0 * scales.pitch;
-            it.here_scale = clamp(scales.pitch / 4 - first, HM) * 4;
-        }
-        return it;
-    };
-    int j = first;
-    Item cur = item_at(j), next = cur;
+    for (int h = 0; h < 2; ++h) {
+        here_a[h] = clamp(p.m - m0 - h * HM, HM);
+        here_b[h] = clamp(p.n - n0 - (K == Kind::kForward ? 0 : h * HN), HN);
+    }
+    [[maybe_unused]] const char *item_scale = nullptr;
+    [[maybe_unused]] int here_scale = 0;
+    [[maybe_unused]] int64_t scale_pitch = 0;
+    if constexpr (SCALED) {
+        const int quarter = __builtin_amdgcn_readfirstlane(tid / HM);
+        const Matrix &scales = quarter >= 2 ? p.b_scale[quarter & 1] : p.a_scale;
+        const int64_t first = quarter >= 2 ? n0 : m0 + quarter * HM;
+        scale_pitch = scales.pitch;
+        item_scale = static_cast<const char *>(scales.p) + first * 4 + kt0 * scale_pitch;
+        here_scale = clamp(scale_pitch / 4 - first, HM) * 4;
+    }
 
-    // Loads.  K-tile kt counts from the current item's first; those past its last
-    // (and past a whole ring of them) are the next item's, whose loads so begin
-    // before the current one's outputs are formed.  All of this is the same for
-    // every lane but the offset, which is out of bounds for chunks past a row's end,
-    // and all choices are selects: a branch here would part the products from what
-    // is to run beside them.
+    // Loads; K-tile kt counts from the item's first, and those past its last are zeros.
+    // All of this is the same for every lane but the offset, which is out of bounds
+    // for chunks past a row's end, and all choices are selects: a branch here would
+    // part the products from what is to run beside them.
     auto load = [&](uint8_t *buf, const char *base, int records, const uint32_t (&off)[2], bool in) {
 #if defined(__HIP_DEVICE_COMPILE__)      // the host pass does not know the resource type
         // 0x00020000: raw 32-bit data.
@@ -394,18 +378,16 @@ __device__ __forceinline__ void multiply_items(const Product &p, const Plan &pla
                 16, in ? off[i] : 0x80000000u, 0, 0, 0);
 #endif
     };
-    // A half of an item's operand at its K-tile `local`, `more` bytes from the
-    // first half.
+    // A half of an operand, `more` bytes from the first one.
     auto load_half = [&](auto turned, uint8_t *buf, const char *base, int64_t step, int64_t second,
-                         int64_t more, int here, int pitch, const uint32_t (&off)[2], int chunk,
-                         int local, int kt, bool exists) {
-        int in_seg = kt;
+                         int64_t more, int here, int pitch, const uint32_t (&off)[2], int chunk, int kt) {
+        int in_seg = kt0 + kt;
         if constexpr (K == Kind::kInput) {
-            const bool seg = kt >= seg_depth;
+            const bool seg = in_seg >= seg_depth;
             in_seg -= seg ? seg_depth : 0;
             more += seg ? second : 0;
         }
-        base += local * step + more;
+        base += kt * step + more;
         int records;
         bool in;
         if constexpr (decltype(turned)::value != 0) {
@@ -415,38 +397,27 @@ __device__ __forceinline__ void multiply_items(const Product &p, const Plan &pla
             records = here * pitch;
             in = chunk + in_seg * 8 < k_chunks;
         }
-        load(buf, base, exists ? records : 0, off, in);
+        load(buf, base, kt < count ? records : 0, off, in);
     };
     auto load_a = [&](auto stage, auto half, int kt) {
         constexpr int h = decltype(half)::value;
-        const bool on = S::WALKS && kt >= cur.end;
-        const int local = on ? kt - cur.end : kt;
-        load_half(Int<A_TURNED>{}, lds_a(stage, half), on ? next.a : cur.a, step_a, second_a,
-                  (int64_t)(h * HM) * (A_TURNED ? SIZE : pitch_a), on ? next.here_a[h] : cur.here_a[h],
-                  pitch_a, off_a, chunk_a, local, local + (on ? next.kt0 : cur.kt0),
-                  local < (on ? next.count : cur.count));
+        load_half(Int<A_TURNED>{}, lds_a(stage, half), item_a, step_a, second_a,
+                  (int64_t)(h * HM) * (A_TURNED ? SIZE : pitch_a), here_a[h], pitch_a, off_a, chunk_a, kt);
     };
     auto load_b = [&](auto stage, auto half, int kt) {
         constexpr int h = decltype(half)::value;
-        const bool on = S::WALKS && kt >= cur.end;
-        const int local = on ? kt - cur.end : kt;
         // (forward: the second half is the same rows of the other weight)
-        load_half(Int<B_TURNED>{}, lds_b(stage, half), on ? next.b : cur.b, step_b, second_b,
-                  h == 0 ? 0 : K == Kind::kForward ? second_b : (int64_t)HN * SIZE,
-                  on ? next.here_b[h] : cur.here_b[h], pitch_b, off_b, chunk_b, local,
-                  local + (on ? next.kt0 : cur.kt0), local < (on ? next.count : cur.count));
+        load_half(Int<B_TURNED>{}, lds_b(stage, half), item_b, step_b, second_b,
+                  h == 0 ? 0 : K == Kind::kForward ? second_b : (int64_t)HN * SIZE, here_b[h], pitch_b,
+                  off_b, chunk_b, kt);
     };
     // Scales of a K-tile: one 4-byte load a thread.
     [[maybe_unused]] const uint32_t scale_off = tid % HM * 4;
     auto load_scales = [&](auto stage, int kt) {
 #if defined(__HIP_DEVICE_COMPILE__)
         if constexpr (SCALED) {
-            const bool on = S::WALKS && kt >= cur.end;
-            const int local = on ? kt - cur.end : kt;
-            const int records = local < (on ? next.count : cur.count)
-                                    ? on ? next.here_scale : cur.here_scale : 0;
             const auto r = __builtin_amdgcn_make_buffer_rsrc(
-                (void *)((on ? next.scale : cur.scale) + local * scales.pitch), 0, records, 0x00020000);
+                (void *)(item_scale + kt * scale_pitch), 0, kt < count ? here_scale : 0, 0x00020000);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 r, (__attribute__((address_space(3))) void *)(lds_s(stage) + wave * kWave * 4), 4,
                 scale_off, 0, 0, 0);
@@ -521,6 +492,12 @@ __device__ __forceinline__ void multiply_items(const Product &p, const Plan &pla
             sb[h] = read_scales(stage, at_sb + h * HM * 4, Int<NF>{});
     };
     f4v sum[2][2][MF][NF];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+#pragma unroll
+            for (int e = 0; e < NF; ++e) sum[q >> 1][q & 1][i][e] = (f4v){0.0f, 0.0f, 0.0f, 0.0f};
     // Products of a row fragment with a half of B.
     auto multiply = [&](auto qa, auto qb, auto fi) {
         constexpr int a = decltype(qa)::value, b = decltype(qb)::value, i = decltype(fi)::value;
@@ -531,8 +508,8 @@ __device__ __forceinline__ void multiply_items(const Product &p, const Plan &pla
         });
     };
 
-    // K-tile t of an item lies in stage t % RING (items take whole rings of them: an
-    // exit in between would make the compiler wait for all loads at its target).
+    // K-tile t lies in stage t % RING.  (An item takes whole rings of them: an exit in
+    // between would make the compiler wait for all loads at its target.)
     // Loads are in the order A0, F, scales, S, A1 of each K-tile, so "the half has
     // arrived" is a count of those after it.
     using C0 = Int<0>;
@@ -597,56 +574,34 @@ __device__ __forceinline__ void multiply_items(const Product &p, const Plan &pla
         read_b(Next{}, G{});
         last_use(C1{}, F{}, Next{}, C0{});
     };
-    for (;;) {
-        if constexpr (S::WALKS) {
-            // (after the last item there is none: nothing exists of its K-tiles)
-            j += stride;
-            next = j < plan.items ? item_at(j) : cur;
-            if (j >= plan.items) next.count = 0;
-        }
+    for (int kt = 0; kt < count; kt += RING)
+        for_each<RING>([&](auto stage) { k_tile(stage, kt + decltype(stage)::value); });
+    // (loads of nothing may still be on their way to LDS)
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+    if (part >= 0) {
+        float *const slab = p.slabs + (int64_t)part * S::SLAB;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
             for (int i = 0; i < MF; ++i)
 #pragma unroll
-                for (int e = 0; e < NF; ++e)
-                    sum[q >> 1][q & 1][i][e] = (f4v){0.0f, 0.0f, 0.0f, 0.0f};
-        for (int kt = 0; kt < cur.end; kt += RING) {
-            k_tile(C0{}, kt);
-            k_tile(C1{}, kt + 1);
-            if constexpr (RING == 4) {
-                k_tile(Int<2>{}, kt + 2);
-                k_tile(Int<3>{}, kt + 3);
-            }
-        }
-        if (cur.part >= 0) {
-            float *const slab = p.slabs + (int64_t)cur.part * S::SLAB;
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int i = 0; i < MF; ++i)
-#pragma unroll
-                    for (int e = 0; e < NF; ++e) {
-                        const int at = ((q >> 1) * MF + i) * 4 + (q & 1) * 2 + e;
-                        *reinterpret_cast<f4v *>(slab + (int64_t)(at * THREADS + tid) * 4) =
-                            sum[q >> 1][q & 1][i][e];
-                    }
-        } else {
-            const Finish<E, K, S> finish{p, place, cur.tile};
-#pragma unroll
-            for (int qa = 0; qa < 2; ++qa)
-#pragma unroll
-                for (int i = 0; i < MF; ++i) {
-                    const f4v v[2][2] = {{sum[qa][0][i][0], sum[qa][0][i][1]},
-                                         {sum[qa][1][i][0], sum[qa][1][i][1]}};
-                    finish(qa, i, v);
+                for (int e = 0; e < NF; ++e) {
+                    const int at = ((q >> 1) * MF + i) * 4 + (q & 1) * 2 + e;
+                    *reinterpret_cast<f4v *>(slab + (int64_t)(at * THREADS + tid) * 4) =
+                        sum[q >> 1][q & 1][i][e];
                 }
-        }
-        if (!S::WALKS || j >= plan.items) break;
-        cur = next;
+        return;
     }
-    // (loads of nothing may still be on their way to LDS)
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const Finish<E, K, S> finish{p, place, tile};
+#pragma unroll
+    for (int qa = 0; qa < 2; ++qa)
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+            const f4v v[2][2] = {{sum[qa][0][i][0], sum[qa][0][i][1]},
+                                 {sum[qa][1][i][0], sum[qa][1][i][1]}};
+            finish(qa, i, v);
+        }
 }
 
 template <typename E, Kind K, typename S>
@@ -654,7 +609,7 @@ __global__ __launch_bounds__(S::THREADS) void product_kernel(Product p, Plan pla
     using M = Lds<E, S>;
     __shared__ __align__(1024) uint8_t a00[M::HALF], a01[M::HALF], a10[M::HALF], a11[M::HALF],
         b0[M::REST], b1[M::REST], b2[M::MORE], b3[M::MORE];
-    multiply_items<E, K, S>(p, plan, blockIdx.x, gridDim.x, M{{a00, a01, a10, a11}, {b0, b1, b2, b3}});
+    multiply_item<E, K, S>(p, plan, blockIdx.x, M{{a00, a01, a10, a11}, {b0, b1, b2, b3}});
 }
 
 // Both products of a small backward pass in one launch: neither fills the GPU.
@@ -665,12 +620,11 @@ __global__ __launch_bounds__(S::THREADS) void both_kernel(Product input, Plan in
     __shared__ __align__(1024) uint8_t a00[M::HALF], a01[M::HALF], a10[M::HALF], a11[M::HALF],
         b0[M::REST], b1[M::REST], b2[M::MORE], b3[M::MORE];
     const M mem = {{a00, a01, a10, a11}, {b0, b1, b2, b3}};
-    static_assert(!S::WALKS, "an item a work-group");
     const int j = (int)blockIdx.x;
     if (j < input_plan.items)
-        multiply_items<E, Kind::kInput, S>(input, input_plan, j, 0, mem);
+        multiply_item<E, Kind::kInput, S>(input, input_plan, j, mem);
     else
-        multiply_items<E, Kind::kWeight, S>(weight, weight_plan, j - input_plan.items, 0, mem);
+        multiply_item<E, Kind::kWeight, S>(weight, weight_plan, j - input_plan.items, mem);
 }
 
 // Adds the parts of split tile `split` in order and finishes row fragment `part` of it.
@@ -784,9 +738,8 @@ inline Choice choose(Kind kind, const Product &p, int size) {
 
 template <typename E, Kind K, typename S>
 taco_status launch_product(const Product &p, const Choice &c, hipStream_t stream) {
-    const int32_t groups = S::WALKS && c.plan.items > kLargeCost.places ? kLargeCost.places : c.plan.items;
     const taco_status st = launch(reinterpret_cast<const void *>(&product_kernel<E, K, S>),
-                                  dim3((unsigned)groups), S::THREADS, stream, p, c.plan);
+                                  dim3((unsigned)c.plan.items), S::THREADS, stream, p, c.plan);
     if (st != TACO_OK || c.split_tiles == 0) return st;
     return launch(reinterpret_cast<const void *>(&join_kernel<E, K, S>),
                   dim3((unsigned)c.split_tiles, 2 * S::MF), S::THREADS, stream, p, c.plan);
