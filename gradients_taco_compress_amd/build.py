@@ -1,5 +1,5 @@
-"""Build libtaco.so, libtaco_probe.so, libtaco_norm.so and libtaco_gated.so in-tree with
-hipcc for gfx950.
+"""Build libtaco.so, libtaco_probe.so, libtaco_norm.so, libtaco_rms.so and libtaco_gated.so
+in-tree with hipcc for gfx950.
 
     python gradients_taco_compress_amd/build.py
     TACO_HIPCC_FLAGS="-DTACO_WAVES_PER_GROUP=8" python gradients_taco_compress_amd/build.py
@@ -44,6 +44,12 @@ NORM_LIB = os.path.join(PKG, "libtaco_norm.so")
 #: Its fast path from torch (host code only), a Python extension module.
 NORM_TORCH_SOURCE = os.path.join(CSRC, "taco_norm_torch.cpp")
 NORM_TORCH = os.path.join(PKG, "_norm_torch.so")
+#: Root-mean-square norm, a library of its own, built like NORM_LIB.
+RMS_SOURCES = [os.path.join(CSRC, f) for f in
+               ("taco_rms_abi.hip", "taco_rms_bf16.hip", "taco_rms_f16.hip", "taco_rms_f32.hip")]
+RMS_LIB = os.path.join(PKG, "libtaco_rms.so")
+RMS_TORCH_SOURCE = os.path.join(CSRC, "taco_rms_torch.cpp")
+RMS_TORCH = os.path.join(PKG, "_rms_torch.so")
 #: The gated feed-forward block, a library of its own: the C ABI, the matrix
 #: products (one unit per operand type) and the element-wise kernels.
 GATED_SOURCES = [os.path.join(CSRC, f) for f in
@@ -137,64 +143,55 @@ def _torch_command(source: str, library: str, out: str) -> list:
     cmd += [source, "-o", out]
     for path in library_paths():
         cmd += ["-L", path]
-    return cmd + ["-L", PKG, f"-l:{library}", "-Wl,-rpath,$ORIGIN", "-ltorch_python",
+    return cmd + ["-L", os.path.dirname(library), f"-l:{os.path.basename(library)}", "-Wl,-rpath,$ORIGIN", "-ltorch_python",
                   "-ltorch_hip", "-ltorch_cpu", "-lc10_hip", "-lc10"]
 
 
-def build_gated(verbose: bool = False) -> str:
-    """Compile GATED_SOURCES (in parallel), link GATED_LIB and GATED_TORCH;
-    always recompiles.  Returns GATED_LIB."""
+def _build_library(sources, lib, torch_source, torch_module, verbose: bool) -> str:
+    """Compile `sources` (in parallel), link `lib` and the torch module that calls
+    it; always recompiles.  Returns lib."""
     from concurrent.futures import ThreadPoolExecutor
     tag = f".tmp{os.getpid()}"
-    objs = [src + tag + ".o" for src in GATED_SOURCES]
+    objs = [src + tag + ".o" for src in sources]
+    name = os.path.basename(lib)
     try:
         with ThreadPoolExecutor(max_workers=len(objs)) as pool:
             jobs = [pool.submit(_run, [HIPCC, *FLAGS, "-I", os.path.join(ROOT, "include"),
                                        "-c", src, "-o", obj], verbose)
-                    for src, obj in zip(GATED_SOURCES, objs)]
+                    for src, obj in zip(sources, objs)]
             for j in jobs:
                 j.result()
-        _run([HIPCC, "--offload-arch=gfx950", "-shared", "-Wl,-soname,libtaco_gated.so", *objs,
-              "-o", GATED_LIB + tag], verbose)
-        os.replace(GATED_LIB + tag, GATED_LIB)
-        _run(_torch_command(GATED_TORCH_SOURCE, "libtaco_gated.so", GATED_TORCH + tag), verbose)
-        os.replace(GATED_TORCH + tag, GATED_TORCH)
+        _run([HIPCC, "--offload-arch=gfx950", "-shared", f"-Wl,-soname,{name}", *objs, "-o",
+              lib + tag], verbose)
+        os.replace(lib + tag, lib)
+        _run(_torch_command(torch_source, lib, torch_module + tag), verbose)
+        os.replace(torch_module + tag, torch_module)
     finally:
-        for path in objs + [GATED_LIB + tag, GATED_TORCH + tag]:
+        for path in objs + [lib + tag, torch_module + tag]:
             if os.path.exists(path):
                 os.remove(path)
-    return GATED_LIB
+    return lib
 
 
 def build_norm(verbose: bool = False) -> str:
-    """Compile NORM_SOURCES (in parallel), link NORM_LIB and NORM_TORCH;
-    always recompiles.  Returns NORM_LIB."""
-    from concurrent.futures import ThreadPoolExecutor
-    tag = f".tmp{os.getpid()}"
-    objs = [src + tag + ".o" for src in NORM_SOURCES]
-    try:
-        with ThreadPoolExecutor(max_workers=len(objs)) as pool:
-            jobs = [pool.submit(_run, [HIPCC, *FLAGS, "-I", os.path.join(ROOT, "include"),
-                                       "-c", src, "-o", obj], verbose)
-                    for src, obj in zip(NORM_SOURCES, objs)]
-            for j in jobs:
-                j.result()
-        _run([HIPCC, "--offload-arch=gfx950", "-shared", "-Wl,-soname,libtaco_norm.so", *objs,
-              "-o", NORM_LIB + tag], verbose)
-        os.replace(NORM_LIB + tag, NORM_LIB)
-        _run(_torch_command(NORM_TORCH_SOURCE, "libtaco_norm.so", NORM_TORCH + tag), verbose)
-        os.replace(NORM_TORCH + tag, NORM_TORCH)
-    finally:
-        for path in objs + [NORM_LIB + tag, NORM_TORCH + tag]:
-            if os.path.exists(path):
-                os.remove(path)
-    return NORM_LIB
+    """Layer norm: NORM_SOURCES to NORM_LIB, and NORM_TORCH."""
+    return _build_library(NORM_SOURCES, NORM_LIB, NORM_TORCH_SOURCE, NORM_TORCH, verbose)
+
+
+def build_rms(verbose: bool = False) -> str:
+    """Root-mean-square norm: RMS_SOURCES to RMS_LIB, and RMS_TORCH."""
+    return _build_library(RMS_SOURCES, RMS_LIB, RMS_TORCH_SOURCE, RMS_TORCH, verbose)
+
+
+def build_gated(verbose: bool = False) -> str:
+    """The gated block: GATED_SOURCES to GATED_LIB, and GATED_TORCH."""
+    return _build_library(GATED_SOURCES, GATED_LIB, GATED_TORCH_SOURCE, GATED_TORCH, verbose)
 
 
 if __name__ == "__main__":
     import argparse
     ap = argparse.ArgumentParser(
-        description="Build libtaco (and libtaco_probe, libtaco_norm, libtaco_gated) for gfx950.")
+        description="Build libtaco (and libtaco_probe, libtaco_norm, libtaco_rms, libtaco_gated) for gfx950.")
     ap.add_argument("-q", action="store_true", help="quiet")
     ap.add_argument("--out", default=None,
                     help="build only the operator library, to this path")
@@ -202,4 +199,5 @@ if __name__ == "__main__":
     print(build(verbose=not a.q, out=a.out))
     if not a.out:
         print(build_norm(verbose=not a.q))
+        print(build_rms(verbose=not a.q))
         print(build_gated(verbose=not a.q))

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include "taco_gated.h"
+#include "taco_checks.hpp"
 #include "taco_gated_internal.hpp"
 
 using namespace taco_gated;
@@ -13,19 +14,13 @@ namespace {
 
 constexpr int64_t kSize = 2;           // bytes of an element
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 int64_t round_up(int64_t n, int64_t d) { return (n + d - 1) / d * d; }
 
-// Largest tensor extent accepted, in elements: byte sizes stay far inside 64
-// bits, and the largest launch inside a grid's 2^32 threads.
-constexpr int64_t kMaxElements = INT64_C(1) << 48;
+// Largest product of rows and width accepted: the largest launch stays inside a
+// grid's 2^32 threads.
 constexpr int64_t kMaxProduct = INT64_C(1) << 37;
 
 bool valid_width(int64_t n) { return n > 0 && n <= TACO_GATED_MAX_WIDTH; }
-bool valid_rows(int64_t rows, int64_t width, int64_t ld) {
-    if (rows < 0 || width <= 0 || ld < width) return false;
-    return rows == 0 || ld <= kMaxElements / rows;
-}
 bool valid_sizes(int64_t rows, int64_t hidden, int64_t features) {
     if (rows < 0 || !valid_width(hidden) || !valid_width(features)) return false;
     const int64_t wide = hidden > features ? hidden : features;
@@ -34,37 +29,10 @@ bool valid_sizes(int64_t rows, int64_t hidden, int64_t features) {
 bool valid(taco_gated_activation a) {
     return a == TACO_GATED_SILU || a == TACO_GATED_GELU || a == TACO_GATED_GELU_TANH;
 }
-bool valid(taco_norm_dtype d) { return d == TACO_NORM_BF16 || d == TACO_NORM_F16; }
+bool valid_type(taco_norm_dtype d) { return d == TACO_NORM_BF16 || d == TACO_NORM_F16; }
 
-// A buffer that a call touches: rows of `width` bytes, `pitch` apart, over
-// `bytes` in all (pitch 0: one row).
-struct Span {
-    const void *p;
-    int64_t bytes;
-    int64_t width, pitch;
-};
-Span rows_span(const void *p, int64_t rows, int64_t width, int64_t ld) {
-    return {p, rows > 0 ? ((rows - 1) * ld + width) * kSize : 0, width * kSize, ld * kSize};
-}
-bool overlap(const Span &a, const Span &b) {
-    if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    if (a0 >= b0 + (uintptr_t)b.bytes || b0 >= a0 + (uintptr_t)a.bytes) return false;
-    // Columns of one wider tensor: with one pitch, the rows lie the same in
-    // every stretch of that length.
-    if (a.pitch == 0 || a.pitch != b.pitch) return true;
-    const int64_t pitch = a.pitch, d = (int64_t)(b0 - a0) % pitch, from = d < 0 ? d + pitch : d;
-    return from < a.width || from + b.width > pitch;
-}
-template <int NO, int NI>
-bool any_overlap(const Span (&outs)[NO], const Span (&ins)[NI]) {
-    for (int o = 0; o < NO; ++o) {
-        for (int i = 0; i < NI; ++i)
-            if (overlap(outs[o], ins[i])) return true;
-        for (int i = 0; i < o; ++i)
-            if (overlap(outs[o], outs[i])) return true;
-    }
-    return false;
+Span rows16(const void *p, int64_t rows, int64_t width, int64_t ld) {
+    return rows_span(p, rows, width, ld, kSize);
 }
 
 // An operand [rows, width]: as it is, or as a copy in the workspace whose rows
@@ -181,7 +149,7 @@ taco_status taco_gated_forward(const void *x, int64_t ldx, const void *gate_weig
                                taco_gated_activation activation, void *a, int64_t lda, void *gate,
                                void *up, int64_t ldgu, void *workspace, int64_t workspace_bytes,
                                hipStream_t stream) {
-    if (!valid(dtype)) return TACO_ERR_FORMAT;
+    if (!valid_type(dtype)) return TACO_ERR_FORMAT;
     const bool save = gate || up;
     if (!valid_sizes(rows, hidden, features) || !valid_rows(rows, hidden, ldx) ||
         !valid_rows(features, hidden, ldg) || !valid_rows(features, hidden, ldu) ||
@@ -197,10 +165,10 @@ taco_status taco_gated_forward(const void *x, int64_t ldx, const void *gate_weig
     if (!aligned(x, 2) || !aligned(gate_weight, 2) || !aligned(up_weight, 2) || !aligned(a, 2) ||
         !aligned(gate, 2) || !aligned(up, 2) || (o.bytes && !aligned(workspace, 16)))
         return TACO_ERR_ALIGN;
-    const Span outs[] = {rows_span(a, rows, features, lda), rows_span(gate, rows, features, ldgu),
-                         rows_span(up, rows, features, ldgu), {workspace, o.bytes}};
-    const Span ins[] = {rows_span(x, rows, hidden, ldx), rows_span(gate_weight, features, hidden, ldg),
-                        rows_span(up_weight, features, hidden, ldu)};
+    const Span outs[] = {rows16(a, rows, features, lda), rows16(gate, rows, features, ldgu),
+                         rows16(up, rows, features, ldgu), {workspace, o.bytes}};
+    const Span ins[] = {rows16(x, rows, hidden, ldx), rows16(gate_weight, features, hidden, ldg),
+                        rows16(up_weight, features, hidden, ldu)};
     if (any_overlap(outs, ins)) return TACO_ERR_ALIAS;
     if (workspace_bytes < o.bytes) return TACO_ERR_PARAM;
     Product p = sizes(rows, features, hidden);
@@ -242,7 +210,7 @@ taco_status taco_gated_backward(const void *da, int64_t ldda, const void *x, int
                                 taco_norm_dtype dtype, taco_gated_activation activation, void *dx,
                                 int64_t lddx, void *dgate_weight, void *dup_weight,
                                 void *workspace, int64_t workspace_bytes, hipStream_t stream) {
-    if (!valid(dtype)) return TACO_ERR_FORMAT;
+    if (!valid_type(dtype)) return TACO_ERR_FORMAT;
     const bool want_dx = dx, want_dw = dgate_weight || dup_weight;
     if (!valid_sizes(rows, hidden, features) || !valid_rows(rows, features, ldda) ||
         !valid_rows(rows, features, ldgu) || (want_dw && !valid_rows(rows, hidden, ldx)) ||
@@ -270,12 +238,12 @@ taco_status taco_gated_backward(const void *da, int64_t ldda, const void *x, int
         (want_dx && (!aligned(gate_weight, 2) || !aligned(up_weight, 2))) || !aligned(dx, 2) ||
         !aligned(dgate_weight, 2) || !aligned(dup_weight, 2) || !aligned(workspace, 16))
         return TACO_ERR_ALIGN;
-    const Span outs[] = {rows_span(dx, rows, hidden, lddx), dg_span, du_span, {workspace, o.bytes}};
-    const Span ins[] = {rows_span(da, rows, features, ldda), rows_span(gate, rows, features, ldgu),
-                        rows_span(up, rows, features, ldgu),
-                        rows_span(want_dw ? x : nullptr, rows, hidden, ldx),
-                        rows_span(want_dx ? gate_weight : nullptr, features, hidden, ldg),
-                        rows_span(want_dx ? up_weight : nullptr, features, hidden, ldu)};
+    const Span outs[] = {rows16(dx, rows, hidden, lddx), dg_span, du_span, {workspace, o.bytes}};
+    const Span ins[] = {rows16(da, rows, features, ldda), rows16(gate, rows, features, ldgu),
+                        rows16(up, rows, features, ldgu),
+                        rows16(want_dw ? x : nullptr, rows, hidden, ldx),
+                        rows16(want_dx ? gate_weight : nullptr, features, hidden, ldg),
+                        rows16(want_dx ? up_weight : nullptr, features, hidden, ldu)};
     if (any_overlap(outs, ins)) return TACO_ERR_ALIAS;
     if (workspace_bytes < o.bytes) return TACO_ERR_PARAM;
     Arena arena = {static_cast<char *>(workspace), {}, 0};
@@ -322,7 +290,7 @@ taco_status taco_gated_forward_mx(const uint8_t *x_codes, const uint8_t *x_scale
                                   int64_t hidden, int64_t features, taco_norm_dtype dtype,
                                   taco_gated_activation activation, void *a, int64_t lda,
                                   void *workspace, int64_t workspace_bytes, hipStream_t stream) {
-    if (!valid(dtype)) return TACO_ERR_FORMAT;
+    if (!valid_type(dtype)) return TACO_ERR_FORMAT;
     if (!valid_mx(rows, hidden, features) || !valid_rows(rows, features, lda)) return TACO_ERR_SHAPE;
     if (!valid(activation)) return TACO_ERR_PARAM;
     if (rows == 0) return TACO_OK;
@@ -334,7 +302,7 @@ taco_status taco_gated_forward_mx(const uint8_t *x_codes, const uint8_t *x_scale
         !aligned(a, 2) || (need && !aligned(workspace, 16)))
         return TACO_ERR_ALIGN;
     const int64_t blocks = hidden / 32;
-    const Span outs[] = {rows_span(a, rows, features, lda), {workspace, need}};
+    const Span outs[] = {rows16(a, rows, features, lda), {workspace, need}};
     const Span ins[] = {{x_codes, rows * hidden}, {x_scales, rows * blocks},
                         {gate_codes, features * hidden}, {gate_scales, features * blocks},
                         {up_codes, features * hidden}, {up_scales, features * blocks}};
@@ -369,12 +337,12 @@ taco_status taco_gated_forward_mx(const uint8_t *x_codes, const uint8_t *x_scale
 taco_status taco_gated_mx_encode(const void *x, int64_t ldx, int64_t rows, int64_t hidden,
                                  taco_norm_dtype dtype, uint8_t *codes, uint8_t *scale_bytes,
                                  hipStream_t stream) {
-    if (!valid(dtype) && dtype != TACO_NORM_F32) return TACO_ERR_FORMAT;
+    if (!valid(dtype)) return TACO_ERR_FORMAT;
     if (!valid_width(hidden) || hidden % 32 != 0 || !valid_rows(rows, hidden, ldx))
         return TACO_ERR_SHAPE;
     if (rows == 0) return TACO_OK;
     if (!x || !codes || !scale_bytes) return TACO_ERR_NULL;
-    const int64_t size = dtype == TACO_NORM_F32 ? 4 : 2;
+    const int64_t size = size_of(dtype);
     if (!aligned(x, size)) return TACO_ERR_ALIGN;
     const Span outs[] = {{codes, rows * hidden}, {scale_bytes, rows * (hidden / 32)}};
     const Span ins[] = {{x, ((rows - 1) * ldx + hidden) * size}};

@@ -6,59 +6,12 @@
 #include <hip/hip_runtime.h>
 
 #include "taco_norm.h"
+#include "taco_checks.hpp"
 #include "taco_norm_internal.hpp"
 
 using namespace taco_norm;
 
 namespace {
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-bool valid(taco_norm_dtype d) {
-    return d == TACO_NORM_BF16 || d == TACO_NORM_F16 || d == TACO_NORM_F32;
-}
-int64_t size_of(taco_norm_dtype d) { return d == TACO_NORM_F32 ? 4 : 2; }
-
-// Largest tensor extent accepted, in elements: byte sizes stay far inside 64 bits.
-constexpr int64_t kMaxElements = INT64_C(1) << 48;
-
-// [rows, width] with rows ld apart.
-bool valid_rows(int64_t rows, int64_t width, int64_t ld) {
-    if (rows < 0 || width <= 0 || ld < width) return false;
-    return rows == 0 || ld <= kMaxElements / rows;
-}
-
-// A buffer that a call touches: rows of `width` bytes, `pitch` apart, over
-// `bytes` in all (pitch 0: one row).
-struct Span {
-    const void *p;
-    int64_t bytes;
-    int64_t width, pitch;
-};
-Span rows_span(const void *p, int64_t rows, int64_t width, int64_t ld, int64_t size) {
-    return {p, rows > 0 ? ((rows - 1) * ld + width) * size : 0, width * size, ld * size};
-}
-bool overlap(const Span &a, const Span &b) {
-    if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    if (a0 >= b0 + (uintptr_t)b.bytes || b0 >= a0 + (uintptr_t)a.bytes) return false;
-    // Columns of one wider tensor: with one pitch, the rows lie the same in
-    // every stretch of that length.
-    if (a.pitch == 0 || a.pitch != b.pitch) return true;
-    const int64_t pitch = a.pitch, d = (int64_t)(b0 - a0) % pitch, from = d < 0 ? d + pitch : d;
-    return from < a.width || from + b.width > pitch;
-}
-// Whether an output overlaps an input or another output.
-template <int NO, int NI>
-bool any_overlap(const Span (&outs)[NO], const Span (&ins)[NI]) {
-    for (int o = 0; o < NO; ++o) {
-        for (int i = 0; i < NI; ++i)
-            if (overlap(outs[o], ins[i])) return true;
-        for (int i = 0; i < o; ++i)
-            if (overlap(outs[o], outs[i])) return true;
-    }
-    return false;
-}
 
 taco_status check_types(taco_norm_dtype dtype, taco_norm_dtype param_dtype) {
     if (!valid(dtype) || !valid(param_dtype)) return TACO_ERR_FORMAT;
@@ -164,57 +117,6 @@ taco_status backward(const void *dy, int64_t lddy, bool checkpoint, const void *
     a.params_f32 = param_dtype == TACO_NORM_F32;
     a.inv_scale = 1.0f / scale_of(hidden);
     return with_type(dtype, [&](auto k) { return decltype(k)::backward(a, stream); });
-}
-
-template <typename Fn>
-taco_status with_rms_type(taco_norm_dtype dtype, Fn &&fn) {
-    switch (dtype) {
-        case TACO_NORM_BF16: return fn(Rms<BF16>{});
-        case TACO_NORM_F16: return fn(Rms<F16>{});
-        default: return fn(Rms<F32>{});
-    }
-}
-
-// An output may stand in the place of an input that has its rows (each element
-// is read before it is written, by the thread that writes it).
-bool same_place(const Span &a, const Span &b) { return a.p && a.p == b.p && a.pitch == b.pitch; }
-
-taco_status rms_forward(const void *x, int64_t ldx, const void *residual, int64_t ldr,
-                        int64_t rows, int64_t hidden, taco_norm_dtype dtype, const void *weight,
-                        taco_norm_dtype param_dtype, float eps, bool mx, void *y, int64_t ldy,
-                        uint8_t *codes, uint8_t *scales, void *total, int64_t ldt, float *rstd,
-                        hipStream_t stream) {
-    const taco_status st = check_types(dtype, param_dtype);
-    if (st != TACO_OK) return st;
-    if (!valid_hidden(hidden) || !valid_rows(rows, hidden, ldx) ||
-        (residual && !valid_rows(rows, hidden, ldr)) || (total && !valid_rows(rows, hidden, ldt)) ||
-        (mx ? hidden % 32 != 0 : !valid_rows(rows, hidden, ldy)))
-        return TACO_ERR_SHAPE;
-    if (!(eps >= 0.0f) || isinf(eps) || (total && !residual)) return TACO_ERR_PARAM;
-    if (rows == 0) return TACO_OK;
-    if (!x || (mx ? !codes || !scales : !y)) return TACO_ERR_NULL;
-    const int64_t e = size_of(dtype), p = size_of(param_dtype);
-    if (!aligned(x, e) || !aligned(residual, e) || !aligned(y, e) || !aligned(total, e) ||
-        !aligned(weight, p) || !aligned(rstd, 4))
-        return TACO_ERR_ALIGN;
-    const Span outs[] = {rows_span(y, rows, hidden, ldy, e), rows_span(total, rows, hidden, ldt, e),
-                         {codes, rows * hidden}, {scales, rows * (hidden / 32)}, {rstd, rows * 4}};
-    const Span ins[] = {rows_span(x, rows, hidden, ldx, e),
-                        rows_span(residual, rows, hidden, ldr, e), {weight, hidden * p}};
-    for (const Span &o : outs) {
-        const Span rest[] = {same_place(o, ins[0]) ? Span{} : ins[0],
-                             same_place(o, ins[1]) ? Span{} : ins[1], ins[2]};
-        const Span one[] = {o};
-        if (any_overlap(one, rest)) return TACO_ERR_ALIAS;
-    }
-    const Span none[] = {Span{}};
-    if (any_overlap(outs, none)) return TACO_ERR_ALIAS;
-    RmsForward a = {};
-    a.x = x; a.residual = residual; a.weight = weight;
-    a.y = y; a.total = total; a.rstd = rstd; a.codes = codes; a.scales = scales;
-    a.ldx = ldx; a.ldr = ldr; a.ldy = ldy; a.ldt = ldt; a.rows = rows;
-    a.hidden = (int32_t)hidden; a.params_f32 = param_dtype == TACO_NORM_F32; a.eps = eps;
-    return with_rms_type(dtype, [&](auto k) { return decltype(k)::forward(a, stream); });
 }
 
 template <typename T>
@@ -342,75 +244,6 @@ taco_status taco_norm_weight_grad(const void *dy, int64_t lddy, const uint8_t *c
     a.dw_f32 = dw_dtype == TACO_NORM_F32; a.accumulate = accumulate != 0;
     a.inv_scale = 1.0f / scale_of(hidden);
     return weight_grad(a, dtype, stream);
-}
-
-taco_status taco_norm_rms_forward(const void *x, int64_t ldx, const void *residual, int64_t ldr,
-                                  int64_t rows, int64_t hidden, taco_norm_dtype dtype,
-                                  const void *weight, taco_norm_dtype param_dtype, float eps,
-                                  void *y, int64_t ldy, void *total, int64_t ldt, float *rstd,
-                                  hipStream_t stream) {
-    return rms_forward(x, ldx, residual, ldr, rows, hidden, dtype, weight, param_dtype, eps, false,
-                       y, ldy, nullptr, nullptr, total, ldt, rstd, stream);
-}
-
-taco_status taco_norm_rms_mx(const void *x, int64_t ldx, const void *residual, int64_t ldr,
-                             int64_t rows, int64_t hidden, taco_norm_dtype dtype,
-                             const void *weight, taco_norm_dtype param_dtype, float eps,
-                             uint8_t *codes, uint8_t *scales, void *total, int64_t ldt,
-                             hipStream_t stream) {
-    return rms_forward(x, ldx, residual, ldr, rows, hidden, dtype, weight, param_dtype, eps, true,
-                       nullptr, hidden, codes, scales, total, ldt, nullptr, stream);
-}
-
-int64_t taco_norm_rms_backward_workspace(int64_t rows, int64_t hidden) {
-    if (!valid_hidden(hidden) || !valid_rows(rows, hidden, hidden)) return -1;
-    return rows == 0 ? 0 : backward_parts(rows, hidden) * hidden * (int64_t)sizeof(float);
-}
-
-taco_status taco_norm_rms_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
-                                   const float *rstd, const void *dtotal, int64_t lddt,
-                                   const void *weight, int64_t rows, int64_t hidden,
-                                   taco_norm_dtype dtype, taco_norm_dtype param_dtype, void *dx,
-                                   int64_t lddx, void *dweight, void *workspace,
-                                   int64_t workspace_bytes, hipStream_t stream) {
-    const taco_status st = check_types(dtype, param_dtype);
-    if (st != TACO_OK) return st;
-    if (!valid_hidden(hidden) || !valid_rows(rows, hidden, lddy) ||
-        !valid_rows(rows, hidden, ldx) || !valid_rows(rows, hidden, lddx) ||
-        (dtotal && !valid_rows(rows, hidden, lddt)))
-        return TACO_ERR_SHAPE;
-    const int64_t e = size_of(dtype), p = size_of(param_dtype);
-    const Span dw = {dweight, hidden * p}, w = {weight, hidden * p};
-    if (rows == 0) {
-        if (!aligned(dweight, p)) return TACO_ERR_ALIGN;
-        if (overlap(dw, w)) return TACO_ERR_ALIAS;
-        return dweight ? fill_zero(dweight, hidden, param_dtype, stream) : TACO_OK;
-    }
-    if (!dy || !x || !rstd || !dx || (dweight && !workspace)) return TACO_ERR_NULL;
-    if (!aligned(dy, e) || !aligned(x, e) || !aligned(dx, e) || !aligned(dtotal, e) ||
-        !aligned(weight, p) || !aligned(dweight, p) || !aligned(rstd, 4) ||
-        (dweight && !aligned(workspace, 16)))
-        return TACO_ERR_ALIGN;
-    const int64_t need = dweight ? taco_norm_rms_backward_workspace(rows, hidden) : 0;
-    const Span dx_span = rows_span(dx, rows, hidden, lddx, e);
-    const Span dy_span = rows_span(dy, rows, hidden, lddy, e);
-    const Span dt_span = rows_span(dtotal, rows, hidden, lddt, e);
-    const Span outs[] = {dx_span, dw, {dweight ? workspace : nullptr, need}};
-    const Span others[] = {rows_span(x, rows, hidden, ldx, e), {rstd, rows * 4}, w};
-    // dx may be dy or dtotal itself: every element is read before it is written.
-    const Span into_dx[] = {same_place(dx_span, dy_span) ? Span{} : dy_span,
-                            same_place(dx_span, dt_span) ? Span{} : dt_span};
-    const Span sums[] = {dw, outs[2]}, one[] = {dx_span}, grads[] = {dy_span, dt_span};
-    if (any_overlap(outs, others) || any_overlap(one, into_dx) || any_overlap(sums, grads))
-        return TACO_ERR_ALIAS;
-    if (workspace_bytes < need) return TACO_ERR_PARAM;
-    RmsBackward a = {};
-    a.dy = dy; a.x = x; a.dtotal = dtotal; a.rstd = rstd; a.weight = weight;
-    a.dx = dx; a.dweight = dweight;
-    a.partial = dweight ? static_cast<float *>(workspace) : nullptr;
-    a.lddy = lddy; a.ldx = ldx; a.lddt = lddt; a.lddx = lddx; a.rows = rows;
-    a.hidden = (int32_t)hidden; a.params_f32 = param_dtype == TACO_NORM_F32;
-    return with_rms_type(dtype, [&](auto k) { return decltype(k)::backward(a, stream); });
 }
 
 }  // extern "C"

@@ -1,7 +1,7 @@
 // Root-mean-square norm's row kernels for gfx950, templated on the activations'
 // type: the forward pass with or without the residual's addition, into rows of
 // the same type or into 8-bit codes with block scales, and the backward pass
-// (formulas in taco_norm.h, the 8-bit form in taco_mx.hpp).
+// (formulas in taco_rms.h, the 8-bit form in taco_mx.hpp).
 //
 // They are laid out as layer norm's (taco_norm_rows.hpp): a row belongs to TPR
 // threads, is held in registers between the reduction over it and the use of its
@@ -18,6 +18,7 @@
 #pragma once
 
 #include "taco_norm_rows.hpp"
+#include "taco_rms_internal.hpp"
 #include "taco_mx.hpp"
 
 namespace taco_norm {

@@ -1,5 +1,5 @@
 // What the fast paths of the torch layers (taco_norm_torch.cpp,
-// taco_gated_torch.cpp) share: looking at tensors, making outputs, and turning
+// taco_rms_torch.cpp, taco_gated_torch.cpp) share: looking at tensors, making outputs, and turning
 // errors into Python's.
 #pragma once
 
@@ -67,6 +67,22 @@ bool on_device(const at::Tensor *t, c10::Device dev) {
 
 bool vector(const at::Tensor *t, c10::Device dev, int64_t n, ScalarType dtype) {
     return on_device(t, dev) && t->scalar_type() == dtype && t->numel() == n && t->is_contiguous();
+}
+
+// A norm parameter: None, or hidden contiguous elements of the activations'
+// type or float32, and of one type with the other parameter.
+[[maybe_unused]] bool parameter(PyObject *o, c10::Device dev, int64_t hidden, ScalarType dtype, const void **p,
+               ScalarType *ptype, bool *typed) {
+    *p = nullptr;
+    if (o == Py_None) return true;
+    const at::Tensor *t = tensor(o);
+    if (!on_device(t, dev) || t->numel() != hidden || !t->is_contiguous()) return false;
+    const ScalarType s = t->scalar_type();
+    if ((s != dtype && s != at::kFloat) || (*typed && s != *ptype)) return false;
+    *ptype = s;
+    *typed = true;
+    *p = t->data_ptr();
+    return true;
 }
 
 at::Tensor make(at::IntArrayRef sizes, ScalarType dtype, c10::Device dev) {

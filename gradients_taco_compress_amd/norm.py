@@ -1,11 +1,12 @@
-"""Binding of libtaco_norm (include/taco_norm.h): layer norm for training, with
+"""Binding of libtaco_norm (include/taco_norm.h) and libtaco_rms
+(include/taco_rms.h): layer norm for training, with
 an 8-bit checkpoint of the normalised activation that serves both the norm's
 backward pass and the weight gradient of the linear layer behind it; and
 root-mean-square norm with the residual's addition, for training and into 8 bits.
 
 Three layers:
 
-* ``taco_norm_*``: the C ABI with the same names and arguments (device
+* ``taco_norm_*`` and ``taco_rms_*``: the C ABIs with the same names and arguments (device
   pointers and stream handles as ints).
 * ``layer_norm``, ``layer_norm_backward``, ``layer_norm_checkpoint``,
   ``layer_norm_checkpoint_backward``, ``checkpoint_weight_grad``, ``rms_norm``,
@@ -66,18 +67,39 @@ _SIGNATURES = {
     "taco_norm_weight_grad_workspace": ([_P, _I64, _P, _I64, _I64, _I64], _I64),
     "taco_norm_weight_grad": ([_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _P, _I32, _P, _I32, _I32,
                                _P, _P, _I64, _P], _STATUS),
-    "taco_norm_rms_forward": ([_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I32, _F32, _P, _I64, _P,
-                               _I64, _P, _P], _STATUS),
-    "taco_norm_rms_mx": ([_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I32, _F32, _P, _P, _P, _I64,
-                          _P], _STATUS),
-    "taco_norm_rms_backward_workspace": ([_I64, _I64], _I64),
-    "taco_norm_rms_backward": ([_P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _I64, _I32, _I32, _P,
-                                _I64, _P, _P, _I64, _P], _STATUS),
 }
 #: Symbols the library exports (checked against include/taco_norm.h).
 EXPORTS = tuple(_SIGNATURES)
 for _name, (_args, _res) in _SIGNATURES.items():
     _fn = getattr(_lib, _name)
+    _fn.argtypes, _fn.restype = _args, _res
+    globals()[_name] = _fn
+
+# Root-mean-square norm is a library of its own (include/taco_rms.h).
+RMS_LIB_PATH = os.path.join(PKG, "libtaco_rms.so")
+if not os.path.exists(RMS_LIB_PATH):
+    raise ImportError(
+        f"libtaco_rms.so is not built ({RMS_LIB_PATH} missing); run "
+        "`python gradients_taco_compress_amd/build.py` (there is no CPU fallback)")
+_rms = ctypes.CDLL(RMS_LIB_PATH)
+try:
+    from . import _rms_torch as _fast_rms
+except ImportError as e:
+    raise ImportError(f"the torch module of libtaco_rms is not built ({e}); run "
+                      "`python gradients_taco_compress_amd/build.py`") from e
+_RMS_SIGNATURES = {
+    "taco_rms_forward": ([_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I32, _F32, _P, _I64, _P,
+                               _I64, _P, _P], _STATUS),
+    "taco_rms_mx": ([_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I32, _F32, _P, _P, _P, _I64,
+                          _P], _STATUS),
+    "taco_rms_backward_workspace": ([_I64, _I64], _I64),
+    "taco_rms_backward": ([_P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _I64, _I32, _I32, _P,
+                                _I64, _P, _P, _I64, _P], _STATUS),
+}
+#: Symbols that library exports (checked against include/taco_rms.h).
+RMS_EXPORTS = tuple(_RMS_SIGNATURES)
+for _name, (_args, _res) in _RMS_SIGNATURES.items():
+    _fn = getattr(_rms, _name)
     _fn.argtypes, _fn.restype = _args, _res
     globals()[_name] = _fn
 
@@ -403,7 +425,7 @@ def rms_norm(x, weight=None, eps: float = 1e-5, residual=None, out=None, total=N
     rstd), total = x + residual (None without a residual), rstd float32 [rows], as
     the backward pass takes them.  out and total may be x or residual (in place)."""
     if out is None and total is None and rstd is None and stream is None:
-        done = _fast.rms_norm(x, weight, eps, residual)
+        done = _fast_rms.rms_norm(x, weight, eps, residual)
         if done is not None:
             return done
     rows, hidden, ldx = _pitch(x, "x")
@@ -419,7 +441,7 @@ def rms_norm(x, weight=None, eps: float = 1e-5, residual=None, out=None, total=N
     rstd = at.empty(rows, torch.float32) if rstd is None else rstd
     ldy = _same_rows(out, "out", x.dtype, rows, hidden)
     ldt = 0 if total is None else _same_rows(total, "total", x.dtype, rows, hidden)
-    at.call(_lib.taco_norm_rms_forward, "taco_norm_rms_forward", x.data_ptr(), ldx, r, ldr, rows,
+    at.call(_rms.taco_rms_forward, "taco_rms_forward", x.data_ptr(), ldx, r, ldr, rows,
             hidden, DTYPES[x.dtype], w, DTYPES[ptype], eps, out.data_ptr(), ldy, _ptr(total), ldt,
             _vector(rstd, rows, "rstd"))
     return out, total, rstd
@@ -431,7 +453,7 @@ def rms_norm_mx(x, weight=None, eps: float = 1e-5, residual=None, total=None, st
     2^(byte - 127), as gated.gated_forward_mx takes them.  total may be x or
     residual (in place)."""
     if total is None and stream is None:
-        done = _fast.rms_norm_mx(x, weight, eps, residual)
+        done = _fast_rms.rms_norm_mx(x, weight, eps, residual)
         if done is not None:
             return done
     rows, hidden, ldx = _pitch(x, "x")
@@ -448,7 +470,7 @@ def rms_norm_mx(x, weight=None, eps: float = 1e-5, residual=None, total=None, st
     if residual is not None and total is None:
         total = at.empty(x.shape, x.dtype)
     ldt = 0 if total is None else _same_rows(total, "total", x.dtype, rows, hidden)
-    at.call(_lib.taco_norm_rms_mx, "taco_norm_rms_mx", x.data_ptr(), ldx, r, ldr, rows, hidden,
+    at.call(_rms.taco_rms_mx, "taco_rms_mx", x.data_ptr(), ldx, r, ldr, rows, hidden,
             DTYPES[x.dtype], w, DTYPES[ptype], eps, codes.data_ptr(), scales.data_ptr(),
             _ptr(total), ldt)
     return codes, scales, total
@@ -461,7 +483,7 @@ def rms_norm_backward(dy, x, rstd, weight=None, dtotal=None, dx=None, param_grad
     residual alike, and may be dy or dtotal (in place); dweight is of param_dtype
     (weight's type; float32 without a weight), None without param_grads."""
     if dx is None and param_grads and param_dtype is None and stream is None:
-        done = _fast.rms_norm_backward(dy, x, rstd, weight, dtotal)
+        done = _fast_rms.rms_norm_backward(dy, x, rstd, weight, dtotal)
         if done is not None:
             return done
     rows, hidden, lddy = _pitch(dy, "dy")
@@ -473,9 +495,9 @@ def rms_norm_backward(dy, x, rstd, weight=None, dtotal=None, dx=None, param_grad
     dx = at.empty(dy.shape, dy.dtype) if dx is None else dx
     lddx = _same_rows(dx, "dx", dy.dtype, rows, hidden)
     dw = at.empty(hidden, ptype) if param_grads else None
-    ws = (at.workspace(_lib.taco_norm_rms_backward_workspace(rows, hidden)) if param_grads
+    ws = (at.workspace(_rms.taco_rms_backward_workspace(rows, hidden)) if param_grads
           else None)
-    at.call(_lib.taco_norm_rms_backward, "taco_norm_rms_backward", dy.data_ptr(), lddy,
+    at.call(_rms.taco_rms_backward, "taco_rms_backward", dy.data_ptr(), lddy,
             x.data_ptr(), ldx, q, _ptr(dtotal), lddt, w, rows, hidden, DTYPES[dy.dtype],
             DTYPES[ptype], dx.data_ptr(), lddx, _ptr(dw), _ptr(ws),
             0 if ws is None else ws.numel())

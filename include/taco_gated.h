@@ -21,8 +21,8 @@
  *
  * kept as one byte a code (TACO_FORMAT_E4M3 of taco.h; zeros are code 0) and one
  * byte e + 127 a block; a block that holds an infinity or a NaN has scale byte
- * 255 and codes 127, NaN both.  taco_norm_rms_mx of taco_norm.h writes rows in
- * this form.
+ * 255 and codes 127, NaN both.  taco_rms_mx of taco_rms.h writes rows in this
+ * form.
  *
  * Conventions (those of taco_norm.h, except where stated)
  *   - Tensor pointers are DEVICE pointers owned by the caller.  The library

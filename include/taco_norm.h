@@ -1,9 +1,7 @@
 /*
  * libtaco_norm -- layer norm for training on AMD Instinct MI355X (gfx950),
  * with an 8-bit checkpoint of the normalised activation that serves both the
- * norm's backward pass and the weight gradient of the linear layer behind it;
- * and root-mean-square norm with the residual's addition, into rows of the same
- * type or of 8-bit codes with block scales (at the end).
+ * norm's backward pass and the weight gradient of the linear layer behind it.
  *
  * Over a [rows, hidden] tensor, row t and column k:
  *
@@ -162,55 +160,6 @@ taco_status taco_norm_weight_grad(const void *dy, int64_t lddy, const uint8_t *c
                                   taco_norm_dtype param_dtype, void *dw,
                                   taco_norm_dtype dw_dtype, int32_t accumulate, float *dbias,
                                   void *workspace, int64_t workspace_bytes, hipStream_t stream);
-
-/*
- * Root-mean-square norm, with the residual's addition:
- *
- *     s = x + residual     q_t = (mean_k s_tk^2 + eps)^(-1/2)     y_tk = s_tk q_t w_k
- *
- *     g = dy w,   h_tk = s_tk q_t
- *     dx_tk = dtotal_tk + q_t (g_tk - h_tk mean_k(g_tk h_tk))     dw_k = sum_t dy_tk h_tk
- *
- * residual and weight may be NULL (0 and 1).  dx is the gradient of x and of
- * residual alike; dtotal is the gradient that arrives at s by its other ways.
- * Conventions as above; ldr, ldt and lddt are the row pitches of residual,
- * total and dtotal (not looked at where those are NULL), and
- *   - total [rows, hidden] is s, for the next addition and the backward pass.  It
- *     may be NULL, and has to be without a residual (PARAM; s is x then).  y is
- *     formed from s before it is rounded.
- *   - y and total may each be x itself or residual itself (same pointer and
- *     pitch), dx may be dy or dtotal itself.
- *   - A row's squares have to fit float32: a mean beyond 3e38 overflows.
- */
-
-/* Forward.  rstd: [rows] float32 output q, may be NULL. */
-taco_status taco_norm_rms_forward(const void *x, int64_t ldx, const void *residual, int64_t ldr,
-                                  int64_t rows, int64_t hidden, taco_norm_dtype dtype,
-                                  const void *weight, taco_norm_dtype param_dtype, float eps,
-                                  void *y, int64_t ldy, void *total, int64_t ldt, float *rstd,
-                                  hipStream_t stream);
-
-/* Forward into 8 bits: y as codes [rows, hidden] and scales [rows, hidden / 32], the
- * block-scaled form of taco_gated.h, which taco_gated_forward_mx reads; formed
- * from y in float32.  hidden is a multiple of 32 (SHAPE). */
-taco_status taco_norm_rms_mx(const void *x, int64_t ldx, const void *residual, int64_t ldr,
-                             int64_t rows, int64_t hidden, taco_norm_dtype dtype,
-                             const void *weight, taco_norm_dtype param_dtype, float eps,
-                             uint8_t *codes, uint8_t *scales, void *total, int64_t ldt,
-                             hipStream_t stream);
-
-/* Bytes of workspace that taco_norm_rms_backward needs for dweight (0 with rows
- * == 0; -1 for a bad shape).  A call with dweight NULL needs none. */
-int64_t taco_norm_rms_backward_workspace(int64_t rows, int64_t hidden);
-
-/* Backward from s (x: total as written by the forward pass, or x without a
- * residual) and rstd.  dweight: [hidden] of param_dtype, may be NULL. */
-taco_status taco_norm_rms_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
-                                   const float *rstd, const void *dtotal, int64_t lddt,
-                                   const void *weight, int64_t rows, int64_t hidden,
-                                   taco_norm_dtype dtype, taco_norm_dtype param_dtype, void *dx,
-                                   int64_t lddx, void *dweight, void *workspace,
-                                   int64_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,6 +1,12 @@
 """Root-mean-square norm without a GPU: the C ABI refuses every bad argument
 before touching the device."""
+import os
+import re
+import subprocess
+
 import pytest
+
+from conftest import ROOT
 
 torch = pytest.importorskip("torch")
 if torch.cuda.device_count() > 0:
@@ -13,15 +19,50 @@ BF16, F16, F32 = range(3)
 A = 1 << 24          # spacing of fake, aligned device addresses
 
 
+def declared():
+    text = open(os.path.join(ROOT, "include", "taco_rms.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    return sorted(set(re.findall(r"\b(taco_rms_[a-z0-9_]+)\s*\(", text)))
+
+
+def test_every_declared_function_is_exported_and_bound():
+    out = subprocess.run(["nm", "-D", "--defined-only", norm.RMS_LIB_PATH], capture_output=True,
+                         text=True).stdout
+    assert set(re.findall(r" T (taco_\w+)", out)) == set(declared()) == set(norm.RMS_EXPORTS)
+    for n in declared():
+        assert callable(getattr(norm, n))
+
+
+def test_rms_sources_compile_like_the_rest(monkeypatch, tmp_path):
+    import __graft_entry__ as g
+    m = g._load_hip_build()
+    cmds = []
+
+    def fake_run(cmd, verbose):
+        cmds.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "wb").close()
+    monkeypatch.setattr(m, "_run", fake_run)
+    monkeypatch.setattr(m, "RMS_LIB", str(tmp_path / "libtaco_rms.so"))
+    monkeypatch.setattr(m, "RMS_TORCH", str(tmp_path / "_rms_torch.so"))
+    m.build_rms()
+    compiles = [c for c in cmds if "-c" in c]
+    assert sorted(c[c.index("-c") + 1] for c in compiles) == sorted(m.RMS_SOURCES)
+    feature = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
+    for c in compiles:
+        assert "--offload-arch=gfx950" in c and "-O3" in c
+        assert any(c[i:i + 4] == feature for i in range(len(c) - 3))
+    assert not [f for f in os.listdir(m.CSRC) if ".tmp" in f]
+
+
 def forward(x=A, ldx=64, r=2 * A, ldr=64, rows=4, hidden=64, dtype=BF16, w=3 * A, pdtype=F32, eps=1e-5,
             y=4 * A, ldy=64, total=5 * A, ldt=64, rstd=6 * A):
-    return norm.taco_norm_rms_forward(x, ldx, r, ldr, rows, hidden, dtype, w, pdtype, eps, y, ldy,
+    return norm.taco_rms_forward(x, ldx, r, ldr, rows, hidden, dtype, w, pdtype, eps, y, ldy,
                                       total, ldt, rstd, 0)
 
 
 def mx(x=A, ldx=64, r=2 * A, ldr=64, rows=4, hidden=64, dtype=BF16, w=3 * A, pdtype=F32, eps=1e-5,
        codes=4 * A, scales=7 * A, total=5 * A, ldt=64):
-    return norm.taco_norm_rms_mx(x, ldx, r, ldr, rows, hidden, dtype, w, pdtype, eps, codes, scales,
+    return norm.taco_rms_mx(x, ldx, r, ldr, rows, hidden, dtype, w, pdtype, eps, codes, scales,
                                  total, ldt, 0)
 
 
@@ -61,8 +102,8 @@ def test_mx_outputs():
 
 def backward(dy=A, lddy=64, x=2 * A, ldx=64, rstd=3 * A, dt=4 * A, lddt=64, w=5 * A, rows=4, hidden=64,
              dtype=BF16, pdtype=F32, dx=6 * A, lddx=64, dw=7 * A, ws=8 * A, nbytes=None):
-    nbytes = norm.taco_norm_rms_backward_workspace(rows, hidden) if nbytes is None else nbytes
-    return norm.taco_norm_rms_backward(dy, lddy, x, ldx, rstd, dt, lddt, w, rows, hidden, dtype, pdtype,
+    nbytes = norm.taco_rms_backward_workspace(rows, hidden) if nbytes is None else nbytes
+    return norm.taco_rms_backward(dy, lddy, x, ldx, rstd, dt, lddt, w, rows, hidden, dtype, pdtype,
                                        dx, lddx, dw, ws, nbytes, 0)
 
 
@@ -80,14 +121,14 @@ def test_backward_refusals():
     assert backward(dx=A, lddx=72) == ALIAS and backward(dx=2 * A) == ALIAS
     assert backward(dw=A) == ALIAS and backward(ws=4 * A) == ALIAS and backward(dw=6 * A) == ALIAS
     assert backward(ws=5 * A) == ALIAS
-    need = norm.taco_norm_rms_backward_workspace(4, 64)
+    need = norm.taco_rms_backward_workspace(4, 64)
     assert need == 64 * 4 and backward(nbytes=need - 1) == PARAM
     assert backward(rows=0, dw=0, dx=0, dy=0, x=0) == OK
     assert backward(rows=0, dw=7 * A + 1) == ALIGN and backward(rows=0, dw=5 * A) == ALIAS
 
 
 def test_backward_workspace():
-    f = norm.taco_norm_rms_backward_workspace
+    f = norm.taco_rms_backward_workspace
     assert f(0, 64) == 0
     assert f(-1, 64) == f(4, 0) == f(4, 1048577) == f(1 << 47, 1 << 10) == -1
     assert f(1, 2560) == 2560 * 4 and f(1 << 20, 2560) == 512 * 2560 * 4
