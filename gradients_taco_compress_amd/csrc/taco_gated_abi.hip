@@ -16,15 +16,18 @@ constexpr int64_t kSize = 2;           // bytes of an element
 
 int64_t round_up(int64_t n, int64_t d) { return (n + d - 1) / d * d; }
 
-// Largest product of rows and width accepted: the largest launch stays inside a
-// grid's 2^32 threads.
-constexpr int64_t kMaxProduct = INT64_C(1) << 37;
+// Sizes accepted: the products' smallest tiles (256 threads to 128x64 outputs at
+// the least) stay inside a grid's 2^32 threads.
+constexpr int64_t kMaxTiles = INT64_C(1) << 24;
+
+int64_t tiles(int64_t m, int64_t n) { return (m + 127) / 128 * ((n + 63) / 64); }
 
 bool valid_width(int64_t n) { return n > 0 && n <= TACO_GATED_MAX_WIDTH; }
 bool valid_sizes(int64_t rows, int64_t hidden, int64_t features) {
-    if (rows < 0 || !valid_width(hidden) || !valid_width(features)) return false;
+    if (rows < 0 || rows > kMaxElements || !valid_width(hidden) || !valid_width(features)) return false;
     const int64_t wide = hidden > features ? hidden : features;
-    return rows <= kMaxProduct / wide && hidden <= kMaxProduct / features;
+    return rows / 128 < kMaxTiles && tiles(rows, wide) < kMaxTiles &&
+           2 * tiles(features, hidden) < kMaxTiles;
 }
 bool valid(taco_gated_activation a) {
     return a == TACO_GATED_SILU || a == TACO_GATED_GELU || a == TACO_GATED_GELU_TANH;

@@ -92,19 +92,19 @@ taco_status zero_row(void *p, int64_t n, taco_norm_dtype dtype, hipStream_t stre
 extern "C" {
 
 taco_status taco_rms_forward(const void *x, int64_t ldx, const void *residual, int64_t ldr,
-                                  int64_t rows, int64_t hidden, taco_norm_dtype dtype,
-                                  const void *weight, taco_norm_dtype param_dtype, float eps,
-                                  void *y, int64_t ldy, void *total, int64_t ldt, float *rstd,
-                                  hipStream_t stream) {
+                             int64_t rows, int64_t hidden, taco_norm_dtype dtype,
+                             const void *weight, taco_norm_dtype param_dtype, float eps,
+                             void *y, int64_t ldy, void *total, int64_t ldt, float *rstd,
+                             hipStream_t stream) {
     return rms_forward(x, ldx, residual, ldr, rows, hidden, dtype, weight, param_dtype, eps, false,
                        y, ldy, nullptr, nullptr, total, ldt, rstd, stream);
 }
 
 taco_status taco_rms_mx(const void *x, int64_t ldx, const void *residual, int64_t ldr,
-                             int64_t rows, int64_t hidden, taco_norm_dtype dtype,
-                             const void *weight, taco_norm_dtype param_dtype, float eps,
-                             uint8_t *codes, uint8_t *scales, void *total, int64_t ldt,
-                             hipStream_t stream) {
+                        int64_t rows, int64_t hidden, taco_norm_dtype dtype,
+                        const void *weight, taco_norm_dtype param_dtype, float eps,
+                        uint8_t *codes, uint8_t *scales, void *total, int64_t ldt,
+                        hipStream_t stream) {
     return rms_forward(x, ldx, residual, ldr, rows, hidden, dtype, weight, param_dtype, eps, true,
                        nullptr, hidden, codes, scales, total, ldt, nullptr, stream);
 }
@@ -115,11 +115,11 @@ int64_t taco_rms_backward_workspace(int64_t rows, int64_t hidden) {
 }
 
 taco_status taco_rms_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
-                                   const float *rstd, const void *dtotal, int64_t lddt,
-                                   const void *weight, int64_t rows, int64_t hidden,
-                                   taco_norm_dtype dtype, taco_norm_dtype param_dtype, void *dx,
-                                   int64_t lddx, void *dweight, void *workspace,
-                                   int64_t workspace_bytes, hipStream_t stream) {
+                              const float *rstd, const void *dtotal, int64_t lddt,
+                              const void *weight, int64_t rows, int64_t hidden,
+                              taco_norm_dtype dtype, taco_norm_dtype param_dtype, void *dx,
+                              int64_t lddx, void *dweight, void *workspace,
+                              int64_t workspace_bytes, hipStream_t stream) {
     const taco_status st = check_types(dtype, param_dtype);
     if (st != TACO_OK) return st;
     if (!valid_hidden(hidden) || !valid_rows(rows, hidden, lddy) ||

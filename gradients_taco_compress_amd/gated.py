@@ -168,13 +168,15 @@ def gated_backward(da, x, gate, up, gate_weight, up_weight, activation: str = "s
     dtype, act = _type(da, "da"), _activation(activation)
     rows, features, ldda = _pitch(da, "da")
     ldgu = _same_rows(gate, "gate", dtype, rows, features)
-    if _same_rows(up, "up", dtype, rows, features) != ldgu:
-        gate, up, ldgu = gate.contiguous(), up.contiguous(), features
+    ldup = _same_rows(up, "up", dtype, rows, features)
     hidden = x.shape[-1] if isinstance(x, torch.Tensor) and x.dim() else 0
     ldx = _same_rows(x, "x", dtype, rows, hidden)
     _, ldg = _weight(gate_weight, "gate_weight", dtype, hidden, features)
     _, ldu = _weight(up_weight, "up_weight", dtype, hidden, features)
     at = _Launch(stream, (da, x, gate, up, gate_weight, up_weight))
+    if ldup != ldgu:
+        with torch.cuda.stream(at.stream):     # (in the order of that stream's work)
+            gate, up, ldgu = gate.contiguous(), up.contiguous(), features
     dx = at.empty(x.shape, dtype) if input_grad else None
     dg, du = ((at.empty((features, hidden), dtype), at.empty((features, hidden), dtype))
               if weight_grads else (None, None))
@@ -259,5 +261,8 @@ class _Gated(torch.autograd.Function):
 
 
 def gated(x, gate_weight, up_weight, activation: str = "silu"):
-    """Differentiable ``act(x gate_weight^T) * (x up_weight^T)``."""
+    """Differentiable ``act(x gate_weight^T) * (x up_weight^T)``.  It keeps x and
+    both projections for its backward pass, nothing without gradients."""
+    if not torch.is_grad_enabled():
+        return gated_forward(_even(x), _even(gate_weight), _even(up_weight), activation)
     return _Gated.apply(x, gate_weight, up_weight, activation)

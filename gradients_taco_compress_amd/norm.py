@@ -1,13 +1,13 @@
 """Binding of libtaco_norm (include/taco_norm.h) and libtaco_rms
-(include/taco_rms.h): layer norm for training, with
-an 8-bit checkpoint of the normalised activation that serves both the norm's
-backward pass and the weight gradient of the linear layer behind it; and
-root-mean-square norm with the residual's addition, for training and into 8 bits.
+(include/taco_rms.h): layer norm for training, with an 8-bit checkpoint of the
+normalised activation that serves both the norm's backward pass and the weight
+gradient of the linear layer behind it; and root-mean-square norm with the
+residual's addition, for training and into 8 bits.
 
 Three layers:
 
-* ``taco_norm_*`` and ``taco_rms_*``: the C ABIs with the same names and arguments (device
-  pointers and stream handles as ints).
+* ``taco_norm_*`` and ``taco_rms_*``: the C ABIs with the same names and
+  arguments (device pointers and stream handles as ints).
 * ``layer_norm``, ``layer_norm_backward``, ``layer_norm_checkpoint``,
   ``layer_norm_checkpoint_backward``, ``checkpoint_weight_grad``, ``rms_norm``,
   ``rms_norm_mx``, ``rms_norm_backward``: the same calls on torch tensors,
@@ -89,12 +89,12 @@ except ImportError as e:
                       "`python gradients_taco_compress_amd/build.py`") from e
 _RMS_SIGNATURES = {
     "taco_rms_forward": ([_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I32, _F32, _P, _I64, _P,
-                               _I64, _P, _P], _STATUS),
-    "taco_rms_mx": ([_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I32, _F32, _P, _P, _P, _I64,
-                          _P], _STATUS),
+                          _I64, _P, _P], _STATUS),
+    "taco_rms_mx": ([_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I32, _F32, _P, _P, _P, _I64, _P],
+                    _STATUS),
     "taco_rms_backward_workspace": ([_I64, _I64], _I64),
     "taco_rms_backward": ([_P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _I64, _I32, _I32, _P,
-                                _I64, _P, _P, _I64, _P], _STATUS),
+                           _I64, _P, _P, _I64, _P], _STATUS),
 }
 #: Symbols that library exports (checked against include/taco_rms.h).
 RMS_EXPORTS = tuple(_RMS_SIGNATURES)
@@ -562,6 +562,7 @@ class _RmsResidual(torch.autograd.Function):
     def forward(ctx, x, residual, weight, eps):
         y, total, rstd = rms_norm(_even(x), weight, eps, residual=_even(residual))
         ctx.save_for_backward(total, rstd, weight)
+        ctx.residual_shape = residual.shape
         ctx.set_materialize_grads(False)
         return y, total
 
@@ -571,13 +572,15 @@ class _RmsResidual(torch.autograd.Function):
         total, rstd, weight = ctx.saved_tensors
         need = ctx.needs_input_grad
         if dy is None:                       # y was not used
-            dw = torch.zeros_like(weight) if need[2] else None
-            return dtotal if need[0] else None, dtotal if need[1] else None, dw, None
-        dtotal = None if dtotal is None else _even(dtotal)
-        dx, dw = rms_norm_backward(_even(dy), total, rstd, weight, dtotal=dtotal,
-                                   param_grads=need[2])
-        return (dx if need[0] else None, dx if need[1] else None,
-                dw.view(weight.shape) if need[2] else None, None)
+            dx, dw = dtotal, torch.zeros_like(weight) if need[2] else None
+        else:
+            dtotal = None if dtotal is None else _even(dtotal)
+            dx, dw = rms_norm_backward(_even(dy), total, rstd, weight, dtotal=dtotal,
+                                       param_grads=need[2])
+            dw = dw.view(weight.shape) if need[2] else None
+        # (the residual has x's rows, not always its leading dimensions)
+        return (dx if need[0] else None, dx.reshape(ctx.residual_shape) if need[1] else None,
+                dw, None)
 
 
 class _NormLinear(torch.autograd.Function):

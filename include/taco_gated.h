@@ -35,8 +35,8 @@
  *     length is no multiple of 8 elements, are first copied to where they do,
  *     which takes their size of workspace and time (few rows excepted: up to
  *     16, forward).
- *   - Sums are float32 (matrix instructions); the activation and its product
- *     are formed in float32 from the unrounded sums, and results are rounded once.
+ *   - Sums are float32 (matrix instructions; for codes see below); the activation
+ *     and its product are formed in float32 from the unrounded sums, and results are rounded once.
  *     dG and dU are rounded to dtype before their products: fp16 gradients need
  *     the usual loss scale.  Results do not depend on timing: no atomics.
  *   - Calls are asynchronous on `stream`.  Checks run in this order: types
@@ -72,7 +72,8 @@ typedef enum {
     TACO_GATED_GELU_TANH = 2
 } taco_gated_activation;
 
-/* Largest hidden and features accepted. */
+/* Largest hidden and features accepted.  (Their product, and that of either with
+ * rows, may be up to 2^36; more is SHAPE where a launch could not hold its tiles.) */
 #define TACO_GATED_MAX_WIDTH 1048576
 
 /* Bytes of workspace of taco_gated_forward for these operands (-1 for a bad
@@ -115,8 +116,9 @@ taco_status taco_gated_backward(const void *da, int64_t ldda, const void *x, int
 int64_t taco_gated_forward_mx_workspace(int64_t rows, int64_t hidden, int64_t features);
 
 /* Forward on codes [.., hidden] and scales [.., hidden / 32] of x and of both
- * weights; hidden is a multiple of 32.  a is of dtype.  Products of codes and
- * scales are exact; the sums are float32. */
+ * weights; hidden is a multiple of 32.  a is of dtype.  The matrix instructions add
+ * the products of codes in groups of eight neighbours, each to within 2^-12 of the
+ * largest product of its group, and the groups in float32. */
 taco_status taco_gated_forward_mx(const uint8_t *x_codes, const uint8_t *x_scales,
                                   const uint8_t *gate_codes, const uint8_t *gate_scales,
                                   const uint8_t *up_codes, const uint8_t *up_scales, int64_t rows,

@@ -41,19 +41,19 @@ extern "C" {
 
 /* Forward.  rstd: [rows] float32 output q, may be NULL. */
 taco_status taco_rms_forward(const void *x, int64_t ldx, const void *residual, int64_t ldr,
-                                  int64_t rows, int64_t hidden, taco_norm_dtype dtype,
-                                  const void *weight, taco_norm_dtype param_dtype, float eps,
-                                  void *y, int64_t ldy, void *total, int64_t ldt, float *rstd,
-                                  hipStream_t stream);
+                             int64_t rows, int64_t hidden, taco_norm_dtype dtype,
+                             const void *weight, taco_norm_dtype param_dtype, float eps,
+                             void *y, int64_t ldy, void *total, int64_t ldt, float *rstd,
+                             hipStream_t stream);
 
 /* Forward into 8 bits: y as codes [rows, hidden] and scales [rows, hidden / 32], the
  * block-scaled form of taco_gated.h, which taco_gated_forward_mx reads; formed
  * from y in float32.  hidden is a multiple of 32 (SHAPE). */
 taco_status taco_rms_mx(const void *x, int64_t ldx, const void *residual, int64_t ldr,
-                             int64_t rows, int64_t hidden, taco_norm_dtype dtype,
-                             const void *weight, taco_norm_dtype param_dtype, float eps,
-                             uint8_t *codes, uint8_t *scales, void *total, int64_t ldt,
-                             hipStream_t stream);
+                        int64_t rows, int64_t hidden, taco_norm_dtype dtype,
+                        const void *weight, taco_norm_dtype param_dtype, float eps,
+                        uint8_t *codes, uint8_t *scales, void *total, int64_t ldt,
+                        hipStream_t stream);
 
 /* Bytes of workspace that taco_rms_backward needs for dweight (0 with rows
  * == 0; -1 for a bad shape).  A call with dweight NULL needs none. */
@@ -62,11 +62,11 @@ int64_t taco_rms_backward_workspace(int64_t rows, int64_t hidden);
 /* Backward from s (x: total as written by the forward pass, or x without a
  * residual) and rstd.  dweight: [hidden] of param_dtype, may be NULL. */
 taco_status taco_rms_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
-                                   const float *rstd, const void *dtotal, int64_t lddt,
-                                   const void *weight, int64_t rows, int64_t hidden,
-                                   taco_norm_dtype dtype, taco_norm_dtype param_dtype, void *dx,
-                                   int64_t lddx, void *dweight, void *workspace,
-                                   int64_t workspace_bytes, hipStream_t stream);
+                              const float *rstd, const void *dtotal, int64_t lddt,
+                              const void *weight, int64_t rows, int64_t hidden,
+                              taco_norm_dtype dtype, taco_norm_dtype param_dtype, void *dx,
+                              int64_t lddx, void *dweight, void *workspace,
+                              int64_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -124,6 +124,21 @@ def backward(da=A, ldda=40, x=2 * A, ldx=64, gate=3 * A, up=4 * A, ldgu=40, wg=5
                                      features, dtype, act, dx, lddx, dg, du, ws, nbytes, 0)
 
 
+def test_sizes_past_a_launch_are_refused():
+    # 2^24 tiles of 128x64 outputs would take 2^32 threads
+    f, b = gated.taco_gated_forward_workspace, gated.taco_gated_backward_workspace
+    rows = 1 << 30
+    assert f(A, 64, A, 64, A, 64, rows, 64, 64) >= 0
+    assert f(A, 64, A, 64, A, 64, 2 * rows, 64, 64) == -1
+    assert f(A, 128, A, 128, A, 128, rows, 128, 64) == -1
+    assert f(A, 64, A, 64, A, 64, rows, 64, 128) == -1
+    assert b(A, 64, A, 64, A, 64, 2 * rows, 64, 64, 1, 1) == -1
+    assert gated.taco_gated_forward_mx_workspace(2 * rows, 64, 64) == -1
+    assert f(A, WIDE, A, WIDE, A, WIDE, 32, WIDE, 65000) >= 0
+    assert f(A, WIDE, A, WIDE, A, WIDE, 32, WIDE, 65536) == -1
+    assert forward(rows=2 * rows, hidden=64, features=64, nbytes=0) == SHAPE
+
+
 def test_backward_refusals():
     assert backward(dtype=F32) == FORMAT
     assert backward(rows=-1) == SHAPE and backward(ldda=39) == SHAPE and backward(ldgu=39) == SHAPE

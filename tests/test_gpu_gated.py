@@ -286,6 +286,27 @@ def test_another_stream(gated):
     assert torch.equal(got_mx, want_mx) and torch.equal(codes, xm[0]) and torch.equal(scales, xm[1])
 
 
+def test_projections_of_different_pitch_on_another_stream(gated):
+    """They are copied to one pitch after the work that is queued there."""
+    announce("pitch, another stream")
+    s = torch.cuda.Stream()
+    x, wg, wu = operands(20, 24, 16, BF, 1)
+    g, u, da = rows_of(20, 16, BF, 2, 1.0, 8), rows_of(20, 16, BF, 3), rows_of(20, 16, BF, 4)
+    want = gated.gated_backward(da, x, g.contiguous(), u, wg, wu)
+    new, old = g.clone(), torch.zeros_like(g)
+    big = torch.ones(4096, 4096, device="cuda")
+    late = torch.as_strided(torch.zeros(20, 24, dtype=BF, device="cuda"), (20, 16), (24, 1))
+    late.copy_(old)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for _ in range(20):
+            big = big @ big * 0.0
+        late.copy_(new)
+    got = gated.gated_backward(da, x, late, u, wg, wu, stream=s)
+    s.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
 def test_graph_replays(gated):
     """Forward, backward and the 8-bit pass in one graph, with split tiles and copies
     of ragged operands; eager calls between the replays."""
