@@ -10,11 +10,18 @@
 // fixed order.  What differs:
 //
 //  * One sum per row, and no mean: sums of squares are joined by adding.
+//  * Few rows have their weight's gradient made by work-groups of its own, in the
+//    same launch as dx.
 //  * y is formed from the float32 sum x + residual; the sum that is written
 //    is that value rounded once.
 //  * 8-bit form: a block of 32 columns is four neighbouring lanes' chunks, so its
 //    maximum takes two DPP steps, and its scale byte is written by the first
 //    of the four.
+//
+// All are bound by HBM, whose copies reach 5.14 TB/s here (reading and writing): forward with
+// residual 16384x3584 bf16 83 us (5.66 TB/s), into 8 bits 8192x2560 27.6 us (5.3), backward
+// 32768x12288 bf16 with dtotal 548 us (5.87); the smallest calls by the launch, 1x2560
+// forward 4.7 us.
 #pragma once
 
 #include "taco_norm_rows.hpp"
@@ -112,13 +119,52 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rms_forward_kernel(RmsFo
 
 // ------------------------------------------------------------ backward ----
 
-template <typename T, int TPR, int NV, bool WHOLE, bool RES>
+// The weight's gradient of 64 columns: eight lanes to a row, rows in turn, and the
+// row groups' sums added in order.
+template <typename T, int THREADS>
+__device__ __forceinline__ void weight_columns(const RmsBackward &a, int col0) {
+    constexpr int GROUPS = THREADS / 8;
+    __shared__ f4v sums[GROUPS][8][2];
+    const int lane = threadIdx.x & 7, group = threadIdx.x >> 3;
+    const int col = col0 + 8 * lane, len = chunk_len(a.hidden, col);
+    const T *const dy = static_cast<const T *>(a.dy);
+    const T *const x = static_cast<const T *>(a.x);
+    float dw[8] = {};
+#pragma unroll 4
+    for (int64_t row = group; row < a.rows; row += GROUPS) {
+        const Raw<T> d = load_chunk<T, false, true>(dy + row * a.lddy + col, dy + row * a.lddy, len);
+        const Raw<T> v = load_chunk<T, false, true>(x + row * a.ldx + col, x + row * a.ldx, len);
+        const float q = a.rstd[row];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[j] = __builtin_fmaf(elem<T>(d, j), elem<T>(v, j) * q, dw[j]);
+    }
+    sums[group][lane][0] = (f4v){dw[0], dw[1], dw[2], dw[3]};
+    sums[group][lane][1] = (f4v){dw[4], dw[5], dw[6], dw[7]};
+    __syncthreads();
+    const int c = threadIdx.x;
+    if (c >= 64 || col0 + c >= a.hidden) return;
+    float s = 0.0f;
+#pragma unroll 8
+    for (int g = 0; g < GROUPS; ++g) s += sums[g][c / 8][c / 4 % 2][c % 4];
+    store_param<T>(a.dweight, a.params_f32, col0 + c, s);
+}
+
+// APART (few rows): the first row_groups work-groups make dx alone, the others the
+// weight's gradient, 64 columns each, from a second look at dy and x, which the
+// caches still hold; no sums to join, so one launch.
+template <typename T, int TPR, int NV, bool WHOLE, bool RES, bool APART>
 __global__ __launch_bounds__(block_threads<TPR>()) void rms_backward_kernel(RmsBackward a) {
     constexpr int RPB = block_threads<TPR>() / TPR;
     constexpr int WPR = TPR / kWave;
+    if constexpr (APART) {
+        if ((int)blockIdx.x >= a.row_groups) {
+            weight_columns<T, block_threads<TPR>()>(a, ((int)blockIdx.x - a.row_groups) * 64);
+            return;
+        }
+    }
     __shared__ float merge[2][WPR > 1 ? WPR : 1];
     // Work-groups of several rows add their threads' column sums here.
-    __shared__ f4v sums[RPB > 1 ? TPR * NV * 2 : 1];
+    __shared__ f4v sums[RPB > 1 && !APART ? TPR * NV * 2 : 1];
     const int t = threadIdx.x % TPR;
     [[maybe_unused]] const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int hidden = a.hidden;
@@ -127,14 +173,15 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rms_backward_kernel(RmsB
     const T *const dt = static_cast<const T *>(a.dtotal);
 
     int len[NV];
-    float w[NV][8], dw[NV][8];
+    float w[NV][8];
+    [[maybe_unused]] float dw[NV][8];
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
         len[c] = chunk_len(hidden, 8 * (c * TPR + t));
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[c][j] = 0.0f;
     }
-    const int64_t stride = (int64_t)gridDim.x * RPB;
+    const int64_t stride = (int64_t)a.row_groups * RPB;
     int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
     // Rows as they are in memory: the current one and the next.
     struct Row {
@@ -163,7 +210,7 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rms_backward_kernel(RmsB
             for (int j = 0; j < 8; ++j) {
                 // (a missing element has dy = 0 and x = 0)
                 const float d = elem<T>(in.dy[c], j), h = elem<T>(in.x[c], j) * q;
-                dw[c][j] = __builtin_fmaf(d, h, dw[c][j]);
+                if constexpr (!APART) dw[c][j] = __builtin_fmaf(d, h, dw[c][j]);
                 dot = __builtin_fmaf(d * w[c][j], h, dot);
             }
         dot = wave_sum<TPR>(dot);
@@ -201,6 +248,7 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rms_backward_kernel(RmsB
         process(held[1], held[0], 1);
     }
 
+    if constexpr (APART) return;
     if (!a.partial) return;
     float *const part = a.partial + (int64_t)blockIdx.x * hidden;
     if constexpr (RPB > 1) {
@@ -373,16 +421,25 @@ struct RmsBackwardLaunch {
     static constexpr int kMaxHeld = sizeof(T) == 4 ? 512 * 24 : 512 * 32;
     RmsBackward a;
     hipStream_t stream;
-    bool whole;
-    int64_t parts;
-    template <int TPR, int NV, bool WHOLE> taco_status go() const {
+    bool whole, apart;
+    template <int TPR, int NV, bool WHOLE, bool APART>
+    taco_status go(const RmsBackward &a, int64_t grid) const {
         const void *fn =
-            a.dtotal ? reinterpret_cast<const void *>(&rms_backward_kernel<T, TPR, NV, WHOLE, true>)
-                     : reinterpret_cast<const void *>(&rms_backward_kernel<T, TPR, NV, WHOLE, false>);
-        return launch(fn, dim3((unsigned)parts), block_threads<TPR>(), stream, a);
+            a.dtotal ? reinterpret_cast<const void *>(&rms_backward_kernel<T, TPR, NV, WHOLE, true, APART>)
+                     : reinterpret_cast<const void *>(&rms_backward_kernel<T, TPR, NV, WHOLE, false, APART>);
+        return launch(fn, dim3((unsigned)grid), block_threads<TPR>(), stream, a);
     }
     template <int TPR, int NV> taco_status run() const {
-        return whole ? go<TPR, NV, true>() : go<TPR, NV, false>();
+        if (!apart)
+            return whole ? go<TPR, NV, true, false>(a, a.row_groups) : go<TPR, NV, false, false>(a, a.row_groups);
+        // (The loads of whole chunks are not to be kept; these are read twice.)
+        const int64_t columns = (a.hidden + 63) / 64;
+        if (a.dx != a.dy) return go<TPR, NV, false, true>(a, a.row_groups + columns);
+        // dx in dy's place: after those who read dy.
+        RmsBackward first = a;
+        first.row_groups = 0;
+        const taco_status st = go<TPR, NV, false, true>(first, columns);
+        return st != TACO_OK ? st : go<TPR, NV, false, true>(a, a.row_groups);
     }
 };
 
@@ -410,9 +467,11 @@ taco_status Rms<K>::forward(const RmsForward &a, hipStream_t stream) {
 }
 
 template <typename K>
-taco_status Rms<K>::backward(const RmsBackward &a, hipStream_t stream) {
+taco_status Rms<K>::backward(const RmsBackward &args, hipStream_t stream) {
     using T = typename K::type;
-    const int64_t parts = backward_parts(a.rows, a.hidden);
+    RmsBackward a = args;
+    const int64_t parts = rms_parts(a.rows, a.hidden);
+    a.row_groups = (int32_t)parts;
     taco_status st;
     if (a.hidden > RmsBackwardLaunch<T>::kMaxHeld) {
         if (a.partial) {
@@ -424,10 +483,13 @@ taco_status Rms<K>::backward(const RmsBackward &a, hipStream_t stream) {
                              : reinterpret_cast<const void *>(&rms_backward_wide_kernel<T, false>),
                     dim3(grid_rows(a.rows, 1, 512)), kWideThreads, stream, a);
     } else {
+        const bool apart = a.partial && rms_apart(a.rows, a.hidden);
+        if (apart) a.row_groups = (int32_t)grid_rows(a.rows, rows_per_group(a.hidden), 256);
         const bool whole = a.hidden % 8 == 0 && on16(a.dy, a.lddy, sizeof(T)) &&
                            on16(a.x, a.ldx, sizeof(T)) && on16(a.dx, a.lddx, sizeof(T)) &&
                            (!a.dtotal || on16(a.dtotal, a.lddt, sizeof(T)));
-        st = for_backward_width(a.hidden, RmsBackwardLaunch<T>{a, stream, whole, parts});
+        st = for_backward_width(a.hidden, RmsBackwardLaunch<T>{a, stream, whole, apart});
+        if (apart) return st;
     }
     if (st != TACO_OK || !a.partial) return st;
     return launch(reinterpret_cast<const void *>(&rms_parts_kernel<T>),

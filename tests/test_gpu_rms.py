@@ -307,6 +307,23 @@ def test_backward_many_rows(norm, rows, hidden):
     assert none is None and torch.equal(only, dx)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,hidden", [(1, 8), (2, 63), (33, 65), (64, 1000), (200, 2567), (255, 130), (256, 4096),
+                                         (257, 4080), (85, 12288), (86, 12288)])
+def test_backward_of_few_rows(norm, rows, hidden, dtype):
+    """Either side of where the weight's gradient is made beside dx, and in dy's
+    place, where it is made before."""
+    announce(f"backward, few rows {rows}x{hidden} {dtype}")
+    x, dy, dt = (rows_of(rows, hidden, dtype, s) for s in (1, 2, 3))
+    rstd, w = (x.float() ** 2).mean(1).add(1e-5).rsqrt(), weight_of(hidden, F32)
+    dx, dw = check_backward(norm, dy, x, rstd, w, dt)
+    into = dy.clone()
+    dx2, dw2 = norm.rms_norm_backward(into, x, rstd, w, dtotal=dt, dx=into)
+    assert torch.equal(dx2, dx) and torch.equal(dw2, dw)
+    only, none = norm.rms_norm_backward(dy, x, rstd, w, dtotal=dt, param_grads=False)
+    assert none is None and torch.equal(only, dx)
+
+
 @pytest.mark.parametrize("rows,hidden", [(1, 40), (64, 128), (1025, 128), (5000, 1000), (300, 17000)])
 def test_weight_gradient_sums_are_exact(norm, rows, hidden):
     announce(f"exact sums {rows}x{hidden}")
