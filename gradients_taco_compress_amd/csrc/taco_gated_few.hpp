@@ -11,8 +11,8 @@
 //    they are waited for; where turns are held ahead, the next round's go out
 //    between the products of this one.
 //
-// Bound by HBM: 1 x 10240x2560 bf16 22.0 us (4.8 TB/s), 4 x 14336x3584 codes
-// 22.5 us (4.7).  Few features fill few CUs, each of which takes about 40 GB/ms
+// Bound by HBM: 1 x 10240x2560 bf16 20.6 to 22.0 us (5.1 to 4.8 TB/s), 4 x 14336x3584
+// codes 23.2 us (4.6).  Few features fill few CUs, each of which takes about 40 GB/ms
 // (1 x 256x8192: 18.7 us).
 #pragma once
 
