@@ -94,16 +94,20 @@ Product sizes(int64_t m, int64_t n, int64_t k) {
 struct ForwardOperands {
     Operand x, gate, up;
     int64_t slab_bytes, bytes;
+    bool few;
 };
 ForwardOperands forward_operands(const void *x, int64_t ldx, const void *gate, int64_t ldg,
                                  const void *up, int64_t ldu, int64_t rows, int64_t hidden,
                                  int64_t features) {
     ForwardOperands o = {operand(x, ldx, rows, hidden), operand(gate, ldg, features, hidden),
-                         operand(up, ldu, features, hidden), 0, 0};
-    if (rows <= kFewRows) return o;
+                         operand(up, ldu, features, hidden), 0, 0, false};
     alike(&o.gate, &o.up);
-    o.slab_bytes = Products<BF16>::workspace(Kind::kForward, sizes(rows, features, hidden));
-    o.bytes = o.slab_bytes + o.x.copy_bytes() + o.gate.copy_bytes() + o.up.copy_bytes();
+    const int64_t copies = o.x.copy_bytes() + o.gate.copy_bytes() + o.up.copy_bytes();
+    const Product p = sizes(rows, features, hidden);
+    o.few = Products<BF16>::few_takes(p, copies);
+    if (o.few) return o;
+    o.slab_bytes = Products<BF16>::workspace(Kind::kForward, p);
+    o.bytes = o.slab_bytes + copies;
     return o;
 }
 
@@ -178,7 +182,7 @@ taco_status taco_gated_forward(const void *x, int64_t ldx, const void *gate_weig
     p.activation = activation;
     p.out[0] = a; p.out[1] = gate; p.out[2] = up;
     p.out_pitch[0] = lda; p.out_pitch[1] = p.out_pitch[2] = ldgu;
-    if (rows <= kFewRows) {
+    if (o.few) {
         p.a[0] = {x, ldx * kSize};
         p.b[0] = {gate_weight, ldg * kSize};
         p.b[1] = {up_weight, ldu * kSize};
@@ -281,8 +285,8 @@ taco_status taco_gated_backward(const void *da, int64_t ldda, const void *x, int
 
 int64_t taco_gated_forward_mx_workspace(int64_t rows, int64_t hidden, int64_t features) {
     if (!valid_mx(rows, hidden, features)) return -1;
-    if (rows <= kFewRows) return 0;
-    Product p = sizes(rows, features, hidden);
+    const Product p = sizes(rows, features, hidden);
+    if (Products<Codes>::few_takes(p, 0)) return 0;
     return Products<Codes>::workspace(Kind::kForward, p) + scale_tile_bytes(rows, hidden / 32) +
            2 * scale_tile_bytes(features, hidden / 32);
 }
@@ -321,7 +325,7 @@ taco_status taco_gated_forward_mx(const uint8_t *x_codes, const uint8_t *x_scale
     p.a_scale = {x_scales, blocks};
     p.b_scale[0] = {gate_scales, blocks};
     p.b_scale[1] = {up_scales, blocks};
-    if (rows <= kFewRows) return Products<Codes>::few(p, stream);
+    if (Products<Codes>::few_takes(p, 0)) return Products<Codes>::few(p, stream);
     Arena arena = {static_cast<char *>(workspace), {}, 0};
     p.slabs = static_cast<float *>(arena.take(Products<Codes>::workspace(Kind::kForward, p)));
     Matrix *const to[] = {&p.a_scale, &p.b_scale[0], &p.b_scale[1]};

@@ -1,19 +1,19 @@
-// Forward pass of the gated block for at most 16 rows (the tokens that a
-// serving step adds): both weights are read once, which is all the time it
-// takes, so they go from memory to the matrix instructions' registers without
-// LDS in between.
+// Forward pass of the gated block for few rows (the tokens that a serving step
+// adds): both weights are read once, which is nearly all the time it takes, so
+// they go from memory to the matrix instructions' registers without LDS in
+// between.
 //
-//  * A wave multiplies the rows by 16 gate and the 16 same up features.  Lane
-//    (g, r) reads chunks of feature r (and of row r of X, which stays in
-//    cache); the waves of a work-group share the summed length and add their
-//    sums in LDS, in order.
+//  * A wave multiplies RF fragments of 16 rows by 16 gate and the 16 same up
+//    features.  Lane (g, r) reads chunks of feature r (and of row r of X, which
+//    stays in cache); the waves of a work-group share the summed length, and
+//    their sums are added in LDS, in order.
 //  * A wave's turn takes 128 bytes of each feature.  All its loads are issued before
 //    they are waited for; where turns are held ahead, the next round's go out
 //    between the products of this one.
 //
 // Bound by HBM: 1 x 10240x2560 bf16 20.6 to 22.0 us (5.1 to 4.8 TB/s), 4 x 14336x3584
-// codes 23.2 us (4.6).  Few features fill few CUs, each of which takes about 40 GB/ms
-// (1 x 256x8192: 18.7 us).
+// codes 23.2 us (4.6); else by what a CU takes in, X's rows among it: 34 GB/ms (codes
+// 25).  Few features fill few CUs (1 x 256x8192: 18.7 us).
 #pragma once
 
 #include <type_traits>
@@ -23,37 +23,44 @@
 namespace taco_gated {
 namespace {
 
-template <typename E, int WAVES, int AHEAD>
+template <typename E, int WAVES, int AHEAD, int RF>
 __global__ __launch_bounds__(WAVES * kWave) void few_kernel(Product p) {
     using El = Element<E>;
     constexpr int SIZE = El::SIZE;
     constexpr bool SCALED = El::SCALED;
-    __shared__ f4v sums[WAVES > 1 ? WAVES - 1 : 1][2][kWave];
+    constexpr int N = 2 + RF;                               // row fragments: gate, up, X
+    static_assert(RF <= WAVES, "a wave to a fragment of X at the end");
+    __shared__ f4v sums[WAVES][2 * RF][kWave];
     const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, r = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int64_t f0 = (int64_t)blockIdx.x * 16;
-    const int64_t f = f0 + r < p.n ? f0 + r : p.n - 1, m = r < p.m ? r : p.m - 1;
+    const int64_t f = f0 + r < p.n ? f0 + r : p.n - 1;
     // Rows of gate, up and X; those past the last are repeated and not stored.
-    const char *const rows[3] = {static_cast<const char *>(p.b[0].p) + f * p.b[0].pitch,
-                                 static_cast<const char *>(p.b[1].p) + f * p.b[1].pitch,
-                                 static_cast<const char *>(p.a[0].p) + m * p.a[0].pitch};
-    [[maybe_unused]] const uint8_t *scales[3] = {};
+    const char *rows[N] = {static_cast<const char *>(p.b[0].p) + f * p.b[0].pitch,
+                           static_cast<const char *>(p.b[1].p) + f * p.b[1].pitch};
+    [[maybe_unused]] const uint8_t *scales[N] = {};
     if constexpr (SCALED) {
         scales[0] = static_cast<const uint8_t *>(p.b_scale[0].p) + f * p.b_scale[0].pitch;
         scales[1] = static_cast<const uint8_t *>(p.b_scale[1].p) + f * p.b_scale[1].pitch;
-        scales[2] = static_cast<const uint8_t *>(p.a_scale.p) + m * p.a_scale.pitch;
+    }
+#pragma unroll
+    for (int i = 0; i < RF; ++i) {
+        const int64_t m = 16 * i + r < p.m ? 16 * i + r : p.m - 1;
+        rows[2 + i] = static_cast<const char *>(p.a[0].p) + m * p.a[0].pitch;
+        if constexpr (SCALED)
+            scales[2 + i] = static_cast<const uint8_t *>(p.a_scale.p) + m * p.a_scale.pitch;
     }
     const int64_t bytes = p.k * SIZE;
     // A K-tile of 128 bytes of each row.
     struct Turn {
-        Fragment v[3];
-        int scale[3];
+        Fragment v[N];
+        int scale[N];
     };
     Turn held[AHEAD];
     auto load = [&](int64_t turn, Turn &to) {
         const int64_t at = turn * kDeep;
 #pragma unroll
-        for (int s = 0; s < 3; ++s) {
+        for (int s = 0; s < N; ++s) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 to.v[s].v[h] = *reinterpret_cast<const u4v_any *>(rows[s] + at + h * 64 + g * 16);
@@ -64,7 +71,7 @@ __global__ __launch_bounds__(WAVES * kWave) void few_kernel(Product p) {
     auto load_rest = [&](int64_t turn, Turn &to) {
         const int64_t at = turn * kDeep;
 #pragma unroll
-        for (int s = 0; s < 3; ++s) {
+        for (int s = 0; s < N; ++s) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int64_t c = at + h * 64 + g * 16, left = bytes - c;
@@ -78,10 +85,15 @@ __global__ __launch_bounds__(WAVES * kWave) void few_kernel(Product p) {
             }
         }
     };
-    f4v gate = {0.0f, 0.0f, 0.0f, 0.0f}, up = gate;
+    f4v gate[RF], up[RF];
+#pragma unroll
+    for (int i = 0; i < RF; ++i) gate[i] = up[i] = (f4v){0.0f, 0.0f, 0.0f, 0.0f};
     auto multiply = [&](const Turn &in) {
-        gate = El::template run<0, 0>(in.v[0], in.v[2], gate, in.scale[0], in.scale[2]);
-        up = El::template run<0, 0>(in.v[1], in.v[2], up, in.scale[1], in.scale[2]);
+#pragma unroll
+        for (int i = 0; i < RF; ++i) {
+            gate[i] = El::template run<0, 0>(in.v[0], in.v[2 + i], gate[i], in.scale[0], in.scale[2 + i]);
+            up[i] = El::template run<0, 0>(in.v[1], in.v[2 + i], up[i], in.scale[1], in.scale[2 + i]);
+        }
     };
     const int64_t turns = bytes / kDeep;
     int64_t turn = wave;
@@ -109,27 +121,28 @@ __global__ __launch_bounds__(WAVES * kWave) void few_kernel(Product p) {
         load_rest(turns, held[0]);
         multiply(held[0]);
     }
-    if constexpr (WAVES > 1) {
-        if (wave > 0) {
-            sums[wave - 1][0][lane] = gate;
-            sums[wave - 1][1][lane] = up;
-        }
-        __syncthreads();
-        if (wave > 0) return;
+    // Wave i adds and finishes fragment i of X.
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w) {
-            gate += sums[w - 1][0][lane];
-            up += sums[w - 1][1][lane];
-        }
+    for (int i = 0; i < RF; ++i) {
+        sums[wave][2 * i][lane] = gate[i];
+        sums[wave][2 * i + 1][lane] = up[i];
+    }
+    __syncthreads();
+    if (wave >= RF) return;
+    f4v all_gate = sums[0][2 * wave][lane], all_up = sums[0][2 * wave + 1][lane];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) {
+        all_gate += sums[w][2 * wave][lane];
+        all_up += sums[w][2 * wave + 1][lane];
     }
     // Lane (g, r): features 4 g + (0..3) of row r.
-    const int64_t first = f0 + 4 * g, left = p.n - first;
-    if (r >= p.m || left <= 0) return;
+    const int64_t first = f0 + 4 * g, left = p.n - first, m = 16 * wave + r;
+    if (m >= p.m || left <= 0) return;
     float vg[4], vu[4], out[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        vg[e] = gate[e];
-        vu[e] = up[e];
+        vg[e] = all_gate[e];
+        vu[e] = all_up[e];
     }
     with_activation(p.activation, [&](auto act) {
 #pragma unroll
@@ -137,10 +150,10 @@ __global__ __launch_bounds__(WAVES * kWave) void few_kernel(Product p) {
     });
     auto store = [&](auto *kind) {
         using T = typename std::remove_pointer<decltype(kind)>::type;
-        store_row<T, 4>(static_cast<T *>(p.out[0]) + r * p.out_pitch[0] + first, out, left);
+        store_row<T, 4>(static_cast<T *>(p.out[0]) + m * p.out_pitch[0] + first, out, left);
         if (p.out[1]) {
-            store_row<T, 4>(static_cast<T *>(p.out[1]) + r * p.out_pitch[1] + first, vg, left);
-            store_row<T, 4>(static_cast<T *>(p.out[2]) + r * p.out_pitch[2] + first, vu, left);
+            store_row<T, 4>(static_cast<T *>(p.out[1]) + m * p.out_pitch[1] + first, vg, left);
+            store_row<T, 4>(static_cast<T *>(p.out[2]) + m * p.out_pitch[2] + first, vu, left);
         }
     };
     if constexpr (SCALED) {
@@ -153,15 +166,47 @@ __global__ __launch_bounds__(WAVES * kWave) void few_kernel(Product p) {
 
 }  // namespace
 
+// The products of up to 16 rows; of up to kFewRows where these few columns a
+// work-group are estimated to take less than tiles and what tiles need: copies of
+// operands that are not on 16-byte rows, scales by K-tile.  In us, this and tiles:
+//     bf16    17 / 32 x 4096x4096     15.9, 18.3 and 23.5, 23.4
+//     bf16    17 / 32 x 10240x2560    30.3, 35.8 and 28.1, 29.0
+//     bf16    64 x 1024x1024          8.6 and 11.6
+//     codes   17 / 64 x 4096x4096     12.2, 19.7 and 22.1, 21.9
+//     codes   64 x 2048x512           4.7 and 8.8
+template <typename E>
+bool Products<E>::few_takes(const Product &p, int64_t copy_bytes) {
+    constexpr int SIZE = Element<E>::SIZE;
+    if (p.m <= 16) return true;
+    if (p.m > kFewRows) return false;
+    // Bytes of a CU's work-groups; rows that are read again and again count half.
+    const int64_t fragments = p.m <= 32 ? 32 : 64, rounds = up(up(p.n, 16), 256);
+    const double in = (double)rounds * (32.0 + 0.5 * (double)(p.m + fragments)) * (double)(p.k * SIZE);
+    const double weights = 2.0 * (double)p.n * (double)(p.k * SIZE) / 5.0e6;
+    const double cu = in / (SIZE == 1 ? 25.0e3 : 34.0e3);
+    const double few_us = 3.0 + (cu > weights ? cu : weights);
+    double tiles_us;
+    const Choice c = choose(Kind::kForward, p, SIZE, &tiles_us);
+    const double join = c.split_tiles ? kJoinUs + 0.015 * (c.plan.items - c.plan.whole) : 0.0;
+    const double read = 4.0 + weights + 0.8 * join;
+    if (read > tiles_us) tiles_us = read;
+    if (SIZE == 1) tiles_us += 4.0;
+    if (copy_bytes) tiles_us += 3.0 + (double)copy_bytes / 2.0e6;
+    return few_us < tiles_us;
+}
+
 template <typename E>
 taco_status Products<E>::few(const Product &p, hipStream_t stream) {
     const dim3 grid((unsigned)up(p.n, 16));
     // Turns held at once: 1, 3 and 4 of 16-bit elements take 22.9, 22.4 and 22.0 us at
     // 1 x 10240x2560, and of codes, whose turn is twice as long in summed elements,
     // 13.5, 16.5 and 16.5 us.  (Four waves 22.2 and 14.1 at their best, sixteen 24.0
-    // and 15.5.)
+    // and 15.5.)  More rows hold one (32 and 64 x 10240x2560: 35.8, 48.1 us; two 35.9, 53.2).
     constexpr int kAhead = Element<E>::SCALED ? 1 : 4;
-    return launch(reinterpret_cast<const void *>(&few_kernel<E, 8, kAhead>), grid, 8 * kWave, stream, p);
+    const void *fn = p.m <= 16   ? reinterpret_cast<const void *>(&few_kernel<E, 8, kAhead, 1>)
+                     : p.m <= 32 ? reinterpret_cast<const void *>(&few_kernel<E, 8, 1, 2>)
+                                 : reinterpret_cast<const void *>(&few_kernel<E, 8, 1, 4>);
+    return launch(fn, grid, 8 * kWave, stream, p);
 }
 
 }  // namespace taco_gated

@@ -53,6 +53,9 @@ template <typename E> struct Products {
     // kInput and kWeight of one backward pass; slabs are input's.
     static int64_t pair_workspace(const Product &input, const Product &weight);
     static taco_status run_pair(const Product &input, Product weight, hipStream_t stream);
+    // Whether few() is to make kForward (p: the sizes), and not run() after copies of
+    // so many bytes.
+    static bool few_takes(const Product &p, int64_t copy_bytes);
     // kForward of at most kFewRows rows; operands at any 2-byte (codes:
     // 16-byte) boundary.
     static taco_status few(const Product &p, hipStream_t stream);
@@ -62,7 +65,7 @@ extern template struct Products<BF16>;
 extern template struct Products<F16>;
 extern template struct Products<Codes>;
 
-constexpr int64_t kFewRows = 16;
+constexpr int64_t kFewRows = 64;
 
 // dG = dA U act'(G), dU = dA act(G) into rows of `to_pitch` elements (a
 // multiple of 8; elements past the last are zero).

@@ -735,12 +735,14 @@ Choice choice_for(Kind kind, const Product &p, int size, const Cost &c, double *
     return r;
 }
 
-inline Choice choose(Kind kind, const Product &p, int size) {
+inline Choice choose(Kind kind, const Product &p, int size, double *us = nullptr) {
     double large_us, small_us, deep_us;
     const Choice large = choice_for<Large>(kind, p, size, kLargeCost, &large_us);
     const Choice small = choice_for<Small>(kind, p, size, kSmallCost, &small_us);
     const Choice deep = choice_for<Deep>(kind, p, size, kDeepCost, &deep_us);
-    if (deep_us <= small_us && deep_us <= large_us) return deep;
+    const double other_us = large_us <= small_us ? large_us : small_us;
+    if (us) *us = deep_us <= other_us ? deep_us : other_us;
+    if (deep_us <= other_us) return deep;
     return large_us <= small_us ? large : small;
 }
 

@@ -33,8 +33,8 @@
  *   - Any alignment of the elements' own size is accepted (codes: 16 bytes).
  *     Operands whose rows do not all start on 16-byte boundaries, or whose
  *     length is no multiple of 8 elements, are first copied to where they do,
- *     which takes their size of workspace and time (few rows excepted: up to
- *     16, forward).
+ *     which takes their size of workspace and time (few rows excepted, forward: up
+ *     to 16, and up to 64 where the library reads them as they are).
  *   - Sums are float32 (matrix instructions; for codes see below); the activation
  *     and its product are formed in float32 from the unrounded sums, and results are rounded once.
  *     dG and dU are rounded to dtype before their products: fp16 gradients need

@@ -63,7 +63,7 @@ def forward(x=A, ldx=64, wg=2 * A, ldg=64, wu=3 * A, ldu=64, rows=32, hidden=64,
                                     lda, gate, up, ldgu, ws, nbytes, 0)
 
 
-@pytest.mark.parametrize("rows", [4, 32])
+@pytest.mark.parametrize("rows", [4, 32, 96])
 def test_forward_refusals(rows):
     def call(**kw):
         return forward(rows=kw.pop("rows", rows), **kw)
@@ -92,26 +92,31 @@ def test_forward_refusals(rows):
 def test_forward_workspace():
     f = gated.taco_gated_forward_workspace
 
-    def need(x=A, ldx=64, wg=2 * A, ldg=64, wu=3 * A, ldu=64, rows=32, hidden=64, features=40):
+    def need(x=A, ldx=64, wg=2 * A, ldg=64, wu=3 * A, ldu=64, rows=96, hidden=64, features=40):
         return f(x, ldx, wg, ldg, wu, ldu, rows, hidden, features)
     assert need() == 0 and need(rows=0) == 0
     assert need(rows=-1) == need(hidden=0) == need(features=0) == need(ldx=63) == -1
     # operands that are not on 16-byte rows are copied; both weights, to one pitch
-    assert need(x=A + 2) == 32 * 128
-    assert need(ldx=65) == 32 * 128
-    assert need(hidden=60) == 32 * 128 + 2 * 40 * 128
+    assert need(x=A + 2) == 96 * 128
+    assert need(ldx=65) == 96 * 128
+    assert need(hidden=60) == 96 * 128 + 2 * 40 * 128
     assert need(wg=2 * A + 2) == 2 * 40 * 128
     assert need(ldg=72) == 2 * 40 * 128
     assert need(ldg=72, ldu=72) == 0
-    assert need(ldx=1 << 23) == 32 * 128                             # too far apart to load in place
-    # few rows read operands as they are
-    assert need(rows=16, x=A + 2, hidden=60, ldg=72) == 0
+    assert need(ldx=1 << 23) == 96 * 128                             # too far apart to load in place
+    # few rows read operands as they are: up to 16, and more where tiles would take longer
+    wide = dict(hidden=16384, features=24, ldx=16384, ldg=16384, ldu=16384)
+    assert need(rows=16, x=A + 2, hidden=60, ldg=72) == 0 and need(rows=16, x=A + 2, **wide) == 0
+    assert need(rows=17, x=A + 2, hidden=60, ldg=72) == need(rows=64, x=A + 2, hidden=60, ldg=72) == 0
+    assert need(rows=65, x=A + 2) == 65 * 128
+    assert need(rows=17, **wide) > 0 and need(rows=64, **wide) > 0   # parts of a split
     # a long sum over few tiles is split
     split = need(ldx=WIDE, ldg=WIDE, ldu=WIDE, hidden=WIDE)
     assert split > 0 and split % (128 * 128 * 4) == 0
-    assert forward(x=A + 2, nbytes=32 * 128 - 1) == PARAM
-    assert forward(x=A + 2, ws=0) == NULL and forward(x=A + 2, ws=7 * A + 8) == ALIGN
-    assert forward(x=A + 2, ws=2 * A) == ALIAS
+    assert forward(rows=96, x=A + 2, nbytes=96 * 128 - 1) == PARAM
+    assert forward(rows=96, x=A + 2, ws=0) == NULL
+    assert forward(rows=96, x=A + 2, ws=7 * A + 8) == ALIGN
+    assert forward(rows=96, x=A + 2, ws=2 * A) == ALIAS
 
 
 def backward(da=A, ldda=40, x=2 * A, ldx=64, gate=3 * A, up=4 * A, ldgu=40, wg=5 * A, ldg=64,
@@ -188,7 +193,7 @@ def forward_mx(xc=A, xs=2 * A, gc=3 * A, gs=4 * A, uc=5 * A, us=6 * A, rows=32, 
                                        lda, ws, nbytes, 0)
 
 
-@pytest.mark.parametrize("rows", [4, 32])
+@pytest.mark.parametrize("rows", [4, 32, 96])
 def test_forward_mx_refusals(rows):
     def call(**kw):
         return forward_mx(rows=kw.pop("rows", rows), **kw)
@@ -208,13 +213,16 @@ def test_forward_mx_refusals(rows):
 
 def test_forward_mx_workspace():
     f = gated.taco_gated_forward_mx_workspace
-    assert f(16, 64, 40) == 0 and f(0, 64, 40) == 0
+    assert f(16, 64, 40) == 0 and f(0, 64, 40) == 0 and f(64, 64, 40) == 0
     # scales by K-tile of 128 codes and 64 rows: 256 bytes each
-    assert f(32, 64, 40) == 256 + 2 * 256
+    assert f(96, 64, 40) == 2 * 256 + 2 * 256
     assert f(65, 160, 130) == 2 * 2 * 256 + 2 * 2 * 3 * 256
+    assert f(64, 16384, 24) > 128 * 3 * 256                          # and parts of a split
     assert f(-1, 64, 40) == f(32, 40, 40) == f(32, 64, 0) == -1
-    assert forward_mx(nbytes=f(32, 64, 40) - 1) == PARAM
-    assert forward_mx(ws=0) == NULL and forward_mx(ws=8 * A + 4) == ALIGN and forward_mx(ws=A) == ALIAS
+    need = f(96, 64, 40)
+    assert forward_mx(rows=96, nbytes=need - 1) == PARAM
+    assert forward_mx(rows=96, ws=0) == NULL and forward_mx(rows=96, ws=8 * A + 4) == ALIGN
+    assert forward_mx(rows=96, ws=A) == ALIAS
 
 
 def encode(x=A, ldx=64, rows=4, hidden=64, dtype=BF16, codes=2 * A, scales=3 * A):

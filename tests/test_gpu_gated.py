@@ -72,6 +72,22 @@ def test_forward(gated, rows, hidden, features, dtype):
     check_forward(gated, *operands(rows, hidden, features, dtype, rows + hidden), kind)
 
 
+# Either side of where up to 64 rows are made without tiles.
+SOME_ROWS = [(17, 40, 33), (32, 1111, 300), (33, 2567, 65), (48, 512, 2048), (64, 8, 5), (64, 1024, 1030), (65, 200, 40),
+             (17, 8192, 256), (33, 16384, 24), (64, 8200, 40), (64, 1000, 9000)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("rows,hidden,features", SOME_ROWS)
+def test_forward_of_some_rows(gated, rows, hidden, features, dtype):
+    announce(f"forward of some rows {rows} {hidden}x{features} {dtype}")
+    check_forward(gated, *operands(rows, hidden, features, dtype, rows), "silu")
+    x, wg, wu = whole(rows, hidden, dtype, 1, 1), whole(features, hidden, dtype, 2, 1), whole(features, hidden, dtype, 3, 1)
+    _, gate, up = gated.gated_forward(x, wg, wu, save=True)
+    for got, w in ((gate, wg), (up, wu)):                           # sums of whole numbers are exact
+        assert torch.equal(got, (x.double() @ w.double().t()).to(dtype))
+
+
 @pytest.mark.parametrize("kind", ACTIVATIONS)
 @pytest.mark.parametrize("rows", [4, 100])
 def test_forward_activations(gated, kind, rows):
@@ -81,7 +97,7 @@ def test_forward_activations(gated, kind, rows):
 
 
 @pytest.mark.parametrize("pitch,offset", [(8, 0), (24, 8), (5, 0), (0, 1), (3, 3), (4, 4)])
-@pytest.mark.parametrize("rows", [3, 70])
+@pytest.mark.parametrize("rows", [3, 30, 64, 70])
 def test_strides(gated, rows, pitch, offset):
     for hidden in (64, 72, 45):
         announce(f"forward strides {rows} {hidden} pitch {pitch} offset {offset}")
@@ -93,7 +109,7 @@ def test_strides(gated, rows, pitch, offset):
             *gated.gated_backward(da, x, g, u, wg, wu, "silu"))
 
 
-@pytest.mark.parametrize("rows", [2, 50])
+@pytest.mark.parametrize("rows", [2, 50, 80])
 def test_weights_of_different_pitch_and_halves_of_one(gated, rows):
     announce("weights of different pitch")
     x = rows_of(rows, 64, BF, 1)
@@ -190,7 +206,7 @@ def test_activation_slopes_far_out(gated, kind):
               torch.tensor([[0.0, 1.0]], device="cuda", dtype=torch.float64), kind).check(a)
 
 
-@pytest.mark.parametrize("rows", [5, 150])
+@pytest.mark.parametrize("rows", [5, 40, 150])
 def test_nan_and_infinities_stay_in_their_rows_and_columns(gated, rows):
     announce(f"nan {rows}")
     x, wg, wu = operands(rows, 72, 70, BF, 1)
@@ -204,7 +220,7 @@ def test_nan_and_infinities_stay_in_their_rows_and_columns(gated, rows):
     assert torch.equal(a[keep], clean[keep])
 
 
-@pytest.mark.parametrize("rows", [9, 140])
+@pytest.mark.parametrize("rows", [9, 24, 60, 140])
 def test_neighbours_are_left_alone(gated, rows):
     """Outputs in wider buffers, NaN around every operand."""
     announce(f"neighbours {rows}")
@@ -384,7 +400,7 @@ def test_every_code_and_scale_is_encoded_as_itself(gated):
     assert scales.flatten().tolist() == list(range(17, 246))
 
 
-MX_SIZES = [(1, 32, 16), (3, 64, 5), (4, 1120, 40), (16, 96, 300), (17, 32, 8), (31, 128, 64),
+MX_SIZES = [(17, 96, 33), (32, 2048, 40), (33, 160, 70), (64, 1024, 130), (1, 32, 16), (3, 64, 5), (4, 1120, 40), (16, 96, 300), (17, 32, 8), (31, 128, 64),
             (64, 160, 129), (130, 512, 65), (200, 1184, 96), (256, 256, 256), (300, 224, 136)]
 
 
@@ -407,7 +423,9 @@ def test_forward_mx(gated, rows, hidden, features, dtype):
 
 
 # Large tiles, split tiles, several items; sums of powers of two are exact.
-@pytest.mark.parametrize("rows,hidden,features", [(2053, 96, 8203), (18, 16384, 24), (300, 24576, 520),
+@pytest.mark.parametrize("rows,hidden,features", [(17, 32, 16), (32, 160, 70), (33, 1120, 130), (64, 4096, 200),
+                                                  (64, 96, 1), (17, 8192, 256), (64, 16384, 24), (64, 992, 9000),
+                                                  (2053, 96, 8203), (18, 16384, 24), (300, 24576, 520),
                                                   (1000, 32, 33000)])
 def test_exact_sums_mx(gated, rows, hidden, features):
     announce(f"exact mx {rows} x {features}x{hidden}")
@@ -423,7 +441,7 @@ def test_exact_sums_mx(gated, rows, hidden, features):
     assert bool(((a.double() - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -16) + 1e-30).all())
 
 
-@pytest.mark.parametrize("rows", [5, 150])
+@pytest.mark.parametrize("rows", [5, 40, 150])
 def test_nan_blocks_in_the_8_bit_pass(gated, rows):
     announce(f"mx nan {rows}")
     x, wg, wu = operands(rows, 160, 70, BF, 1)
