@@ -262,7 +262,18 @@ class _Gated(torch.autograd.Function):
 
 def gated(x, gate_weight, up_weight, activation: str = "silu"):
     """Differentiable ``act(x gate_weight^T) * (x up_weight^T)``.  It keeps x and
-    both projections for its backward pass, nothing without gradients."""
+    both projections for its backward pass, nothing without gradients.
+
+    The tensors are of one type, bf16 or fp16.  Under ``torch.autocast`` they need
+    not be: they are cast to autocast's type, as torch's own linear layer does there,
+    and gradients are in the leaves' types."""
+    auto = torch.get_autocast_dtype("cuda") if torch.is_autocast_enabled("cuda") else None
+    if auto in (torch.bfloat16, torch.float16):
+        for t, name in ((x, "x"), (gate_weight, "gate_weight"), (up_weight, "up_weight")):
+            _device_tensor(t, name)
+            if t.dtype not in DTYPES:
+                raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+        x, gate_weight, up_weight = (t.to(auto) for t in (x, gate_weight, up_weight))
     if not torch.is_grad_enabled():
         return gated_forward(_even(x), _even(gate_weight), _even(up_weight), activation)
     return _Gated.apply(x, gate_weight, up_weight, activation)

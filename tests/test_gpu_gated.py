@@ -523,6 +523,35 @@ def test_autograd_asks_for_what_is_needed(gated):
     assert torch.equal(xt.grad, full[0].grad)
 
 
+@pytest.mark.parametrize("inside", [True, False])
+@pytest.mark.parametrize("auto", [BF, F16])
+@pytest.mark.parametrize("dtype,leaf", [(F32, F32), (BF, F32), (BF, BF), (F16, BF)])
+def test_autograd_under_autocast(gated, dtype, leaf, auto, inside):
+    """In autocast's type, gradients in the leaves'."""
+    announce(f"autocast {dtype} {leaf} under {auto}, backward {'inside' if inside else 'outside'}")
+    x, wg, wu = operands(30, 40, 24, F32, 2)
+    leaves = [x.to(dtype).requires_grad_(), wg.to(leaf).requires_grad_(), wu.to(leaf).requires_grad_()]
+    da = rows_of(30, 24, auto, 8)
+    with torch.autocast("cuda", dtype=auto):
+        a = gated.gated(*leaves)
+        if inside:
+            got = torch.autograd.grad(a, leaves, da)
+    if not inside:
+        got = torch.autograd.grad(a, leaves, da)
+    cast = [t.detach().to(auto) for t in leaves]
+    want, gate, up = gated.gated_forward(*cast, save=True)
+    assert a.dtype == auto and torch.equal(a, want)
+    for g, t, w in zip(got, leaves, gated.gated_backward(da, cast[0], gate, up, *cast[1:])):
+        assert g.dtype == t.dtype and torch.equal(g, w.to(t.dtype))
+    with torch.autocast("cuda", dtype=auto), torch.no_grad():
+        assert torch.equal(gated.gated(*leaves), want)
+    if dtype != leaf or dtype == F32:
+        with pytest.raises(TypeError):
+            gated.gated(*leaves)
+    with torch.autocast("cuda", dtype=auto), pytest.raises(TypeError, match="x must be"):
+        gated.gated(x.double(), *leaves[1:])
+
+
 # ---------------------------------------------------------------- refusals --
 
 def test_refusals(gated):
