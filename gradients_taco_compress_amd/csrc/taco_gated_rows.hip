@@ -35,68 +35,65 @@ __device__ __forceinline__ void load8(const T *p, const T *row, int n, float *f)
                f);
 }
 
-// Work-groups of a kernel that share rows: this one is `at` of `of` along the rows,
-// and `col` of `cols` along the columns; 2^lanes_log2 threads to a row.
+// Work-group `at` of `of` that share the chunks of some rows.
 struct Part {
     int64_t at, of;
-    int col, cols, lanes_log2;
 };
+// f(row, chunk) for this thread's chunks, one after the other along the rows: every
+// thread has one, whatever a row's length.
+template <typename F>
+__device__ __forceinline__ void for_chunks(const Part &part, int64_t rows, int chunks, F &&f) {
+    for (int64_t block = part.at; block * 256 < rows * chunks; block += part.of) {
+        const int64_t first = block * 256 / chunks;
+        const uint32_t at = (uint32_t)(block * 256 - first * chunks) + threadIdx.x;
+        const uint32_t more = at / (uint32_t)chunks;
+        const int64_t row = first + more;
+        if (row < rows) f(row, (int)(at - more * (uint32_t)chunks));
+    }
+}
 
 // A thread to eight neighbours.
 template <typename T, int ACT>
 __device__ __forceinline__ void activation_grad_rows(const ActivationGrad &a, const Part &part) {
-    const int lanes = 1 << part.lanes_log2, lane = threadIdx.x & (lanes - 1), per = 256 >> part.lanes_log2;
-    const int chunks = (int)(a.to_pitch / 8);
-    for (int64_t row = part.at * per + (threadIdx.x >> part.lanes_log2); row < a.rows;
-         row += part.of * per) {
+    for_chunks(part, a.rows, (int)(a.to_pitch / 8), [&](int64_t row, int c) {
         const T *const da = static_cast<const T *>(a.da) + row * a.ldda;
         const T *const gate = static_cast<const T *>(a.gate) + row * a.ldgu;
         const T *const up = static_cast<const T *>(a.up) + row * a.ldgu;
-        T *const dgate = static_cast<T *>(a.dgate) + row * a.to_pitch;
-        T *const dup = static_cast<T *>(a.dup) + row * a.to_pitch;
-        for (int c = part.col * lanes + lane; c < chunks; c += part.cols * lanes) {
-            const int n = a.features - 8 * c;
-            float d[8], g[8], u[8], dg[8], du[8];
-            load8<T>(da + 8 * c, da, n, d);
-            load8<T>(gate + 8 * c, gate, n, g);
-            load8<T>(up + 8 * c, up, n, u);
+        const int n = a.features - 8 * c;
+        float d[8], g[8], u[8], dg[8], du[8];
+        load8<T>(da + 8 * c, da, n, d);
+        load8<T>(gate + 8 * c, gate, n, g);
+        load8<T>(up + 8 * c, up, n, u);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float share = gate_share<ACT>(g[j]);
-                dg[j] = d[j] * u[j] * gate_slope<ACT>(g[j], share);
-                du[j] = d[j] * (g[j] * share);
-                if (j >= n) dg[j] = du[j] = 0.0f;
-            }
-            *reinterpret_cast<u4v *>(dgate + 8 * c) = pack8<T>(dg);
-            *reinterpret_cast<u4v *>(dup + 8 * c) = pack8<T>(du);
+        for (int j = 0; j < 8; ++j) {
+            const float share = gate_share<ACT>(g[j]);
+            dg[j] = d[j] * u[j] * gate_slope<ACT>(g[j], share);
+            du[j] = d[j] * (g[j] * share);
+            if (j >= n) dg[j] = du[j] = 0.0f;
         }
-    }
+        *reinterpret_cast<u4v *>(static_cast<T *>(a.dgate) + row * a.to_pitch + 8 * c) = pack8<T>(dg);
+        *reinterpret_cast<u4v *>(static_cast<T *>(a.dup) + row * a.to_pitch + 8 * c) = pack8<T>(du);
+    });
 }
 
 __device__ __forceinline__ void repack_rows(const Repack &r, const Part &part) {
-    const int lanes = 1 << part.lanes_log2, lane = threadIdx.x & (lanes - 1), per = 256 >> part.lanes_log2;
-    for (int64_t row = part.at * per + (threadIdx.x >> part.lanes_log2); row < r.rows;
-         row += part.of * per) {
-        const char *from = static_cast<const char *>(r.from) + row * r.from_pitch;
-        char *to = static_cast<char *>(r.to) + row * r.to_pitch;
-        for (int64_t at = lane * 16; at < r.to_pitch; at += lanes * 16) {
-            const int64_t n = r.width - at;
-            *reinterpret_cast<u4v *>(to + at) =
-                n > 0 ? load_tail<true>(from + at, from, n < 16 ? (int)n : 16) : (u4v){0u, 0u, 0u, 0u};
-        }
-    }
+    for_chunks(part, r.rows, (int)(r.to_pitch / 16), [&](int64_t row, int c) {
+        const char *const from = static_cast<const char *>(r.from) + row * r.from_pitch;
+        const int64_t at = 16 * (int64_t)c, n = r.width - at;
+        *reinterpret_cast<u4v *>(static_cast<char *>(r.to) + row * r.to_pitch + at) =
+            n > 0 ? load_tail<true>(from + at, from, n < 16 ? (int)n : 16) : (u4v){0u, 0u, 0u, 0u};
+    });
 }
 
 struct Copies {
     Repack r[3];
-    int32_t lanes_log2[3], groups[3];
+    int32_t groups[3];
 };
 // Work-group b of those that all copies take, one after the other.
 __device__ __forceinline__ Part part_of_copies(const Copies &all, int b, int *which) {
     const int second = all.groups[0], third = second + all.groups[1];
     *which = (b >= second) + (b >= third);
-    return {b - (b >= third ? third : b >= second ? second : 0), all.groups[*which], 0, 1,
-            all.lanes_log2[*which]};
+    return {b - (b >= third ? third : b >= second ? second : 0), all.groups[*which]};
 }
 __global__ __launch_bounds__(256) void repack_kernel(Copies all) {
     int which;
@@ -107,14 +104,13 @@ __global__ __launch_bounds__(256) void repack_kernel(Copies all) {
 // The gradients of the activations, and the copies that the products after them need,
 // in one launch.
 template <typename T, int ACT>
-__global__ __launch_bounds__(256) void activation_grad_kernel(ActivationGrad a, int groups, int cols,
-                                                              int lanes_log2, Copies copies) {
+__global__ __launch_bounds__(256) void activation_grad_kernel(ActivationGrad a, int groups, Copies copies) {
     const int b = (int)blockIdx.x;
-    if (b < groups * cols) {
-        activation_grad_rows<T, ACT>(a, {b % groups, groups, b / groups, cols, lanes_log2});
+    if (b < groups) {
+        activation_grad_rows<T, ACT>(a, {b, groups});
     } else {
         int which;
-        const Part part = part_of_copies(copies, b - groups * cols, &which);
+        const Part part = part_of_copies(copies, b - groups, &which);
         repack_rows(copies.r[which], part);
     }
 }
@@ -201,11 +197,7 @@ Copies copies_of(const Repack *r, int count, int64_t *groups) {
     *groups = 0;
     for (int i = 0; i < count; ++i) {
         all.r[i] = r[i];
-        int log2 = 0;
-        while (log2 < 8 && (INT64_C(16) << log2) < r[i].to_pitch) ++log2;
-        all.lanes_log2[i] = log2;
-        const int64_t per = 256 >> log2;
-        all.groups[i] = (int32_t)groups_of((r[i].rows + per - 1) / per, 2048);
+        all.groups[i] = (int32_t)groups_of((r[i].rows * (r[i].to_pitch / 16) + 255) / 256, 1 << 16);
         *groups += all.groups[i];
     }
     return all;
@@ -214,12 +206,7 @@ Copies copies_of(const Repack *r, int count, int64_t *groups) {
 
 taco_status activation_grad(const ActivationGrad &a, bool f16, const Repack *r, int count,
                             hipStream_t stream) {
-    const int64_t chunks = a.to_pitch / 8;
-    int log2 = 0;
-    while (log2 < 8 && (INT64_C(1) << log2) < chunks) ++log2;
-    const int64_t per = 256 >> log2;
-    const int groups = (int)groups_of((a.rows + per - 1) / per, 8192);
-    const int cols = (int)groups_of((chunks + 255) / 256, 64);
+    const int groups = (int)groups_of((a.rows * (a.to_pitch / 8) + 255) / 256, 1 << 17);
     int64_t more;
     const Copies copies = copies_of(r, count, &more);
     const void *fn = nullptr;
@@ -236,8 +223,7 @@ taco_status activation_grad(const ActivationGrad &a, bool f16, const Repack *r, 
             fn = f16 ? reinterpret_cast<const void *>(&activation_grad_kernel<_Float16, TACO_GATED_GELU_TANH>)
                      : reinterpret_cast<const void *>(&activation_grad_kernel<__bf16, TACO_GATED_GELU_TANH>);
     }
-    return launch(fn, dim3((unsigned)((int64_t)groups * cols + more)), 256, stream, a, groups, cols, log2,
-                  copies);
+    return launch(fn, dim3((unsigned)(groups + more)), 256, stream, a, groups, copies);
 }
 
 taco_status repack(const Repack *r, int count, hipStream_t stream) {
