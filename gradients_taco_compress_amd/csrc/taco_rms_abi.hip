@@ -111,7 +111,7 @@ taco_status taco_rms_mx(const void *x, int64_t ldx, const void *residual, int64_
 
 int64_t taco_rms_backward_workspace(int64_t rows, int64_t hidden) {
     if (!valid_hidden(hidden) || !valid_rows(rows, hidden, hidden)) return -1;
-    return rows == 0 ? 0 : rms_parts(rows, hidden) * hidden * (int64_t)sizeof(float);
+    return rows == 0 ? 0 : rms_sums(rows, hidden) * hidden * (int64_t)sizeof(float);
 }
 
 taco_status taco_rms_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,

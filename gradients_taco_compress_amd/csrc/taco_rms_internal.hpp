@@ -30,6 +30,7 @@ struct RmsBackward {
     int32_t hidden;
     int32_t params_f32;
     int32_t row_groups;            // work-groups that walk over rows
+    int32_t segments;              // of the rows, for the weight's gradient apart (0: not apart)
 };
 // Partial sums that the weight's gradient is made of, one per work-group: rows of the
 // workspace, [hidden] float32.  As many as layer norm's, but 512 already from 2048 turns
@@ -45,14 +46,27 @@ inline int64_t rms_parts(int64_t rows, int64_t hidden) {
     return backward_parts(rows, hidden);
 }
 
-// Whether the weight's gradient is made beside dx instead, from a second look at the
-// rows: one launch, where the work-groups of 64 columns do not take longer than what
-// they save.  Parts and this, with dtotal, in a graph:
-//     bf16     1 / 64 / 256 x 2560     5.2, 6.4, 7.0 and 3.0, 3.3, 6.4 us
-//     float32  1 / 64 / 256 x 2560     5.0, 6.3, 7.7 and 2.9, 3.2, 8.0 us
-//     bf16     64 / 256 x 12288        9.1, 14.7 and 4.9, 19.6 us
-//     bf16     512 x 2560              10.4 and 12.1 us
-inline bool rms_apart(int64_t rows, int64_t hidden) { return rows <= 256 && rows * hidden <= 1 << 20; }
+// Segments of the rows whose weight gradients are made beside dx, from a second look at
+// the rows (0: not so, but as parts).  One segment leaves nothing to join: one launch
+// instead of two, up to 128 rows; several are a second launch too, but narrow rows finish
+// sooner.  With dtotal, in a graph, in us, parts and this:
+//     bf16     64 / 128 x 2567      7.5, 9.3 and 4.4, 6.1
+//     bf16     64 / 128 x 12288     10.3, 13.1 and 5.9, 8.2
+//     float32  64 / 128 x 2567      7.6, 10.1 and 4.8, 8.0
+//     float32  256 x 2567           10.5 and 15.9 in one segment, 11.3 in four (as parts)
+//     bf16     256 / 512 x 1024     7.2, 8.6 and 5.0, 5.7; 777 x 1024 9.8 and 10.5 (as parts)
+//     float32  256 / 512 x 1024     7.8, 10.0 and 5.6, 6.5
+//     bf16     512 / 2048 x 128     6.2, 8.0 and 4.8, 5.9
+inline int32_t rms_segments(int64_t rows, int64_t hidden) {
+    if (rows <= 128) return 1;
+    if (hidden <= 128 && rows <= 2048) return 16;
+    return hidden <= 1024 && rows <= 512 ? 8 : 0;
+}
+// Rows of the workspace.
+inline int64_t rms_sums(int64_t rows, int64_t hidden) {
+    const int64_t parts = rms_parts(rows, hidden), segments = rms_segments(rows, hidden);
+    return parts > segments ? parts : segments;
+}
 
 template <typename K>
 struct Rms {

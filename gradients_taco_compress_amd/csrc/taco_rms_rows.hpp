@@ -119,19 +119,21 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rms_forward_kernel(RmsFo
 
 // ------------------------------------------------------------ backward ----
 
-// The weight's gradient of 64 columns: eight lanes to a row, rows in turn, and the
-// row groups' sums added in order.
+// The weight's gradient of 64 columns over segment `segment` of the rows: eight lanes
+// to a row, rows in turn, and the row groups' sums added in order.
 template <typename T, int THREADS>
-__device__ __forceinline__ void weight_columns(const RmsBackward &a, int col0) {
+__device__ __forceinline__ void weight_columns(const RmsBackward &a, int col0, int segment) {
     constexpr int GROUPS = THREADS / 8;
     __shared__ f4v sums[GROUPS][8][2];
+    const int64_t per = (a.rows + a.segments - 1) / a.segments, begin = segment * per;
+    const int64_t end = begin + per < a.rows ? begin + per : a.rows;
     const int lane = threadIdx.x & 7, group = threadIdx.x >> 3;
     const int col = col0 + 8 * lane, len = chunk_len(a.hidden, col);
     const T *const dy = static_cast<const T *>(a.dy);
     const T *const x = static_cast<const T *>(a.x);
     float dw[8] = {};
 #pragma unroll 4
-    for (int64_t row = group; row < a.rows; row += GROUPS) {
+    for (int64_t row = begin + group; row < end; row += GROUPS) {
         const Raw<T> d = load_chunk<T, false, true>(dy + row * a.lddy + col, dy + row * a.lddy, len);
         const Raw<T> v = load_chunk<T, false, true>(x + row * a.ldx + col, x + row * a.ldx, len);
         const float q = a.rstd[row];
@@ -146,19 +148,21 @@ __device__ __forceinline__ void weight_columns(const RmsBackward &a, int col0) {
     float s = 0.0f;
 #pragma unroll 8
     for (int g = 0; g < GROUPS; ++g) s += sums[g][c / 8][c / 4 % 2][c % 4];
-    store_param<T>(a.dweight, a.params_f32, col0 + c, s);
+    if (a.segments == 1) store_param<T>(a.dweight, a.params_f32, col0 + c, s);
+    else a.partial[(int64_t)segment * a.hidden + col0 + c] = s;
 }
 
 // APART (few rows): the first row_groups work-groups make dx alone, the others the
-// weight's gradient, 64 columns each, from a second look at dy and x, which the
-// caches still hold; no sums to join, so one launch.
+// weight's gradient, 64 columns of a segment of the rows each, from a second look at dy
+// and x, which the caches still hold.  One segment leaves no sums to join: one launch.
 template <typename T, int TPR, int NV, bool WHOLE, bool RES, bool APART>
 __global__ __launch_bounds__(block_threads<TPR>()) void rms_backward_kernel(RmsBackward a) {
     constexpr int RPB = block_threads<TPR>() / TPR;
     constexpr int WPR = TPR / kWave;
     if constexpr (APART) {
         if ((int)blockIdx.x >= a.row_groups) {
-            weight_columns<T, block_threads<TPR>()>(a, ((int)blockIdx.x - a.row_groups) * 64);
+            const int b = (int)blockIdx.x - a.row_groups, columns = (a.hidden + 63) / 64;
+            weight_columns<T, block_threads<TPR>()>(a, b % columns * 64, b / columns);
             return;
         }
     }
@@ -433,7 +437,7 @@ struct RmsBackwardLaunch {
         if (!apart)
             return whole ? go<TPR, NV, true, false>(a, a.row_groups) : go<TPR, NV, false, false>(a, a.row_groups);
         // (The loads of whole chunks are not to be kept; these are read twice.)
-        const int64_t columns = (a.hidden + 63) / 64;
+        const int64_t columns = (a.hidden + 63) / 64 * a.segments;
         if (a.dx != a.dy) return go<TPR, NV, false, true>(a, a.row_groups + columns);
         // dx in dy's place: after those who read dy.
         RmsBackward first = a;
@@ -483,18 +487,20 @@ taco_status Rms<K>::backward(const RmsBackward &args, hipStream_t stream) {
                              : reinterpret_cast<const void *>(&rms_backward_wide_kernel<T, false>),
                     dim3(grid_rows(a.rows, 1, 512)), kWideThreads, stream, a);
     } else {
-        const bool apart = a.partial && rms_apart(a.rows, a.hidden);
-        if (apart) a.row_groups = (int32_t)grid_rows(a.rows, rows_per_group(a.hidden), 256);
+        a.segments = rms_segments(a.rows, a.hidden);
+        const bool apart = a.partial && a.segments > 0;
+        if (apart) a.row_groups = (int32_t)grid_rows(a.rows, rows_per_group(a.hidden), 2048);
         const bool whole = a.hidden % 8 == 0 && on16(a.dy, a.lddy, sizeof(T)) &&
                            on16(a.x, a.ldx, sizeof(T)) && on16(a.dx, a.lddx, sizeof(T)) &&
                            (!a.dtotal || on16(a.dtotal, a.lddt, sizeof(T)));
         st = for_backward_width(a.hidden, RmsBackwardLaunch<T>{a, stream, whole, apart});
-        if (apart) return st;
+        if (apart && a.segments == 1) return st;
     }
     if (st != TACO_OK || !a.partial) return st;
     return launch(reinterpret_cast<const void *>(&rms_parts_kernel<T>),
                   dim3((unsigned)((a.hidden + kWave - 1) / kWave)), kSumThreads, stream,
-                  static_cast<const float *>(a.partial), (int)parts, a.hidden, a.dweight, a.params_f32);
+                  static_cast<const float *>(a.partial), (int)(a.segments > 0 ? a.segments : parts), a.hidden,
+                  a.dweight, a.params_f32);
 }
 
 }  // namespace taco_norm

@@ -309,7 +309,9 @@ def test_backward_many_rows(norm, rows, hidden):
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("rows,hidden", [(1, 8), (2, 63), (33, 65), (64, 1000), (200, 2567), (255, 130), (256, 4096),
-                                         (257, 4080), (85, 12288), (86, 12288)])
+                                         (257, 4080), (85, 12288), (86, 12288), (128, 1025), (129, 8), (129, 100), (129, 1024),
+                                         (130, 1025), (511, 136), (512, 1000), (513, 1000), (2048, 128), (2048, 129),
+                                         (2049, 128)])
 def test_backward_of_few_rows(norm, rows, hidden, dtype):
     """Either side of where the weight's gradient is made beside dx, and in dy's
     place, where it is made before."""

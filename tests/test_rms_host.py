@@ -131,6 +131,7 @@ def test_backward_workspace():
     f = norm.taco_rms_backward_workspace
     assert f(0, 64) == 0
     assert f(-1, 64) == f(4, 0) == f(4, 1048577) == f(1 << 47, 1 << 10) == -1
+    assert f(129, 64) == 16 * 64 * 4                          # sixteen segments of the rows
     assert f(1, 2560) == 2560 * 4 and f(1 << 20, 2560) == 512 * 2560 * 4
 
 
