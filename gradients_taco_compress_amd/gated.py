@@ -266,7 +266,10 @@ def gated(x, gate_weight, up_weight, activation: str = "silu"):
 
     The tensors are of one type, bf16 or fp16.  Under ``torch.autocast`` they need
     not be: they are cast to autocast's type, as torch's own linear layer does there,
-    and gradients are in the leaves' types."""
+    and gradients are in the leaves' types.
+
+    A backward pass may be captured into a graph once no eager graph of the same
+    leaves is alive (torch's rule for all of its functions)."""
     auto = torch.get_autocast_dtype("cuda") if torch.is_autocast_enabled("cuda") else None
     if auto in (torch.bfloat16, torch.float16):
         for t, name in ((x, "x"), (gate_weight, "gate_weight"), (up_weight, "up_weight")):

@@ -624,7 +624,11 @@ def norm(x, weight=None, bias=None, eps: float = 1e-5):
 
 def rms(x, weight=None, eps: float = 1e-5, residual=None):
     """Differentiable root-mean-square norm over the last dimension: y, or with
-    a residual (y, x + residual)."""
+    a residual (y, x + residual).  For its backward pass it keeps the sum (x without a
+    residual) and one float32 per row.
+
+    A backward pass may be captured into a graph once no eager graph of the same
+    leaves is alive (torch's rule for all of its functions)."""
     if residual is None:
         return _Rms.apply(x, weight, eps)
     return _RmsResidual.apply(x, residual, weight, eps)
