@@ -569,6 +569,8 @@ class _RmsResidual(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy, dtotal):
+        if dy is None and dtotal is None:    # neither output was given a gradient
+            return None, None, None, None
         total, rstd, weight = ctx.saved_tensors
         need = ctx.needs_input_grad
         if dy is None:                       # y was not used

@@ -1,0 +1,52 @@
+"""Autograd through norm.rms and gated.gated where graphs are unusual: outputs whose
+gradient is undefined.  Every case prints its name before it touches the GPU."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from gated_reference import BF
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def norm():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import gradients_taco_compress_amd.norm as norm
+    return norm
+
+
+def announce(msg):
+    print(f"[case] {msg}", flush=True)
+
+
+def leaves(*shapes):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    return [torch.empty(s, device="cuda").normal_(generator=g).to(BF).requires_grad_() for s in shapes]
+
+
+class Untouched(torch.autograd.Function):
+    """Passes a value on and no gradient back."""
+
+    @staticmethod
+    def forward(ctx, y):
+        return y.clone()
+
+    @staticmethod
+    def backward(ctx, dy):
+        return None
+
+
+def test_outputs_without_gradients(norm):
+    announce("rms, undefined gradients")
+    x, r, w = leaves((5, 72), (5, 72), (72,))
+    y, total = norm.rms(x, w, residual=r)
+    (Untouched.apply(y).sum() + (x * 2).sum()).backward()
+    assert torch.equal(x.grad, torch.full_like(x, 2.0)) and r.grad is None and w.grad is None
+    x.grad = None
+    y, total = norm.rms(x, w, residual=r)
+    (Untouched.apply(y).sum() + (total * 3).sum()).backward()
+    assert torch.equal(x.grad, torch.full_like(x, 3.0)) and torch.equal(r.grad, x.grad)
+    assert w.grad is None or not bool(w.grad.any())
