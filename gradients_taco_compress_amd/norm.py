@@ -574,15 +574,19 @@ class _RmsResidual(torch.autograd.Function):
         total, rstd, weight = ctx.saved_tensors
         need = ctx.needs_input_grad
         if dy is None:                       # y was not used
+            # (dtotal may be the caller's, and other gradients' too: handed on as it is,
+            # or copied, but not as a view, which autograd would take for new memory)
             dx, dw = dtotal, torch.zeros_like(weight) if need[2] else None
+            if need[1] and dx.shape != ctx.residual_shape:
+                return dx if need[0] else None, dx.reshape(ctx.residual_shape).clone(), dw, None
         else:
             dtotal = None if dtotal is None else _even(dtotal)
             dx, dw = rms_norm_backward(_even(dy), total, rstd, weight, dtotal=dtotal,
                                        param_grads=need[2])
             dw = dw.view(weight.shape) if need[2] else None
         # (the residual has x's rows, not always its leading dimensions)
-        return (dx if need[0] else None, dx.reshape(ctx.residual_shape) if need[1] else None,
-                dw, None)
+        dr = dx if dx.shape == ctx.residual_shape else dx.reshape(ctx.residual_shape)
+        return dx if need[0] else None, dr if need[1] else None, dw, None
 
 
 class _NormLinear(torch.autograd.Function):

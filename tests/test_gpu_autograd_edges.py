@@ -50,3 +50,19 @@ def test_outputs_without_gradients(norm):
     (Untouched.apply(y).sum() + (total * 3).sum()).backward()
     assert torch.equal(x.grad, torch.full_like(x, 3.0)) and torch.equal(r.grad, x.grad)
     assert w.grad is None or not bool(w.grad.any())
+
+
+@pytest.mark.parametrize("shape", [(5, 72), (1, 5, 72)])
+def test_gradients_have_memory_of_their_own(norm, shape):
+    announce(f"rms, the gradients' memory, residual {list(shape)}")
+    x, r, w = leaves((5, 72), shape, (72,))
+    one = torch.ones(5, 72, device="cuda", dtype=BF)
+    for turn in (1.0, 2.0):
+        norm.rms(x, w, residual=r)[1].backward(one)
+        assert bool((one == 1).all()) and bool((x.grad == turn).all()) and bool((r.grad == turn).all())
+    assert len({t.untyped_storage().data_ptr() for t in (x.grad, r.grad, one)}) == 3
+    x.grad = r.grad = None
+    torch.autograd.backward(norm.rms(x, w, residual=r), (one, one))
+    want = x.grad.clone()
+    r.grad.zero_()
+    assert torch.equal(x.grad, want) and bool(want.any())

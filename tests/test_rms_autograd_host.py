@@ -57,3 +57,33 @@ def test_outputs_without_gradients(rms):
     (Untouched.apply(y).sum() + (total * 3).sum()).backward()   # the sum alone
     assert torch.equal(x.grad, torch.full_like(x, 3.0)) and torch.equal(r.grad, x.grad)
     assert w.grad is None or not bool(w.grad.any())
+
+
+@pytest.mark.parametrize("shape", [(3, 8), (1, 3, 8)])
+def test_gradients_have_memory_of_their_own(rms, shape):
+    """Where y is not used the sum's gradient is that of x and of the residual: three
+    gradients that a caller may each add to."""
+    x, r, w = leaves((3, 8), shape, (8,))
+    one = torch.ones(3, 8, dtype=torch.float64)
+    rms(x, w, residual=r)[1].backward(one)
+    places = [t.untyped_storage().data_ptr() for t in (x.grad, r.grad, one)]
+    assert len(set(places)) == 3
+    rms(x, w, residual=r)[1].backward(one)                      # adds to both in place
+    assert bool((one == 1).all()) and bool((x.grad == 2).all()) and bool((r.grad == 2).all())
+    assert r.grad.shape == r.shape
+    # through another addition, whose other side receives the same gradient
+    x, r, w, z = leaves((3, 8), shape, (8,), (3, 8))
+    (rms(x, w, residual=r)[1] + z).backward(one)
+    for t in (x, r, z):
+        t.grad.add_(1)
+    assert all(bool((t.grad == 2).all()) for t in (x, r, z)) and bool((one == 1).all())
+    # the residual alone
+    x, r, w = leaves((3, 8), shape, (8,))
+    rms(x.detach(), w.detach(), residual=r)[1].backward(one)
+    assert r.grad.untyped_storage().data_ptr() != one.untyped_storage().data_ptr()
+    # both outputs
+    x, r, w = leaves((3, 8), shape, (8,))
+    torch.autograd.backward(rms(x, w, residual=r), (one, one))
+    r.grad.zero_()
+    assert x.grad.untyped_storage().data_ptr() != r.grad.untyped_storage().data_ptr()
+    assert bool(x.grad.any())
