@@ -25,6 +25,7 @@ import ctypes
 import os
 
 import torch
+from torch.autograd import forward_ad
 
 from . import TacoError  # noqa: F401  (torch's HIP runtime is loaded first)
 from .norm import DTYPES, _check, _device_tensor, _even, _Launch, _pitch, _ptr, _same_rows
@@ -260,6 +261,15 @@ class _Gated(torch.autograd.Function):
         return dx, dg if need[1] else None, du if need[2] else None, None
 
 
+def _tangents(*tensors):
+    """Whether a tensor carries a tangent (forward-mode differentiation, which
+    torch.no_grad does not turn off, and which autograd refuses for the block)."""
+    if getattr(forward_ad, "_current_level", 0) < 0:       # none is open: the usual case
+        return False
+    return any(isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None
+               for t in tensors)
+
+
 def gated(x, gate_weight, up_weight, activation: str = "silu"):
     """Differentiable ``act(x gate_weight^T) * (x up_weight^T)``.  It keeps x and
     both projections for its backward pass, nothing without gradients.
@@ -277,6 +287,6 @@ def gated(x, gate_weight, up_weight, activation: str = "silu"):
             if t.dtype not in DTYPES:
                 raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
         x, gate_weight, up_weight = (t.to(auto) for t in (x, gate_weight, up_weight))
-    if not torch.is_grad_enabled():
+    if not torch.is_grad_enabled() and not _tangents(x, gate_weight, up_weight):
         return gated_forward(_even(x), _even(gate_weight), _even(up_weight), activation)
     return _Gated.apply(x, gate_weight, up_weight, activation)

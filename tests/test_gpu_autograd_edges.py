@@ -1,5 +1,6 @@
-"""Autograd through norm.rms and gated.gated where graphs are unusual: outputs whose
-gradient is undefined.  Every case prints its name before it touches the GPU."""
+"""Autograd through norm.rms and gated.gated in unusual graphs: outputs whose
+gradient is undefined, gradients that are added to, tangents.  Every case prints its
+name before it touches the GPU."""
 from __future__ import annotations
 
 import pytest
@@ -66,3 +67,20 @@ def test_gradients_have_memory_of_their_own(norm, shape):
     want = x.grad.clone()
     r.grad.zero_()
     assert torch.equal(x.grad, want) and bool(want.any())
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.enable_grad])
+def test_tangents_are_refused(mode):
+    """The block has no forward-mode derivative."""
+    import gradients_taco_compress_amd.gated as gated
+    from torch.autograd import forward_ad
+    announce(f"gated, a tangent under {mode.__name__}")
+    x, wg, wu = (t.detach() for t in leaves((5, 72), (40, 72), (40, 72)))
+    want = gated.gated_forward(x, wg, wu)
+    with mode(), forward_ad.dual_level():
+        assert torch.equal(gated.gated(x, wg, wu), want)
+        for i in range(3):
+            args = [x, wg, wu]
+            args[i] = forward_ad.make_dual(args[i], torch.ones_like(args[i]))
+            with pytest.raises(NotImplementedError, match="jvp"):
+                gated.gated(*args)
