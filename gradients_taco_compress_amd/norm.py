@@ -75,18 +75,39 @@ for _name, (_args, _res) in _SIGNATURES.items():
     _fn.argtypes, _fn.restype = _args, _res
     globals()[_name] = _fn
 
-# Root-mean-square norm is a library of its own (include/taco_rms.h).
+# Root-mean-square norm is a library of its own (include/taco_rms.h): where it is not
+# built, layer norm works all the same.
 RMS_LIB_PATH = os.path.join(PKG, "libtaco_rms.so")
-if not os.path.exists(RMS_LIB_PATH):
-    raise ImportError(
-        f"libtaco_rms.so is not built ({RMS_LIB_PATH} missing); run "
-        "`python gradients_taco_compress_amd/build.py` (there is no CPU fallback)")
-_rms = ctypes.CDLL(RMS_LIB_PATH)
-try:
-    from . import _rms_torch as _fast_rms
-except ImportError as e:
-    raise ImportError(f"the torch module of libtaco_rms is not built ({e}); run "
-                      "`python gradients_taco_compress_amd/build.py`") from e
+
+
+class _NotBuilt:
+    """In the place of a library that is missing: any use of it says so."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        def call(*args):
+            raise ImportError(f"{self._why}; run `python gradients_taco_compress_amd/build.py` "
+                              "(there is no CPU fallback)")
+        return call
+
+
+def _load_rms():
+    """(the library, its torch module)."""
+    if not os.path.exists(RMS_LIB_PATH):
+        missing = _NotBuilt(f"libtaco_rms.so is not built ({RMS_LIB_PATH} missing)")
+        return missing, missing
+    lib = ctypes.CDLL(RMS_LIB_PATH)
+    try:
+        from . import _rms_torch
+    except ImportError as e:
+        missing = _NotBuilt(f"the torch module of libtaco_rms is not built ({e})")
+        return missing, missing
+    return lib, _rms_torch
+
+
+_rms, _fast_rms = _load_rms()
 _RMS_SIGNATURES = {
     "taco_rms_forward": ([_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I32, _F32, _P, _I64, _P,
                           _I64, _P, _P], _STATUS),
