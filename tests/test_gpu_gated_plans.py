@@ -42,6 +42,10 @@ def whole(rows, width, seed, most=1):
     return torch.randint(-most, most + 1, (rows, width), generator=gen(seed), device="cuda").float()
 
 
+def powers(n, low, high, seed):
+    return torch.exp2(torch.randint(low, high + 1, (n,), generator=gen(seed), device="cuda").float())
+
+
 def surrounded(t, dtype):
     """t in rows 8 elements further apart, NaN between them (contiguous where its
     rows are copied anyway)."""
@@ -85,6 +89,26 @@ def test_forward(gated, rows, hidden, features, dtype):
     check_activation(a, g, u, kind)
     again = gated.gated_forward(*(surrounded(t, dtype) for t in (x, wg, wu)), kind)
     assert torch.equal(a, again)
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("rows,hidden,features", plans.FORWARD_CODES)
+def test_forward_from_codes(gated, rows, hidden, features, dtype):
+    """Rows, features and blocks along the summed index each have a scale of their own
+    (the blocks' reciprocal, so that sums stay exact): a scale of another place shows."""
+    kind = ACTIVATIONS[(rows + (dtype is F16)) % 3]
+    announce(f"plans codes {rows} x {features}x{hidden} {dtype} {kind}")
+    x, wg, wu = (whole(n, hidden, i) for i, n in enumerate((rows, features, features)))
+    x[:, ::32] = 1.0                                                # no block of zeros
+    wg[:, ::32], wu[:, 1::32] = -1.0, 1.0
+    block = powers(hidden // 32, -6, 6, 4).repeat_interleave(32)
+    x = x * powers(rows, -8, -3, 5)[:, None] * block
+    wg, wu = (w * powers(features, -3, 1, 6 + i)[:, None] / block for i, w in enumerate((wg, wu)))
+    pairs = [gated.mx_encode(t) for t in (x, wg, wu)]
+    assert min(scales.unique().numel() for _, scales in pairs) >= 5      # (rows have scales of their own)
+    a = gated.gated_forward_mx(*pairs, kind, dtype=dtype)
+    g, u = (x.double() @ w.double().t().contiguous() for w in (wg, wu))
+    check_activation(a, g, u, kind)
 
 
 def backward_operands(rows, hidden, features, dtype):
