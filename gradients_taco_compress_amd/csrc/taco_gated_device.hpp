@@ -31,7 +31,8 @@ __device__ __forceinline__ void for_each(F &&f) {
     }
 }
 
-// 1 / (1 + e^-z), accurate to a few float32 steps on both sides.
+// 1 / (1 + e^-z), accurate to a few float32 steps on both sides (0 where it is below
+// 2^-126: z < -87.3).
 __device__ __forceinline__ float sigmoid(float z) {
     return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
 }

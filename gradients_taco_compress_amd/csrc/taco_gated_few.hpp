@@ -11,9 +11,10 @@
 //    they are waited for; where turns are held ahead, the next round's go out
 //    between the products of this one.
 //
-// Bound by HBM: 1 x 10240x2560 bf16 20.6 to 22.0 us (5.1 to 4.8 TB/s), 4 x 14336x3584
-// codes 23.2 us (4.6); else by what a CU takes in, X's rows among it: 34 GB/ms (codes
-// 25).  Few features fill few CUs (1 x 256x8192: 18.7 us).
+// Bound by HBM: 1 x 10240x2560 bf16 20.6 to 23.3 us (5.1 to 4.5 TB/s), 4 x 14336x3584
+// codes 23.2 to 25.1 us (4.6 to 4.2); else by what a CU takes in, X's rows among it:
+// 34 GB/s a CU (codes 25).  Few features fill few CUs (1 x 256x8192: bf16 18.7 us,
+// codes 14.1).
 #pragma once
 
 #include <type_traits>
@@ -174,6 +175,19 @@ __global__ __launch_bounds__(WAVES * kWave) void few_kernel(Product p) {
 //     bf16    64 x 1024x1024          8.6 and 11.6
 //     codes   17 / 64 x 4096x4096     12.2, 19.7 and 22.1, 21.9
 //     codes   64 x 2048x512           4.7 and 8.8
+// Up to 16 rows no estimate is made, so that such a call needs no workspace, whatever
+// its operands' alignment.  That is the faster side nearly everywhere, not where few
+// CUs have features or where 16-bit weights are large (1, 8 and 16 rows, this and tiles):
+//     bf16    256x8192                18.7, 21.3, 23.9 and 22.1, 22.1, 22.1
+//     bf16    768x2048                7.2, 7.8, 8.5 and 13.6, 13.5, 13.5
+//     bf16    2048x7168               18.3, 20.3, 22.7 and 22.7, 22.4, 22.8
+//     bf16    4096x4096               15.8, 15.5, 16.4 and 23.2, 23.5, 23.4
+//     bf16    10240x2560              23.3, 24.2, 26.9 and 27.1, 27.3, 27.6
+//     bf16    14336x3584              40.2, 40.3, 44.2 and 37.9, 37.6, 37.8
+//     codes   256x8192                14.1, 16.7, 18.5 and 18.6, 18.3, 18.4
+//     codes   4096x4096               9.9, 11.0, 11.7 and 22.7, 22.7, 22.5
+//     codes   14336x3584              24.2, 25.2, 28.9 and 29.8, 29.6, 29.8
+//     codes   14336x4096              30.1, 32.9, 36.3 and 34.8, 34.2, 34.3
 template <typename E>
 bool Products<E>::few_takes(const Product &p, int64_t copy_bytes) {
     constexpr int SIZE = Element<E>::SIZE;

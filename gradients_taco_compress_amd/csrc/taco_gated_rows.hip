@@ -1,7 +1,8 @@
 // The element-wise kernels of libtaco_gated: the gradients of both projections
 // from that of their product, copies of operands to aligned rows, and the
 // block-scaled 8-bit encoding of weights.  All of them stream HBM once: gradients of
-// 8192 x 10240 bf16 140 us (6.0 TB/s), the scales of 16384 x 14336x3584 6.5 us.
+// 8192 x 10240 bf16 140 us (6.0 TB/s), codes of 14336x3584 bf16 27.4 us (5.7) and float32
+// 44.1 us (5.9), the scales of 16384 x 14336x3584 6.5 us.
 #include "taco_gated_internal.hpp"
 #include "taco_gated_device.hpp"
 #include "taco_mx.hpp"

@@ -19,9 +19,12 @@
 //    of the four.
 //
 // All are bound by HBM, whose copies reach 5.14 TB/s here (reading and writing): forward with
-// residual 16384x3584 bf16 83 us (5.66 TB/s), into 8 bits 8192x2560 27.6 us (5.3), backward
-// 32768x12288 bf16 with dtotal 548 us (5.87); the smallest calls by the launch, 1x2560
-// forward 4.7 us.
+// residual 16384x3584 bf16 83 us (5.66 TB/s), float32 188 us (5.0) and 2048x2560 float32
+// 19.0 us (4.4), into 8 bits 8192x2560 27.6 us (5.3), backward 32768x12288 bf16 with dtotal
+// 548 us (5.87); the smallest calls by the launch, 1x2560 forward 2.0 to 2.5 us of kernel in
+// a call of 5.3 or more.  Backward, wide rows spill registers: APART beyond 6144 columns (192
+// to 568 bytes a thread); else most ragged rows beyond 8192 columns and whole ones with dtotal
+// beyond 12288 (float32: 6144 and 8192), 40 to 592 bytes.
 #pragma once
 
 #include "taco_norm_rows.hpp"

@@ -72,8 +72,9 @@ typedef enum {
     TACO_GATED_GELU_TANH = 2
 } taco_gated_activation;
 
-/* Largest hidden and features accepted.  (Their product, and that of either with
- * rows, may be up to 2^36; more is SHAPE where a launch could not hold its tiles.) */
+/* Largest hidden and features accepted.  A launch has to hold a call's tiles of 128 by
+ * 64 elements, so those of [rows, the larger of hidden and features], and twice those
+ * of [features, hidden], have to be fewer than 2^24, and rows fewer than 2^31 (SHAPE). */
 #define TACO_GATED_MAX_WIDTH 1048576
 
 /* Bytes of workspace of taco_gated_forward for these operands (-1 for a bad

@@ -128,7 +128,8 @@ def test_leading_dimensions(gated):
     assert torch.equal(gated.gated_forward(x[0], wg, wu), gated.gated_forward(x[:1], wg, wu)[0])
 
 
-# Large tiles, several items a work-group, split tiles; every edge ragged.
+# Large tiles in one piece (the first two sizes), small ones in one piece and in parts;
+# every edge ragged.
 @pytest.mark.parametrize("rows,hidden,features", [(2053, 72, 8203), (1000, 8, 33000), (33000, 40, 130),
                                                   (18, 16384, 24), (260, 9000, 200), (300, 24576, 520)])
 def test_exact_sums_forward(gated, rows, hidden, features):
@@ -422,7 +423,8 @@ def test_forward_mx(gated, rows, hidden, features, dtype):
     ref.check(a)
 
 
-# Large tiles, split tiles, several items; sums of powers of two are exact.
+# Without tiles, small tiles in one piece and in parts, large ones in one piece; sums of
+# powers of two are exact.
 @pytest.mark.parametrize("rows,hidden,features", [(17, 32, 16), (32, 160, 70), (33, 1120, 130), (64, 4096, 200),
                                                   (64, 96, 1), (17, 8192, 256), (64, 16384, 24), (64, 992, 9000),
                                                   (2053, 96, 8203), (18, 16384, 24), (300, 24576, 520),
