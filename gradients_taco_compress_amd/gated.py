@@ -272,7 +272,8 @@ def _tangents(*tensors):
 
 def gated(x, gate_weight, up_weight, activation: str = "silu"):
     """Differentiable ``act(x gate_weight^T) * (x up_weight^T)``.  It keeps x and
-    both projections for its backward pass, nothing without gradients.
+    both projections for its backward pass, nothing without gradients.  It has no
+    forward-mode derivative: a tangent is refused.
 
     The tensors are of one type, bf16 or fp16.  Under ``torch.autocast`` they need
     not be: they are cast to autocast's type, as torch's own linear layer does there,
